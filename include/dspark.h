@@ -53,6 +53,13 @@ typedef enum {
   DSPARK_LAUNCH_COOPERATIVE = 0,  /* cooperative launch: every workgroup is guaranteed resident (default) */
   DSPARK_LAUNCH_EXCLUSIVE = 1     /* plain launch; the caller guarantees no other kernel runs meanwhile */
 } dspark_launch;
+/* Activation of dspark_linear. */
+typedef enum {
+  DSPARK_ACT_NONE = 0,  /* z                                            */
+  DSPARK_ACT_RELU = 1,  /* max(z, 0)                                    */
+  DSPARK_ACT_GELU = 2,  /* z Phi(z), Phi the standard normal's integral */
+  DSPARK_ACT_SILU = 3   /* z / (1 + exp(-z))                            */
+} dspark_activation;
 /* Verify-length policy of dspark_serve. */
 typedef enum {
   DSPARK_POLICY_GLOBAL = 0,           /* dspark_schedule on the iteration's own survivals */
@@ -519,6 +526,151 @@ dspark_status dspark_serve(
  */
 dspark_status dspark_set_draft_launch(dspark_launch mode);
 dspark_launch dspark_get_draft_launch(void);
+
+/*
+ * dspark_linear — a linear layer with its bias, activation and residual in
+ * one pass: the output projection that gives the base logits U from the
+ * backbone's hidden states, and the backbone's own layers.
+ *
+ * Defined by: [P-blog] §4 parallel stage (gamma positions give gamma base
+ * logit vectors U_k from the backbone's hidden states); the formula:
+ *   z = x w^T + bias                    (fp32 accumulate)
+ *   y = act(z) + residual               (fp32, rounded once to the storage type)
+ *
+ * Arguments
+ *   M, N, K       rows, output features, input features (M == 0 or N == 0 is
+ *                 a no-op; K == 0 leaves z = bias)
+ *   dtype         storage of x, w, bias, residual, y
+ *   x  [M][K], w  [N][K]      16-byte aligned
+ *   bias      [N]    or NULL
+ *   act              activation
+ *   residual  [M][N] or NULL; may be y itself (added in place)
+ *   y         [M][N] out
+ *   pre  fp32 [M][N] out, or NULL: z, which dspark_linear_backward takes when
+ *                 there is an activation.  It is kept in fp32: rounded to bf16
+ *                 it would add half a bf16 step to every gradient.
+ *   workspace     >= dspark_linear_workspace_bytes(M, N, K, dtype) bytes
+ *                 (NULL if that is 0), 256-byte aligned, any contents.  Calls
+ *                 that can overlap need separate ones.
+ * Outputs overlap no input but y the residual.  Results do not depend on
+ * execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
+ */
+dspark_status dspark_linear(
+    int M, int N, int K, dspark_dtype dtype, const void* x, const void* w, const void* bias,
+    dspark_activation act, const void* residual, void* y, float* pre,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace dspark_linear needs; 0 for empty or unsupported shapes.
+ * Needs no GPU. */
+size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
+
+/*
+ * dspark_linear_backward — gradients of dspark_linear:
+ *   dz = dy act'(z)   (rounded to the storage type for the two products)
+ *   dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz
+ * each summed in fp32 and rounded once; the residual's gradient is dy itself.
+ * relu's slope at 0 is 0.
+ *
+ * Arguments: sizes, types and layouts as dspark_linear, and
+ *   dy   [M][N]      16-byte aligned
+ *   pre  fp32 [M][N] z as dspark_linear wrote it (NULL without activation)
+ *   dx [M][K], dw [N][K], dbias [N] out; each may be NULL: not computed.
+ *                 With M == 0, dw and dbias are zero; with N == 0, dx is.
+ *   workspace     >= dspark_linear_backward_workspace_bytes(M, N, K, dtype)
+ *                 bytes, 256-byte aligned, any contents.
+ */
+dspark_status dspark_linear_backward(
+    int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x, const void* w,
+    dspark_activation act, const float* pre, void* dx, void* dw, void* dbias,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
+
+/*
+ * dspark_markov_loss — softmax cross entropy over the logits that
+ * dspark_markov_draft draws from, without keeping the logits.
+ *
+ * Defined by: [P-blog] §4 (z_k = U_k plus the low-rank transition bias
+ * W1[x_{k-1}] W2) and §7 (the drafter is trained with a position-weighted
+ * cross entropy; weights enter through the gradient's g).  For every row n
+ * (a position of a request; any order), z_n over the vocabulary:
+ *   z_n(v) = U[n][v] + h[n] . Wo[v] + W1[prev[n]] . W2[:, v]   (fp32 accumulate)
+ *   lse[n] = ln sum_v exp z_n(v),   nll[n] = lse[n] - z_n(label[n])
+ * Each of the three parts may be left out (NULL, d = 0, r = 0), not all.
+ *
+ * A row whose label is outside [0, V) is ignored: nll = lse = 0, and its U,
+ * h and prev are not used, whatever they hold.
+ *
+ * Arguments
+ *   N, V, d, r    rows (0: no-op), vocabulary, hidden size, Markov rank
+ *   dtype         storage of U, h, Wo, W1, W2
+ *   label int32 [N]
+ *   U     [N][V] or NULL     base logits; -inf masks a token
+ *   h     [N][d], Wo [V][d]  hidden states and output projection (d > 0), 16-byte aligned
+ *   prev  int32 [N]          x_{k-1}, clamped to the vocabulary (r > 0)
+ *   W1    [V][r], W2 [r][V]  (r > 0), 16-byte aligned
+ *   nll, lse  fp32 [N] out
+ *   workspace     >= dspark_markov_loss_workspace_bytes(N, V, d, r, dtype)
+ *                 bytes, 256-byte aligned, any contents.  Calls that can
+ *                 overlap need separate ones.
+ * Limits: N <= 2^20, V <= 2^24, d, r <= 65536.  Nothing depends on execution
+ * order: the same inputs give the same bits.
+ */
+dspark_status dspark_markov_loss(
+    int N, int V, int d, int r, dspark_dtype dtype, const int32_t* label, const void* U,
+    const void* h, const void* Wo, const int32_t* prev, const void* W1, const void* W2,
+    float* nll, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dtype dtype);
+
+/*
+ * dspark_markov_loss_backward — gradients of sum_n g[n] nll[n]:
+ *   dz_n(v) = g[n] (exp(z_n(v) - lse[n]) - [v = label[n]])
+ *   dU = dz,  dh = dz Wo,  dWo = dz^T h,  dW2 = sum_n W1[prev[n]] (x) dz_n,
+ *   dW1[t] = sum over the rows n with prev[n] = t of W2 dz_n
+ * The logits are computed again, piece by piece of the vocabulary; dz is
+ * rounded to the storage type for the products, sums are fp32, each gradient
+ * is rounded once.  Ignored rows have no part in any sum; their rows of dU
+ * and dh are zero.
+ *
+ * Arguments: inputs as dspark_markov_loss, and
+ *   g    fp32 [N]  gradient of the loss by nll (position weights, 1 / count)
+ *   lse  fp32 [N]  as dspark_markov_loss wrote it
+ *   dU [N][V], dh [N][d], dWo [V][d], dW1 [V][r], dW2 [r][V] out, in the
+ *                 storage type; each may be NULL: not computed
+ *   workspace     >= dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype)
+ *                 bytes, 256-byte aligned, any contents
+ * N == 0 leaves dWo, dW1 and dW2 zero.
+ */
+dspark_status dspark_markov_loss_backward(
+    int N, int V, int d, int r, dspark_dtype dtype, const float* g, const float* lse,
+    const int32_t* label, const void* U, const void* h, const void* Wo, const int32_t* prev,
+    const void* W1, const void* W2, void* dU, void* dh, void* dWo, void* dW1, void* dW2,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_markov_loss_backward_workspace_bytes(int N, int V, int d, int r, dspark_dtype dtype);
+
+/*
+ * dspark_hidden_draft — drafting from the hidden states alone: the base
+ * logits U = h Wo^T + bias (dspark_linear), then dspark_markov_draft on them.
+ *
+ * Defined by: the two operations it chains.
+ * Arguments: those of dspark_markov_draft, with Wo [V][d] (16-byte aligned,
+ * as h here is) and bias [V] or NULL, and
+ *   U  [B][gamma][V] out   the base logits, in the storage type
+ *   workspace  >= dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dtype)
+ *              bytes, 256-byte aligned: the drafting workspace, with its
+ *              zero-fill rule, then the projection's.
+ * Limits: those of both, and B * gamma <= 2^20.
+ */
+dspark_status dspark_hidden_draft(
+    int B, int gamma, int V, int r, int d, dspark_dtype dtype,
+    const int32_t* anchor, const void* h, const void* Wo, const void* bias, const void* W1,
+    const void* W2, const float* conf_w, float conf_b, const float* sts_T, dspark_sampling mode,
+    uint64_t seed, void* U, int32_t* tokens, float* logit, float* conf, float* surv,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_hidden_draft_workspace_bytes(int B, int gamma, int V, int r, int d, dspark_dtype dtype);
 
 /* Static description of a status code. */
 const char* dspark_status_string(dspark_status s);

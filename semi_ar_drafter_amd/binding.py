@@ -84,6 +84,21 @@ def _declare(lib):
     lib.dspark_sts_fit.restype = c_int
     lib.dspark_verify.argtypes = [c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
     lib.dspark_verify.restype = c_int
+    lib.dspark_linear.argtypes = [c_int] * 4 + [c_vp] * 3 + [c_int] + [c_vp] * 4 + [c_size, c_vp]
+    lib.dspark_linear.restype = c_int
+    lib.dspark_linear_backward.argtypes = [c_int] * 4 + [c_vp] * 3 + [c_int] + [c_vp] * 5 + [c_size, c_vp]
+    lib.dspark_linear_backward.restype = c_int
+    lib.dspark_markov_loss.argtypes = [c_int] * 5 + [c_vp] * 10 + [c_size, c_vp]
+    lib.dspark_markov_loss.restype = c_int
+    lib.dspark_markov_loss_backward.argtypes = [c_int] * 5 + [c_vp] * 15 + [c_size, c_vp]
+    lib.dspark_markov_loss_backward.restype = c_int
+    lib.dspark_hidden_draft.argtypes = ([c_int] * 6 + [c_vp] * 7 + [c_f, c_vp, c_int, c_u64] + [c_vp] * 6 +
+                                        [c_size, c_vp])
+    lib.dspark_hidden_draft.restype = c_int
+    for name, n in (("linear", 4), ("linear_backward", 4), ("markov_loss", 5), ("markov_loss_backward", 5),
+                    ("hidden_draft", 6)):
+        f = getattr(lib, f"dspark_{name}_workspace_bytes")
+        f.argtypes, f.restype = [c_int] * n, c_size
     lib.dspark_status_string.argtypes = [c_int]
     lib.dspark_status_string.restype = ctypes.c_char_p
     lib.dspark_last_error.argtypes = []
@@ -548,3 +563,238 @@ def verify(tokens, target, lens, out=None):
                            _ptr(acc), _ptr(bonus), _stream())
     _check(st)
     return acc, bonus
+
+
+# ----------------------------------------------------------------------------
+# the vocabulary projection: linear layer, loss and their gradients
+# ----------------------------------------------------------------------------
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _storage(t, name):
+    torch = _torch()
+    _need(t, name)
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return DSPARK_BF16 if t.dtype == torch.bfloat16 else DSPARK_F32
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _optional(t, name, dtype, shape, device):
+    if t is not None:
+        _need(t, name, dtype, shape, device)
+
+
+def _scratch(nbytes, device, kind, workspace):
+    """(pointer, bytes) of the workspace of a call on `device`'s current stream."""
+    if workspace is not None:
+        _need(workspace, "workspace", _torch().uint8, None, device)
+        return _ptr(workspace), ctypes.c_size_t(workspace.numel())
+    if nbytes == 0:
+        return _ptr(None), ctypes.c_size_t(0)
+    ws = _captured(nbytes, device) or _workspace(nbytes, device, kind)
+    return _ptr(ws), ctypes.c_size_t(ws.numel())
+
+
+class _Buffer:
+    """A workspace that is true (a tensor of several values has no truth)."""
+
+    def __init__(self, t):
+        self.t = t
+        self.data_ptr, self.numel = t.data_ptr, t.numel
+
+
+def _captured(nbytes, device, zero=False):
+    """Under graph capture: a workspace of the call's own, from the graph's
+    memory pool.  A cached one would be shared by graphs that can be replayed
+    at the same time, and would not live as long as they do."""
+    torch = _torch()
+    if not torch.cuda.is_current_stream_capturing():
+        return None
+    return _Buffer((torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=device))
+
+
+def _on(device):
+    """The device the operands live on becomes the current one, so that its
+    current stream takes the launches."""
+    return _torch().cuda.device(device)
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None, workspace=None):
+    """y = act(x @ w.T + bias) + residual in one kernel; returns y [M, N].
+
+    x [M, K], w [N, K], bias [N] and residual [M, N] are all float32 or all
+    bfloat16 device tensors; act is "none", "relu", "gelu" (with the error
+    function) or "silu".  `pre`, a float32 [M, N] tensor, receives
+    x @ w.T + bias for linear_backward.  `out` takes y; it may be `residual`."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    _need(w, "w", x.dtype, (N, K), dev)
+    _optional(bias, "bias", x.dtype, (N,), dev)
+    _optional(residual, "residual", x.dtype, (M, N), dev)
+    _optional(pre, "pre", torch.float32, (M, N), dev)
+    _optional(out, "out", x.dtype, (M, N), dev)
+    a = _act(act)
+    with _on(dev):
+        y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+        ws, n = _scratch(int(lib.dspark_linear_workspace_bytes(M, N, K, dt)), dev, "linear", workspace)
+        _check(lib.dspark_linear(M, N, K, dt, _ptr(x), _ptr(w), _ptr(bias), a, _ptr(residual), _ptr(y), _ptr(pre),
+                                 ws, n, _stream()))
+    return y
+
+
+def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "dbias"), workspace=None):
+    """Gradients of linear(); returns (dx [M, K], dw [N, K], dbias [N]) in the
+    storage type, None for those not named in `need`.  `pre` is what linear()
+    wrote (only with an activation).  The residual's gradient is dy itself."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    _need(w, "w", x.dtype, (N, K), dev)
+    _need(dy, "dy", x.dtype, (M, N), dev)
+    a = _act(act)
+    if a and pre is None:
+        raise ValueError("an activation's gradient needs pre")
+    _optional(pre, "pre", torch.float32, (M, N), dev)
+    if set(need) - {"dx", "dw", "dbias"}:
+        raise ValueError("need names dx, dw and dbias")
+    with _on(dev):
+        new = lambda name, *sh: torch.empty(sh, dtype=x.dtype, device=dev) if name in need else None  # noqa: E731
+        dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
+        ws, n = _scratch(int(lib.dspark_linear_backward_workspace_bytes(M, N, K, dt)), dev, "linear_backward",
+                         workspace)
+        _check(lib.dspark_linear_backward(M, N, K, dt, _ptr(dy), _ptr(x), _ptr(w), a, _ptr(pre), _ptr(dx), _ptr(dw),
+                                          _ptr(db), ws, n, _stream()))
+    return dx, dw, db
+
+
+def _loss_inputs(label, U, h, Wo, prev, W1, W2):
+    """Checks the loss's inputs; returns (N, V, d, r, dtype, device, storage)."""
+    torch = _torch()
+    if (h is None) != (Wo is None) or (W1 is None) != (W2 is None) or (prev is None) != (W1 is None):
+        raise ValueError("h goes with Wo, and prev with W1 and W2")
+    first = next((t for t in (U, Wo, W2) if t is not None), None)
+    if first is None:
+        raise ValueError("no logits: give U, h and Wo, or prev, W1 and W2")
+    _need(label, "label", torch.int32)
+    (N,) = label.shape
+    dt = _storage(first, "logits' inputs")
+    V = U.shape[1] if U is not None else Wo.shape[0] if Wo is not None else W2.shape[1]
+    d = Wo.shape[1] if Wo is not None else 0
+    r = W2.shape[0] if W2 is not None else 0
+    dev = first.device
+    _need(label, "label", torch.int32, (N,), dev)
+    _optional(U, "U", first.dtype, (N, V), dev)
+    _optional(h, "h", first.dtype, (N, d), dev)
+    _optional(Wo, "Wo", first.dtype, (V, d), dev)
+    _optional(prev, "prev", torch.int32, (N,), dev)
+    _optional(W1, "W1", first.dtype, (V, r), dev)
+    _optional(W2, "W2", first.dtype, (r, V), dev)
+    return N, V, d, r, dt, dev, first.dtype
+
+
+def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out=None, workspace=None):
+    """Cross entropy over z = U + h @ Wo.T + W1[prev] @ W2 without keeping the
+    logits; returns (nll, lse), float32 [N].
+
+    label int32 [N] (outside [0, V): the row is ignored, its nll and lse are
+    0), U [N, V], h [N, d], Wo [V, d], prev int32 [N], W1 [V, r], W2 [r, V];
+    each of the three parts may be left out, not all."""
+    torch = _torch()
+    lib = load()
+    N, V, d, r, dt, dev, _ = _loss_inputs(label, U, h, Wo, prev, W1, W2)
+    with _on(dev):
+        if out is None:
+            out = (torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev))
+        nll, lse = out
+        _need(nll, "nll", torch.float32, (N,), dev)
+        _need(lse, "lse", torch.float32, (N,), dev)
+        ws, n = _scratch(int(lib.dspark_markov_loss_workspace_bytes(N, V, d, r, dt)), dev, "markov_loss", workspace)
+        _check(lib.dspark_markov_loss(N, V, d, r, dt, _ptr(label), _ptr(U), _ptr(h), _ptr(Wo), _ptr(prev), _ptr(W1),
+                                      _ptr(W2), _ptr(nll), _ptr(lse), ws, n, _stream()))
+    return nll, lse
+
+
+def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, need=None,
+                         workspace=None):
+    """Gradients of sum(g * nll) of markov_loss(); returns a dict of the
+    gradients named in `need` (of "dU", "dh", "dWo", "dW1", "dW2"; by default
+    all whose inputs are given), in the storage type.  g float32 [N] holds the
+    position weights; lse is what markov_loss() returned."""
+    torch = _torch()
+    lib = load()
+    N, V, d, r, dt, dev, dtype = _loss_inputs(label, U, h, Wo, prev, W1, W2)
+    _need(g, "g", torch.float32, (N,), dev)
+    _need(lse, "lse", torch.float32, (N,), dev)
+    shapes = {}
+    if U is not None:
+        shapes["dU"] = (N, V)
+    if Wo is not None:
+        shapes.update(dh=(N, d), dWo=(V, d))
+    if W2 is not None:
+        shapes.update(dW1=(V, r), dW2=(r, V))
+    need = list(shapes) if need is None else list(need)
+    for k in need:
+        if k not in shapes:
+            raise ValueError(f"no input for the gradient {k}")
+    with _on(dev):
+        grads = {k: torch.empty(shapes[k], dtype=dtype, device=dev) for k in need}
+        ws, n = _scratch(int(lib.dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dt)), dev,
+                         "markov_loss_backward", workspace)
+        _check(lib.dspark_markov_loss_backward(
+            N, V, d, r, dt, _ptr(g), _ptr(lse), _ptr(label), _ptr(U), _ptr(h), _ptr(Wo), _ptr(prev), _ptr(W1),
+            _ptr(W2), *[_ptr(grads.get(k)) for k in ("dU", "dh", "dWo", "dW1", "dW2")], ws, n, _stream()))
+    return grads
+
+
+def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None, mode: str = "greedy", seed: int = 0,
+                 U=None, out=None, workspace=None):
+    """markov_draft() from the hidden states alone: the base logits
+    U = h @ Wo.T + bias are made first, in one call.  h [B, gamma, d],
+    Wo [V, d], bias [V]; `U` [B, gamma, V] receives the base logits.  Other
+    arguments and the result as markov_draft."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(h, "h")
+    B, gamma, d = h.shape
+    V, r = W1.shape
+    dev = h.device
+    _need(anchor, "anchor", torch.int32, (B,), dev)
+    _need(Wo, "Wo", h.dtype, (V, d), dev)
+    _optional(bias, "bias", h.dtype, (V,), dev)
+    _need(W1, "W1", h.dtype, (V, r), dev)
+    _need(W2, "W2", h.dtype, (r, V), dev)
+    _need(conf_w, "conf_w", torch.float32, (d + r,), dev)
+    _need(sts_T, "sts_T", torch.float32, (gamma,), dev)
+    _optional(U, "U", h.dtype, (B, gamma, V), dev)
+    with _on(dev):
+        if U is None:
+            U = torch.empty((B, gamma, V), dtype=h.dtype, device=dev)
+        if out is None:
+            out = (torch.empty((B, gamma), dtype=torch.int32, device=dev),
+                   torch.empty((B, gamma), dtype=torch.float32, device=dev),
+                   torch.empty((B, gamma), dtype=torch.float32, device=dev),
+                   torch.empty((B, gamma), dtype=torch.float32, device=dev))
+        tokens, logit, conf, surv = out
+        nbytes = int(lib.dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dt))
+        ws = workspace
+        if ws is None:
+            ws = _captured(nbytes, dev, zero=True) or _workspace(nbytes, dev, "hidden_draft", (B, gamma))
+        _check(lib.dspark_hidden_draft(
+            B, gamma, V, r, d, dt, _ptr(anchor), _ptr(h), _ptr(Wo), _ptr(bias), _ptr(W1), _ptr(W2), _ptr(conf_w),
+            ctypes.c_float(conf_b), _ptr(sts_T), DSPARK_GUMBEL if mode == "gumbel" else DSPARK_GREEDY,
+            ctypes.c_uint64(seed & (2 ** 64 - 1)), _ptr(U), _ptr(tokens), _ptr(logit), _ptr(conf), _ptr(surv),
+            _ptr(ws), ctypes.c_size_t(ws.numel()), _stream()))
+    return tokens, logit, conf, surv

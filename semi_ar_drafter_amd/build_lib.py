@@ -27,6 +27,8 @@ SOURCES = [
     ("schedule_verify.hip", True),
     ("parallel_draft.hip", True),
     ("sts_fit.hip", True),
+    ("linear.hip", True),
+    ("markov_loss.hip", True),
 ]
 # Per-source flags.  The draft kernel's inputs are finite by contract, so its
 # maxima need not quiet signalling NaNs (no canonicalising instruction before

@@ -86,7 +86,7 @@ dspark_status draft_impl(int B, int gamma, int V, int r, int d, dspark_dtype dty
                          bool rnn, const float* conf_w, float conf_b, const float* sts_T, dspark_sampling mode,
                          uint64_t seed, int32_t* tokens, float* logit, float* conf, float* surv, void* workspace,
                          size_t workspace_bytes, hipStream_t stream, bool noalloc = false,
-                         const dspark::StepArgs* step = nullptr, bool* fused = nullptr) {
+                         const dspark::StepArgs* step = nullptr, bool* fused = nullptr, bool check_only = false) {
   g_last_error[0] = '\0';
   if (B < 0 || gamma < 0 || V < 0 || r < 0 || d < 0)
     return fail(DSPARK_ERR_INVALID_ARG, "negative size");
@@ -145,6 +145,7 @@ dspark_status draft_impl(int B, int gamma, int V, int r, int d, dspark_dtype dty
   a.decay = rnn ? decay : nullptr;
   a.noalloc = noalloc;
   a.step = step;
+  a.check_only = check_only;
   const char* why = nullptr;
   hipError_t e = dspark::launch_markov_draft(a, stream, &why, fused);
   if (why) return fail(DSPARK_ERR_UNSUPPORTED, "%s", why);
@@ -412,6 +413,253 @@ dspark_status dspark_step(int B, int gamma, int V, int r, int d, dspark_dtype dt
   if (e == hipSuccess) e = dspark::launch_verify(B, gamma, tokens, target, lens, accepted, bonus, stream);
   if (e != hipSuccess) return hip_fail(e);
   return DSPARK_OK;
+}
+
+namespace {
+
+bool known_dtype(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
+bool misaligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// Checks shared by the linear layer's two directions; nullptr or the complaint.
+dspark_status linear_sizes(int M, int N, int K, dspark_dtype dtype, dspark_activation act) {
+  if (M < 0 || N < 0 || K < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
+  if (!known_dtype(dtype)) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype");
+  if (act != DSPARK_ACT_NONE && act != DSPARK_ACT_RELU && act != DSPARK_ACT_GELU && act != DSPARK_ACT_SILU)
+    return fail(DSPARK_ERR_INVALID_ARG, "unknown activation");
+  if (M > dspark::kMaxRows) return fail(DSPARK_ERR_UNSUPPORTED, "M > 2^20");
+  if (N > kMaxV) return fail(DSPARK_ERR_UNSUPPORTED, "N > 2^24");
+  if (K > kMaxD) return fail(DSPARK_ERR_UNSUPPORTED, "K > 65536");
+  return DSPARK_OK;
+}
+
+dspark_status check_workspace(const void* ws, size_t have, size_t need, const char* name) {
+  if (need == 0) return DSPARK_OK;
+  if (!ws || have < need) return fail(DSPARK_ERR_WORKSPACE, "workspace missing or smaller than %s()", name);
+  if (misaligned(ws, 256)) return fail(DSPARK_ERR_WORKSPACE, "workspace not 256-byte aligned");
+  return DSPARK_OK;
+}
+
+}  // namespace
+
+size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+  if (M <= 0 || N <= 0 || K < 0 || M > dspark::kMaxRows || N > kMaxV || K > kMaxD || !known_dtype(dtype)) return 0;
+  return dspark::linear_workspace_bytes(M, N, K, dtype == DSPARK_BF16);
+}
+
+dspark_status dspark_linear(int M, int N, int K, dspark_dtype dtype, const void* x, const void* w, const void* bias,
+                            dspark_activation act, const void* residual, void* y, float* pre, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = linear_sizes(M, N, K, dtype, act);
+  if (st != DSPARK_OK) return st;
+  if (M == 0 || N == 0) return DSPARK_OK;
+  if (!y || (K > 0 && (!x || !w))) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(x, 16) || misaligned(w, 16)) return fail(DSPARK_ERR_INVALID_ARG, "x and w need 16-byte alignment");
+  if (misaligned(bias, elem) || misaligned(residual, elem) || misaligned(y, elem) || misaligned(pre, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  st = check_workspace(workspace, workspace_bytes, dspark_linear_workspace_bytes(M, N, K, dtype),
+                       "dspark_linear_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  dspark::LinearArgs a;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.act = int(act);
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.y = y;
+  a.pre = pre;
+  a.ws = workspace;
+  hipError_t e = dspark::launch_linear(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+  if (M < 0 || N <= 0 || K < 0 || M > dspark::kMaxRows || N > kMaxV || K > kMaxD || !known_dtype(dtype)) return 0;
+  return dspark::linear_backward_workspace_bytes(M, N, K, dtype == DSPARK_BF16);
+}
+
+dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x,
+                                     const void* w, dspark_activation act, const float* pre, void* dx, void* dw,
+                                     void* dbias, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = linear_sizes(M, N, K, dtype, act);
+  if (st != DSPARK_OK) return st;
+  const bool some = M > 0 && N > 0;
+  if ((some && !dy) || (some && act != DSPARK_ACT_NONE && !pre) || (some && dx && K > 0 && !w) ||
+      (some && dw && K > 0 && !x))
+    return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(dy, 16))
+    return fail(DSPARK_ERR_INVALID_ARG, "x, w and dy need 16-byte alignment");
+  if (misaligned(dx, elem) || misaligned(dw, elem) || misaligned(dbias, elem) || misaligned(pre, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  st = check_workspace(workspace, workspace_bytes, dspark_linear_backward_workspace_bytes(M, N, K, dtype),
+                       "dspark_linear_backward_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  dspark::LinearBackwardArgs a;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.act = int(act);
+  a.dy = dy;
+  a.x = x;
+  a.w = w;
+  a.pre = pre;
+  a.dx = dx;
+  a.dw = dw;
+  a.dbias = dbias;
+  a.ws = workspace;
+  hipError_t e = dspark::launch_linear_backward(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+namespace {
+
+bool loss_sizes_fit(int N, int V, int d, int r) {
+  return N >= 0 && V >= 1 && d >= 0 && r >= 0 && N <= dspark::kMaxRows && V <= kMaxV && d <= kMaxD && r <= kMaxD;
+}
+
+// Checks shared by the loss and its gradient.
+dspark_status loss_inputs(const dspark::LossArgs& a, dspark_dtype dtype) {
+  if (a.N < 0 || a.V < 0 || a.d < 0 || a.r < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
+  if (!known_dtype(dtype)) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype");
+  if (a.V < 1) return fail(DSPARK_ERR_INVALID_ARG, "V must be positive");
+  if ((a.d > 0) != (a.Wo != nullptr) || (a.d == 0 && a.h) || (a.r > 0) != (a.W2 != nullptr) ||
+      (a.r == 0 && (a.W1 || a.prev)))
+    return fail(DSPARK_ERR_INVALID_ARG, "h and Wo go with d > 0, prev, W1 and W2 with r > 0");
+  if (a.N > 0 && (!a.label || (a.d > 0 && !a.h) || (a.r > 0 && (!a.W1 || !a.prev))))
+    return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if (a.N > 0 && !a.U && a.d == 0 && a.r == 0)
+    return fail(DSPARK_ERR_INVALID_ARG, "no logits: give U, h and Wo, or prev, W1 and W2");
+  if (a.N > dspark::kMaxRows) return fail(DSPARK_ERR_UNSUPPORTED, "N > 2^20");
+  if (a.V > kMaxV) return fail(DSPARK_ERR_UNSUPPORTED, "V > 2^24");
+  if (a.d > kMaxD || a.r > kMaxD) return fail(DSPARK_ERR_UNSUPPORTED, "d or r > 65536");
+  if (misaligned(a.h, 16) || misaligned(a.Wo, 16) || misaligned(a.W1, 16) || misaligned(a.W2, 16))
+    return fail(DSPARK_ERR_INVALID_ARG, "h, Wo, W1 and W2 need 16-byte alignment");
+  if (misaligned(a.U, a.bf16 ? 2 : 4) || misaligned(a.label, 4) || misaligned(a.prev, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  return DSPARK_OK;
+}
+
+dspark::LossArgs loss_args(int N, int V, int d, int r, dspark_dtype dtype, const int32_t* label, const void* U,
+                           const void* h, const void* Wo, const int32_t* prev, const void* W1, const void* W2,
+                           void* ws) {
+  dspark::LossArgs a = {};
+  a.N = N;
+  a.V = V;
+  a.d = d;
+  a.r = r;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.label = label;
+  a.prev = prev;
+  a.U = U;
+  a.h = h;
+  a.Wo = Wo;
+  a.W1 = W1;
+  a.W2 = W2;
+  a.ws = ws;
+  return a;
+}
+
+}  // namespace
+
+size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dtype dtype) {
+  if (!loss_sizes_fit(N, V, d, r) || !known_dtype(dtype) || N == 0) return 0;
+  return dspark::loss_workspace_bytes(N, V, d, r, dtype == DSPARK_BF16, false);
+}
+
+dspark_status dspark_markov_loss(int N, int V, int d, int r, dspark_dtype dtype, const int32_t* label, const void* U,
+                                 const void* h, const void* Wo, const int32_t* prev, const void* W1, const void* W2,
+                                 float* nll, float* lse, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark::LossArgs a = loss_args(N, V, d, r, dtype, label, U, h, Wo, prev, W1, W2, workspace);
+  dspark_status st = loss_inputs(a, dtype);
+  if (st != DSPARK_OK) return st;
+  if (N == 0) return DSPARK_OK;
+  if (!nll || !lse) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if (misaligned(nll, 4) || misaligned(lse, 4)) return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_workspace_bytes(N, V, d, r, dtype),
+                       "dspark_markov_loss_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  a.nll = nll;
+  a.lse = lse;
+  hipError_t e = dspark::launch_markov_loss(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_markov_loss_backward_workspace_bytes(int N, int V, int d, int r, dspark_dtype dtype) {
+  if (!loss_sizes_fit(N, V, d, r) || !known_dtype(dtype)) return 0;
+  return dspark::loss_workspace_bytes(N, V, d, r, dtype == DSPARK_BF16, true);
+}
+
+dspark_status dspark_markov_loss_backward(int N, int V, int d, int r, dspark_dtype dtype, const float* g,
+                                          const float* lse, const int32_t* label, const void* U, const void* h,
+                                          const void* Wo, const int32_t* prev, const void* W1, const void* W2,
+                                          void* dU, void* dh, void* dWo, void* dW1, void* dW2, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark::LossArgs a = loss_args(N, V, d, r, dtype, label, U, h, Wo, prev, W1, W2, workspace);
+  dspark_status st = loss_inputs(a, dtype);
+  if (st != DSPARK_OK) return st;
+  if (N > 0 && (!g || !lse)) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if ((dU && N > 0 && !U) || (d == 0 && (dh || dWo)) || (r == 0 && (dW1 || dW2)))
+    return fail(DSPARK_ERR_INVALID_ARG, "gradient of an input that is not there");
+  const size_t elem = a.bf16 ? 2 : 4;
+  if (misaligned(g, 4) || misaligned(lse, 4) || misaligned(dU, elem) || misaligned(dh, elem) ||
+      misaligned(dWo, elem) || misaligned(dW1, elem) || misaligned(dW2, elem))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype),
+                       "dspark_markov_loss_backward_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  a.lse_in = lse;
+  a.g = g;
+  a.dU = dU;
+  a.dh = dh;
+  a.dWo = dWo;
+  a.dW1 = dW1;
+  a.dW2 = dW2;
+  hipError_t e = dspark::launch_markov_loss_backward(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_hidden_draft_workspace_bytes(int B, int gamma, int V, int r, int d, dspark_dtype dtype) {
+  const size_t draft = dspark_draft_workspace_bytes(B, gamma, V, r);
+  if (draft == 0 || (long long)B * gamma > dspark::kMaxRows) return draft;
+  return draft + dspark_linear_workspace_bytes(B * gamma, V, d, dtype);
+}
+
+dspark_status dspark_hidden_draft(int B, int gamma, int V, int r, int d, dspark_dtype dtype, const int32_t* anchor,
+                                  const void* h, const void* Wo, const void* bias, const void* W1, const void* W2,
+                                  const float* conf_w, float conf_b, const float* sts_T, dspark_sampling mode,
+                                  uint64_t seed, void* U, int32_t* tokens, float* logit, float* conf, float* surv,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  if (B < 0 || gamma < 0 || V < 0 || r < 0 || d < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
+  if ((long long)B * gamma > dspark::kMaxRows) return fail(DSPARK_ERR_UNSUPPORTED, "B * gamma > 2^20");
+  // every check of the draft before the product is enqueued
+  dspark_status st = draft_impl(B, gamma, V, r, d, dtype, anchor, U, h, W1, W2, nullptr, false, conf_w, conf_b, sts_T,
+                                mode, seed, tokens, logit, conf, surv, workspace, workspace_bytes, stream, false,
+                                nullptr, nullptr, /*check_only=*/true);
+  if (st != DSPARK_OK || B == 0 || gamma == 0) return st;
+  const size_t draft = dspark_draft_workspace_bytes(B, gamma, V, r);
+  if (workspace_bytes < dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dtype))
+    return fail(DSPARK_ERR_WORKSPACE, "workspace smaller than dspark_hidden_draft_workspace_bytes()");
+  st = dspark_linear(B * gamma, V, d, dtype, h, Wo, bias, DSPARK_ACT_NONE, nullptr, U, nullptr,
+                     static_cast<unsigned char*>(workspace) + draft, workspace_bytes - draft, stream);
+  if (st != DSPARK_OK) return st;
+  return draft_impl(B, gamma, V, r, d, dtype, anchor, U, h, W1, W2, nullptr, false, conf_w, conf_b, sts_T, mode, seed,
+                    tokens, logit, conf, surv, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@ struct DraftArgs {
   bool exclusive;   // plain launch: the caller guarantees nothing else runs on the device
   const float* decay = nullptr;   // non-null: RNN head with this per-channel state decay [r] (bf16 only)
   bool noalloc = false;           // ws ignored: the per-device static scratch is used (Markov head)
+  bool check_only = false;        // nothing is launched: the shape's checks alone
   const StepArgs* step = nullptr;  // non-null: schedule and verify in the same launch when the shape allows
 };
 
@@ -120,5 +121,46 @@ hipError_t launch_sts_fit(const StsArgs& a, hipStream_t stream);
 
 hipError_t launch_verify(int B, int gamma, const int32_t* tokens, const int32_t* target,
                          const int32_t* lens, int32_t* accepted, int32_t* bonus, hipStream_t stream);
+
+// Linear layer (x [M][K], w [N][K]) and its gradients.
+struct LinearArgs {
+  int M, N, K;
+  bool bf16;
+  int act;
+  const void *x, *w, *bias, *residual;
+  void* y;
+  float* pre;
+  void* ws;
+};
+struct LinearBackwardArgs {
+  int M, N, K;
+  bool bf16;
+  int act;
+  const void *dy, *x, *w;
+  const float* pre;
+  void *dx, *dw, *dbias;
+  void* ws;
+};
+constexpr int kMaxRows = 1 << 20;   // rows of the linear layer and of the loss
+size_t linear_workspace_bytes(int M, int N, int K, bool bf16);
+size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t stream);
+hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t stream);
+
+// Cross entropy over the heads' logits; the gradient's members are unused by
+// the forward call and the other way round.
+struct LossArgs {
+  int N, V, d, r;
+  bool bf16;
+  const int32_t *label, *prev;
+  const void *U, *h, *Wo, *W1, *W2;
+  float *nll, *lse;
+  const float *lse_in, *g;
+  void *dU, *dh, *dWo, *dW1, *dW2;
+  void* ws;
+};
+size_t loss_workspace_bytes(int N, int V, int d, int r, bool bf16, bool backward);
+hipError_t launch_markov_loss(const LossArgs& a, hipStream_t stream);
+hipError_t launch_markov_loss_backward(const LossArgs& a, hipStream_t stream);
 
 }  // namespace dspark

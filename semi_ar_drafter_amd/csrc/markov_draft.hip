@@ -1642,6 +1642,7 @@ hipError_t launch_markov_draft(const DraftArgs& a, hipStream_t stream, const cha
     *unsupported = "too many requests per workgroup for the confidence epilogue";
     return hipSuccess;
   }
+  if (a.check_only) return hipSuccess;
   const DraftWorkspace L = draft_workspace_layout(a.B, a.gamma, rnn ? a.r : 0);
   char* ws = static_cast<char*>(a.ws);
   if (a.noalloc) {   // every check has passed: set up (first call) and take this device's scratch

@@ -1,0 +1,349 @@
+// Softmax cross entropy over the drafting heads' logits, without keeping the
+// logits, and its gradient.
+//
+//   z_n(v) = U[n][v] + h_n . Wo[v] + W1[prev_n] . W2[:, v]
+//   lse_n  = ln sum_v exp z_n(v),  nll_n = lse_n - z_n(label_n)
+//   dz_n(v) = g_n (exp(z_n(v) - lse_n) - [v = label_n])
+//
+// Rows without a label are left out at the start: the rows that have one are
+// gathered into X = [h | W1[prev]] (both parts zero-padded to a multiple of
+// 64), so that ignored rows cost no product and whatever they hold touches
+// nothing.  Their number stays on the device.
+//
+// Forward: the product of X with [Wo | W2^T] tile by tile; each tile leaves
+// (max, sum of exponentials) per row, which one small kernel joins.
+// Backward, piece by piece of the vocabulary (the piece's dz is the only
+// array of its width that is kept): logits again, dz, then
+//   dX += dz [Wo | W2^T]     (fp32, over the pieces in order)
+//   dWo = dz^T h,  dW2 = e^T dz    (final: rows are not split)
+// and at the end dX is rounded into dh and summed into dW1, rows with the
+// same previous token in row order.  Nothing is added by atomics: results do
+// not depend on any order of execution.
+#include "launch.h"
+#include "projection.h"
+#include "tile_f32.h"
+
+namespace dspark {
+
+namespace {
+
+inline size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
+
+// Largest width of a piece's dz array, in bytes.
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr int kPieceAlign = 256;
+
+// Lists the rows that have a label, in order: row[i] = n, place[n] = i or -1.
+// One workgroup; each thread takes a run of rows.
+__global__ __launch_bounds__(1024) void compact_kernel(int N, int V, const int* __restrict__ label,
+                                                       int* __restrict__ count, int* __restrict__ row,
+                                                       int* __restrict__ place) {
+  __shared__ int sums[1024];
+  const int tid = threadIdx.x;
+  const int per = (N + 1023) / 1024;
+  const int lo = min(N, tid * per), hi = min(N, lo + per);
+  int c = 0;
+  for (int n = lo; n < hi; ++n) c += unsigned(label[n]) < unsigned(V);
+  sums[tid] = c;
+  __syncthreads();
+  for (int s = 1; s < 1024; s *= 2) {
+    const int o = tid >= s ? sums[tid - s] : 0;
+    __syncthreads();
+    sums[tid] += o;
+    __syncthreads();
+  }
+  int at = sums[tid] - c;
+  for (int n = lo; n < hi; ++n) {
+    const bool used = unsigned(label[n]) < unsigned(V);
+    place[n] = used ? at : -1;
+    if (used) row[at++] = n;
+  }
+  if (tid == 1023) *count = sums[1023];
+}
+
+// X[i] = [h[row[i]] | 0 | W1[prev[row[i]]] | 0]; rows from count up to the
+// next multiple of 64 are zero.  One workgroup per row.
+template <typename T>
+__global__ __launch_bounds__(256) void gather_kernel(int V, int d, int dp, int r, int rp, const int* __restrict__ count,
+                                                     const int* __restrict__ row, const int* __restrict__ prev,
+                                                     const T* __restrict__ h, const T* __restrict__ W1,
+                                                     T* __restrict__ X) {
+  const int i = blockIdx.x, n = *count;
+  if (i >= ((n + 63) & ~63)) return;
+  T* x = X + size_t(i) * (dp + rp);
+  const bool used = i < n;
+  const int src = used ? row[i] : 0;
+  const T zero = from_f32<T>(0.f);
+  if (dp) {
+    const T* hr = h + size_t(src) * d;
+    for (int c = threadIdx.x; c < dp; c += 256) x[c] = used && c < d ? hr[c] : zero;
+  }
+  if (rp) {
+    const int t = used ? min(max(prev[src], 0), V - 1) : 0;
+    const T* wr = W1 + size_t(t) * r;
+    for (int c = threadIdx.x; c < rp; c += 256) x[dp + c] = used && c < r ? wr[c] : zero;
+  }
+}
+
+// lse and nll of every row from the tiles' statistics, a fixed order: 16
+// lanes per row, 16 rows per workgroup.
+__global__ __launch_bounds__(256) void join_kernel(int N, int tiles, const int* __restrict__ place,
+                                                   const float2* __restrict__ stat, long stat_ld,
+                                                   const float* __restrict__ zlab, float* __restrict__ nll,
+                                                   float* __restrict__ lse) {
+  const int n = blockIdx.x * 16 + (threadIdx.x >> 4), first = threadIdx.x & 15;
+  const int i = n < N ? place[n] : -1;
+  const float ninf = -__builtin_huge_valf();
+  float m = ninf, s = 0.f;
+  if (i >= 0)
+    for (int t = first; t < tiles; t += 16) {
+      const float2 q = stat[size_t(t) * stat_ld + i];
+      const float top = fmaxf(m, q.x), ref = top == ninf ? 0.f : top;
+      s = s * __expf(m - ref) + q.y * __expf(q.x - ref);
+      m = top;
+    }
+#pragma unroll
+  for (int x = 1; x < 16; x *= 2) {
+    const float om = __shfl_xor(m, x, 64), os = __shfl_xor(s, x, 64);
+    const float top = fmaxf(m, om), ref = top == ninf ? 0.f : top;
+    s = s * __expf(m - ref) + os * __expf(om - ref);
+    m = top;
+  }
+  if (n < N && first == 0) {
+    // nll from the maximum, not from the rounded lse: where the label has
+    // the maximum, what is left is log(s) to its own accuracy
+    const float l = logf(s);
+    lse[n] = i >= 0 ? m + l : 0.f;
+    nll[n] = i >= 0 ? (m - zlab[i]) + l : 0.f;
+  }
+}
+
+// Rows of dU without a label are zero.
+template <typename T>
+__global__ __launch_bounds__(256) void zero_rows_kernel(int V, const int* __restrict__ place, T* __restrict__ dU) {
+  if (place[blockIdx.x] >= 0) return;
+  T* u = dU + size_t(blockIdx.x) * V;
+  for (int v = threadIdx.x; v < V; v += 256) u[v] = from_f32<T>(0.f);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void zero_kernel(size_t n, T* __restrict__ p) {
+  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256) p[i] = from_f32<T>(0.f);
+}
+
+// dh[n] = the row's dX, zero for rows without a label.
+template <typename T>
+__global__ __launch_bounds__(256) void dh_kernel(int d, long ld, const int* __restrict__ place,
+                                                 const float* __restrict__ dX, T* __restrict__ dh) {
+  const int n = blockIdx.x, i = place[n];
+  for (int c = threadIdx.x; c < d; c += 256) dh[size_t(n) * d + c] = from_f32<T>(i >= 0 ? dX[size_t(i) * ld + c] : 0.f);
+}
+
+// dW1[t] = sum of dE over the rows whose previous token is t, in row order.
+// One wave per row; the first row of a token does its sum (the table was
+// zeroed before).
+template <typename T>
+__global__ __launch_bounds__(256) void dw1_kernel(int V, int r, long ld, const int* __restrict__ count,
+                                                  const int* __restrict__ row, const int* __restrict__ prev,
+                                                  const float* __restrict__ dE, T* __restrict__ dW1) {
+  const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, n = *count;
+  if (i >= n) return;
+  const int t = min(max(prev[row[i]], 0), V - 1);
+  for (int j = 0; j < i; j += 64) {
+    const bool same = j + lane < i && min(max(prev[row[j + lane]], 0), V - 1) == t;
+    if (__any(same)) return;
+  }
+  for (int c0 = 0; c0 < r; c0 += 64) {
+    const int c = c0 + lane;
+    float s = 0.f;
+    for (int j = i; j < n; j += 64) {
+      uint64_t mask = __ballot(j + lane < n && min(max(prev[row[j + lane]], 0), V - 1) == t);
+      while (mask) {
+        const int b = __builtin_ctzll(mask);
+        mask &= mask - 1;
+        if (c < r) s += dE[size_t(j + b) * ld + c];
+      }
+    }
+    if (c < r) dW1[size_t(t) * r + c] = from_f32<T>(s);
+  }
+}
+
+// What the forward and the backward call carve out of the workspace.
+struct Layout {
+  size_t row, place, X, stat, zlab, dz, dX, total;
+  int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
+};
+
+Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
+  const size_t elem = bf16 ? 2 : 4;
+  Layout L = {};
+  L.dp = int(up(d, 64));
+  L.rp = int(up(r, 64));
+  L.rows = int(up(N > 0 ? N : 1, 256));
+  size_t at = 256;   // count
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at += up(bytes, 256);
+    return p;
+  };
+  L.row = take(size_t(N) * 4);
+  L.place = take(size_t(N) * 4);
+  L.X = take(size_t(L.rows) * (L.dp + L.rp) * elem);
+  if (!backward) {
+    L.stat = take((size_t(V) + kTileF32 - 1) / kTileF32 * N * sizeof(float2));
+    L.zlab = take(size_t(N) * 4);
+  } else {
+    const size_t full = up(V, kPieceAlign);
+    const size_t most = kPieceBytes / (size_t(L.rows) * elem);
+    const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
+    L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
+    L.dz = take(size_t(L.rows) * L.width * elem);
+    L.dX = take(size_t(L.rows) * (L.dp + L.rp) * 4);
+  }
+  L.total = at;
+  return L;
+}
+
+template <typename T>
+struct Parts {
+  Layout L;
+  int *count, *row, *place;
+  T* X;
+  int kx;
+};
+
+template <typename T>
+hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t stream) {
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  p.L = L;
+  p.count = reinterpret_cast<int*>(ws);
+  p.row = reinterpret_cast<int*>(ws + L.row);
+  p.place = reinterpret_cast<int*>(ws + L.place);
+  p.X = reinterpret_cast<T*>(ws + L.X);
+  p.kx = L.dp + L.rp;
+  hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
+  if (p.kx && a.N)
+    hipLaunchKernelGGL((gather_kernel<T>), dim3(unsigned(up(a.N, 64))), dim3(256), 0, stream, a.V, a.d, L.dp, a.r,
+                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X);
+  return hipGetLastError();
+}
+
+// The logits of tokens [v0, v0 + nv) as a product.
+template <typename T>
+Product<T> logits(const LossArgs& a, const Parts<T>& p, int v0, int nv) {
+  Product<T> g = {};
+  if (a.d) {
+    g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, a.d, 1, nv};
+    g.B[0] = {p.X, p.kx, 1, p.L.rows};
+    g.K[0] = a.d;
+  }
+  if (a.r) {
+    g.A[1] = {static_cast<const T*>(a.W2) + v0, 1, a.V, nv};
+    g.B[1] = {p.X + p.L.dp, p.kx, 1, p.L.rows};
+    g.K[1] = a.r;
+  }
+  g.nb = p.count;
+  return g;
+}
+
+template <typename T>
+BaseLogits<T> base_logits(const LossArgs& a, const Parts<T>& p, int v0, int nv, const void* dU) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.U) | reinterpret_cast<uintptr_t>(dU);
+  return {static_cast<const T*>(a.U), p.row, a.V, v0, nv, a.V % 4 == 0 && at % (4 * sizeof(T)) == 0};
+}
+
+template <typename T>
+hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
+  const Layout L = layout(a.N, a.V, a.d, a.r, a.bf16, false);
+  Parts<T> p;
+  hipError_t e = start(a, L, p, stream);
+  if (e != hipSuccess) return e;
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  float2* stat = reinterpret_cast<float2*>(ws + L.stat);
+  float* zlab = reinterpret_cast<float*>(ws + L.zlab);
+  StatsEpi<T, 2, kTileF32> epi{base_logits(a, p, 0, a.V, nullptr), a.label, stat, a.N, zlab};
+  if ((e = launch_tile_f32(logits(a, p, 0, a.V), epi, a.V, a.N, stream)) != hipSuccess) return e;
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, stream, a.N,
+                     (a.V + kTileF32 - 1) / kTileF32, p.place, stat, long(a.N), zlab, a.nll, a.lse);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
+  const Layout L = layout(a.N, a.V, a.d, a.r, a.bf16, true);
+  Parts<T> p;
+  hipError_t e = start(a, L, p, stream);
+  if (e != hipSuccess) return e;
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  T* dz = reinterpret_cast<T*>(ws + L.dz);
+  float* dX = reinterpret_cast<float*>(ws + L.dX);
+  T *dU = static_cast<T*>(a.dU), *dWo = static_cast<T*>(a.dWo), *dW2 = static_cast<T*>(a.dW2);
+  const bool rows_h = a.dh != nullptr, rows_e = a.dW1 != nullptr;
+  if (dU && a.N)
+    hipLaunchKernelGGL((zero_rows_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.V, p.place, dU);
+  for (int v0 = 0; v0 < a.V; v0 += L.width) {
+    const int nv = a.V - v0 < L.width ? a.V - v0 : L.width;
+    GradEpi<T> grad{base_logits(a, p, v0, nv, dU), a.label, a.lse_in, a.g, dz, L.width, dU};
+    if ((e = launch_tile_f32(logits(a, p, v0, nv), grad, nv, a.N, stream)) != hipSuccess) return e;
+    const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
+    if (rows_h) {
+      Product<T> g = {};
+      g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, 1, a.d, a.d};
+      g.B[0] = dz_rows;
+      g.K[0] = nv;
+      g.nb = p.count;
+      if ((e = launch_tile_f32(g, AddEpi{dX, p.kx, a.d, v0 == 0}, a.d, a.N, stream)) != hipSuccess) return e;
+    }
+    if (rows_e) {
+      Product<T> g = {};
+      g.A[0] = {static_cast<const T*>(a.W2) + v0, a.V, 1, a.r};
+      g.B[0] = dz_rows;
+      g.K[0] = nv;
+      g.nb = p.count;
+      if ((e = launch_tile_f32(g, AddEpi{dX + L.dp, p.kx, a.r, v0 == 0}, a.r, a.N, stream)) != hipSuccess) return e;
+    }
+    if (dWo) {
+      Product<T> g = {};
+      g.A[0] = {p.X, 1, p.kx, a.d};
+      g.B[0] = dz_tokens;
+      g.k0 = p.count;
+      StoreEpi<T> epi{dWo + size_t(v0) * a.d, a.d, a.d,
+                      a.d % 4 == 0 && reinterpret_cast<uintptr_t>(dWo) % (4 * sizeof(T)) == 0};
+      if ((e = launch_tile_f32(g, epi, a.d, nv, stream)) != hipSuccess) return e;
+    }
+    if (dW2) {
+      Product<T> g = {};
+      g.A[0] = dz_tokens;
+      g.B[0] = {p.X + L.dp, 1, p.kx, a.r};
+      g.k0 = p.count;
+      StoreEpi<T> epi{dW2 + v0, a.V, nv, a.V % 4 == 0 && reinterpret_cast<uintptr_t>(dW2) % (4 * sizeof(T)) == 0};
+      if ((e = launch_tile_f32(g, epi, nv, a.r, stream)) != hipSuccess) return e;
+    }
+  }
+  if (a.dh && a.N)
+    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(p.kx), p.place, dX,
+                       static_cast<T*>(a.dh));
+  if (a.dW1) {
+    hipLaunchKernelGGL((zero_kernel<T>), dim3(2048), dim3(256), 0, stream, size_t(a.V) * a.r, static_cast<T*>(a.dW1));
+    if (a.N)
+      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned((a.N + 3) / 4)), dim3(256), 0, stream, a.V, a.r, long(p.kx),
+                         p.count, p.row, a.prev, dX + L.dp, static_cast<T*>(a.dW1));
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t loss_workspace_bytes(int N, int V, int d, int r, bool bf16, bool backward) {
+  return layout(N, V, d, r, bf16, backward).total;
+}
+
+hipError_t launch_markov_loss(const LossArgs& a, hipStream_t stream) {
+  return a.bf16 ? loss_t<bf16_t>(a, stream) : loss_t<float>(a, stream);
+}
+
+hipError_t launch_markov_loss_backward(const LossArgs& a, hipStream_t stream) {
+  return a.bf16 ? loss_backward_t<bf16_t>(a, stream) : loss_backward_t<float>(a, stream);
+}
+
+}  // namespace dspark

@@ -1,0 +1,390 @@
+// Shared parts of the projection kernels (linear.hip, markov_loss.hip): the
+// operand and tile descriptions and the epilogues.
+//
+// Every product is written as C(a, b) = sum_k A(a, k) * B(b, k).  The a axis
+// is always the one that is contiguous in the output, because an MFMA
+// accumulator holds four consecutive a of one b per lane: outputs are stored
+// four values at a time, and a softmax over a needs only an in-lane reduction
+// and two lane exchanges.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_util.h"
+
+namespace dspark {
+
+typedef uint16_t bf16_t;   // storage of a bfloat16
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(bf16_t x) { return bf16_to_f32(x); }
+
+// fp32 -> bf16, round to nearest even (NaN stays NaN): the only rounding of
+// an output, after all sums have been made in fp32.
+__device__ __forceinline__ bf16_t f32_to_bf16(float f) {
+  const __bf16 h = (__bf16)f;
+  return __builtin_bit_cast(bf16_t, h);
+}
+template <typename T> __device__ __forceinline__ T from_f32(float f);
+template <> __device__ __forceinline__ float from_f32<float>(float f) { return f; }
+template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) { return f32_to_bf16(f); }
+
+// Four consecutive values at p; `vec` (uniform): p is aligned for one wide access.
+__device__ __forceinline__ f32x4_t load4(const float* p, int n, bool vec) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (vec && n >= 4) return *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) v[i] = p[i];
+  return v;
+}
+__device__ __forceinline__ f32x4_t load4(const bf16_t* p, int n, bool vec) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (vec && n >= 4) {
+    const u32x2_t u = *reinterpret_cast<const u32x2_t*>(p);
+    v[0] = bf16_lo(u[0]);
+    v[1] = bf16_hi(u[0]);
+    v[2] = bf16_lo(u[1]);
+    v[3] = bf16_hi(u[1]);
+    return v;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) v[i] = bf16_to_f32(p[i]);
+  return v;
+}
+__device__ __forceinline__ void store4(float* p, f32x4_t v, int n, bool vec) {
+  if (vec && n >= 4) {
+    *reinterpret_cast<f32x4_t*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) p[i] = v[i];
+}
+__device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n, bool vec) {
+  if (vec && n >= 4) {
+    u32x2_t u;
+    u[0] = uint32_t(f32_to_bf16(v[0])) | (uint32_t(f32_to_bf16(v[1])) << 16);
+    u[1] = uint32_t(f32_to_bf16(v[2])) | (uint32_t(f32_to_bf16(v[3])) << 16);
+    *reinterpret_cast<u32x2_t*>(p) = u;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) p[i] = f32_to_bf16(v[i]);
+}
+
+// exp(x), x <= 0: for fp32 storage to the last bit or two; for bf16 storage by
+// the hardware's base-2 exponential, whose argument rounding costs |x| 2^-23
+// relative, far below the half step 2^-8 that dz is rounded by.
+template <typename T> __device__ __forceinline__ float exp_of(float x);
+template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
+template <> __device__ __forceinline__ float exp_of<bf16_t>(float x) { return __expf(x); }
+
+// One operand: element (a, k) at p[a * sa + k * sk], one of the strides 1;
+// a in [0, n).
+template <typename T>
+struct Operand {
+  const T* p;
+  long sa, sk;
+  int n;
+};
+
+// A product whose contraction has up to two parts (the output projection and
+// the Markov factor share one accumulator).
+template <typename T>
+struct Product {
+  Operand<T> A[2], B[2];
+  int K[2];
+  // Device-side sizes, where a host does not know them (rows that have a
+  // label): the number of b in use, and the length of the first contraction.
+  const int* nb = nullptr;
+  const int* k0 = nullptr;
+};
+
+// Where a wave's accumulators lie: acc[i][j][e] is C(a0 + 16 i + 4 (lane / 16)
+// + e, b0 + 16 j + lane % 16).  tile_a: index of the workgroup's tile along a;
+// wave_a of waves_a: the wave's place along a inside it.
+struct TileAt {
+  int a0, b0, nb, tile_a, wave_a, wave_b;
+};
+
+// ---------------------------------------------------------------------------
+// Activations
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float act_value(int act, float z) {
+  if (act == 1) return z > 0.f ? z : 0.f;
+  if (act == 2) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == 3) return z / (1.f + __expf(-z));
+  return z;
+}
+// d act / dz
+__device__ __forceinline__ float act_slope(int act, float z) {
+  if (act == 1) return z > 0.f ? 1.f : 0.f;
+  if (act == 2)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  if (act == 3) {
+    const float s = 1.f / (1.f + __expf(-z));
+    return s + z * s * (1.f - s);
+  }
+  return 1.f;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues.  init() fills the accumulators before the product, done() takes
+// them after it; lds is the workgroup's shared memory, free by then.
+// ---------------------------------------------------------------------------
+template <int FM, int FN>
+__device__ __forceinline__ void acc_zero(f32x4_t (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+}
+
+// y[b][a] = act(C + bias[a]) + residual[b][a]; pre[b][a] = C + bias[a] if asked for.
+template <typename T>
+struct LinearEpi {
+  const T* bias;
+  const T* residual;
+  T* y;
+  float* pre;
+  int act, na;
+  bool vec;   // rows of na values keep four-value alignment
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+    acc_zero(acc);
+  }
+  template <int FM, int FN>
+  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+      const int n = na - a;
+      f32x4_t bv = {0.f, 0.f, 0.f, 0.f};
+      if (bias) bv = load4(bias + a, n, false);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b >= t.nb) continue;
+        f32x4_t v = acc[i][j] + bv;
+        const size_t at = size_t(b) * na + a;
+        if (pre) store4(pre + at, v, n, vec);
+        if (act) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = act_value(act, v[e]);
+        }
+        if (residual) v += load4(residual + at, n, vec);
+        store4(y + at, v, n, vec);
+      }
+    }
+  }
+};
+
+// out[b][a] = C as T (row stride ld): a weight gradient.
+template <typename T>
+struct StoreEpi {
+  T* out;
+  long ld;
+  int na;
+  bool vec;
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+    acc_zero(acc);
+  }
+  template <int FM, int FN>
+  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb) store4(out + size_t(b) * ld + a, acc[i][j], na - a, vec);
+      }
+    }
+  }
+};
+
+// sum[b][a] (+)= C in fp32 (row stride ld, a multiple of 4): a row gradient
+// gathered over the pieces of the vocabulary, in piece order.
+struct AddEpi {
+  float* sum;
+  long ld;
+  int na;
+  bool first;
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+    acc_zero(acc);
+    if (first) return;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb) acc[i][j] = load4(sum + size_t(b) * ld + a, na - a, true);
+      }
+    }
+  }
+  template <int FM, int FN>
+  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb) store4(sum + size_t(b) * ld + a, acc[i][j], na - a, true);
+      }
+    }
+  }
+};
+
+// The logits' share of the loss kernels: a is a token id (from v0 on), b a
+// compact row; U[row[b]][v0 + a] starts the accumulator if base logits are
+// given.
+template <typename T>
+struct BaseLogits {
+  const T* U;
+  const int* row;
+  long V;
+  int v0, na;
+  bool vec;   // v0 and V keep four-value alignment
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+    acc_zero(acc);
+    if (!U) return;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int b = t.b0 + 16 * j + (lane & 15);
+      if (b >= t.nb) continue;
+      const T* u = U + size_t(row[b]) * V + v0;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+        if (a < na) acc[i][j] = load4(u + a, na - a, vec);
+      }
+    }
+  }
+};
+
+// Softmax statistics of one tile of the vocabulary: stat[tile_a][b] = (max,
+// sum of exp(z - max)) in fp32; zlab[b] = the logit of the row's label, by
+// the tile that holds it.  A tile whose logits are all -inf (masked base
+// logits) has max -inf and sum 0.
+template <typename T, int WAVES_A, int BN>
+struct StatsEpi {
+  BaseLogits<T> base;
+  const int* label;   // [N], by original row
+  float2* stat;       // [tiles][stat_ld]
+  long stat_ld;
+  float* zlab;
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+    base.init(acc, t);
+  }
+  template <int FM, int FN>
+  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void* lds) const {
+    const int lane = threadIdx.x & 63;
+    float2* part = static_cast<float2*>(lds);   // [WAVES_A][BN]
+    const float ninf = -__builtin_huge_valf();
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int b = t.b0 + 16 * j + (lane & 15);
+      const int y = b < t.nb ? label[base.row[b]] - base.v0 : -1;
+      float m = ninf;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (a + e >= base.na) acc[i][j][e] = ninf;
+          if (a + e == y) zlab[b] = acc[i][j][e];
+          m = fmaxf(m, acc[i][j][e]);
+        }
+      }
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      const float ref = m == ninf ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += exp_of<T>(acc[i][j][e] - ref);
+      s += __shfl_xor(s, 16, 64);
+      s += __shfl_xor(s, 32, 64);
+      if (lane < 16) part[t.wave_a * BN + t.wave_b * 16 * FN + 16 * j + lane] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < BN; c += blockDim.x) {
+      const int b = t.b0 - t.wave_b * 16 * FN + c;
+      if (b >= t.nb) continue;
+      float2 q = part[c];
+      for (int w = 1; w < WAVES_A; ++w) {
+        const float2 o = part[w * BN + c];
+        const float m = fmaxf(q.x, o.x);
+        const float ref = m == ninf ? 0.f : m;
+        q.y = q.y * __expf(q.x - ref) + o.y * __expf(o.x - ref);
+        q.x = m;
+      }
+      stat[size_t(t.tile_a) * stat_ld + b] = q;
+    }
+  }
+};
+
+// Gradient of the loss by the logits, of one piece of the vocabulary:
+// dz[b][a] = g (exp(z - lse) - [a is the label]), rounded to T because the
+// next products take it in T; b beyond the rows in use get 0 (they end the
+// contraction of the weight gradients).  dU, if asked for, gets the same.
+template <typename T>
+struct GradEpi {
+  BaseLogits<T> base;
+  const int* label;
+  const float* lse;
+  const float* g;
+  T* dz;
+  long dz_ld;
+  T* dU;
+  template <int FM, int FN>
+  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+    base.init(acc, t);
+  }
+  template <int FM, int FN>
+  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int b = t.b0 + 16 * j + (lane & 15);
+      const bool in = b < t.nb;
+      const int row = in ? base.row[b] : 0;
+      const int y = in ? label[row] - base.v0 : -1;
+      const float l = in ? lse[row] : 0.f, gb = in ? g[row] : 0.f;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+        f32x4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp_of<T>(acc[i][j][e] - l);
+          v[e] = in && a + e < base.na ? gb * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
+        }
+        // the piece's width dz_ld is a multiple of the tile: every a of the tile is inside it
+        store4(dz + size_t(b) * dz_ld + a, v, 4, true);
+        if (dU && in && a < base.na) store4(dU + size_t(row) * base.V + base.v0 + a, v, base.na - a, base.vec);
+      }
+    }
+  }
+};
+
+}  // namespace dspark
