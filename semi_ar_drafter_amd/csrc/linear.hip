@@ -7,6 +7,7 @@
 // rows that give the bias gradient.
 #include "launch.h"
 #include "projection.h"
+#include "tile_bf16.h"
 #include "tile_f32.h"
 
 namespace dspark {
@@ -15,28 +16,27 @@ namespace {
 
 constexpr int kDzRows = 64;   // rows per workgroup of dz_kernel
 
-// dz[m][n] = T(dy act'(pre)) into rows of ld values (columns N..ld zero), and
-// part[chunk][n] = the chunk's sum of dz over its rows, in fp32, before the
-// rounding to T.  256 threads, one column each.
+// dz[m][n] = T(dy act'(pre)) into rows of ld values (columns N..ld and rows
+// M..rows zero), and part[chunk][n] = the chunk's sum of dz over its rows, in
+// fp32, before the rounding to T.  256 threads, one column each.
 template <typename T>
-__global__ __launch_bounds__(256) void dz_kernel(int M, int N, int act, const T* __restrict__ dy,
+__global__ __launch_bounds__(256) void dz_kernel(int M, int rows, int N, int act, const T* __restrict__ dy,
                                                  const float* __restrict__ pre, T* __restrict__ dz, long ld,
                                                  float* __restrict__ part) {
   const int n = blockIdx.x * 256 + threadIdx.x;
-  const int m0 = blockIdx.y * kDzRows, m1 = min(M, m0 + kDzRows);
-  if (n >= N) {
-    if (dz && n < ld)
-      for (int m = m0; m < m1; ++m) dz[size_t(m) * ld + n] = from_f32<T>(0.f);
-    return;
-  }
+  const int m0 = blockIdx.y * kDzRows, m1 = min(rows, m0 + kDzRows);
+  if (n >= ld) return;
   float s = 0.f;
   for (int m = m0; m < m1; ++m) {
-    float v = to_f32(dy[size_t(m) * N + n]);
-    if (act) v *= act_slope(act, pre[size_t(m) * N + n]);
+    float v = 0.f;
+    if (m < M && n < N) {
+      v = to_f32(dy[size_t(m) * N + n]);
+      if (act) v *= act_slope(act, pre[size_t(m) * N + n]);
+    }
     if (dz) dz[size_t(m) * ld + n] = from_f32<T>(v);
     s += v;
   }
-  if (part) part[size_t(blockIdx.y) * N + n] = s;
+  if (part && n < N) part[size_t(blockIdx.y) * N + n] = s;
 }
 
 // dbias[n] = sum over chunks, in chunk order.
@@ -50,18 +50,42 @@ __global__ __launch_bounds__(256) void dbias_kernel(int N, int chunks, const flo
   dbias[n] = from_f32<T>(s);
 }
 
+// dst[r][0..ld) = src[r][0..n), zeros behind: rows whose length is no multiple
+// of a step, copied for the bf16 kernels.  One workgroup per row.
+__global__ __launch_bounds__(256) void pad_rows_kernel(int n, long ld, const bf16_t* __restrict__ src,
+                                                       bf16_t* __restrict__ dst) {
+  const bf16_t* s = src + size_t(blockIdx.x) * n;
+  bf16_t* d = dst + size_t(blockIdx.x) * ld;
+  for (int i = threadIdx.x; i < ld; i += 256) d[i] = i < n ? s[i] : bf16_t(0);
+}
+
+// y = act(sum over splits + bias) + residual, the splits in order: four
+// values per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void join_splits_kernel(int M, int N, int splits, const float* __restrict__ part,
+                                                          long ld, LinearEpi<T> epi) {
+  const int quads = (N + 3) / 4;
+  const long at = long(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= long(M) * quads) return;
+  const int b = int(at / quads), a = int(at % quads) * 4, n = N - a;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + (size_t(s) * M + b) * ld + a);
+  epi.finish(v, b, a, n);
+}
+
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-inline long dz_stride(int N) { return (long(N) + 63) / 64 * 64; }
+inline long up64(long x) { return (x + 63) / 64 * 64; }
+inline long dz_stride(int N) { return up64(N); }
 inline int dz_chunks(int M) { return (M + kDzRows - 1) / kDzRows; }
 
+// Splits of a bf16 product's contraction into partial sums [split][rows][up64(na)].
+inline size_t split_bytes(int na, int nb, long K) {
+  const int s = splits_for(na, nb, K);
+  return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
+}
+
 template <typename T>
-hipError_t linear_t(const LinearArgs& a, hipStream_t stream) {
-  Product<T> g = {};
-  const T* x = static_cast<const T*>(a.x);
-  const T* w = static_cast<const T*>(a.w);
-  g.A[0] = {w, a.K, 1, a.N};
-  g.B[0] = {x, a.K, 1, a.M};
-  g.K[0] = a.K;
+LinearEpi<T> linear_epi(const LinearArgs& a) {
   LinearEpi<T> epi;
   epi.bias = static_cast<const T*>(a.bias);
   epi.residual = static_cast<const T*>(a.residual);
@@ -71,67 +95,172 @@ hipError_t linear_t(const LinearArgs& a, hipStream_t stream) {
   epi.na = a.N;
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.residual);
   epi.vec = a.N % 4 == 0 && at % (4 * sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
-  return launch_tile_f32(g, epi, a.N, a.M, stream);
+  return epi;
+}
+
+// A product into epi, or by way of split partial sums in `part`.
+template <int LA, int LB>
+hipError_t product(const Product<bf16_t>& g, bool any, const LinearEpi<bf16_t>& epi, int na, int nb, float* part,
+                   hipStream_t stream) {
+  const int splits = splits_for(na, nb, g.K[0]);
+  hipError_t e;
+  if (splits == 1) {
+    auto make = [&](auto) { return epi; };
+    return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, 1, stream)
+               : launch_bf16<LA, LA, LB, false>(g, make, na, nb, 1, stream);
+  }
+  const long ld = up64(na);
+  auto make = [&](auto) { return AddEpi{part, ld, na, true, long(nb) * ld}; };
+  e = any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, splits, stream)
+          : launch_bf16<LA, LA, LB, false>(g, make, na, nb, splits, stream);
+  if (e != hipSuccess) return e;
+  const long quads = long(nb) * ((na + 3) / 4);
+  hipLaunchKernelGGL((join_splits_kernel<bf16_t>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, stream, nb, na,
+                     splits, part, ld, epi);
+  return hipGetLastError();
+}
+
+hipError_t linear_bf16(const LinearArgs& a, hipStream_t stream) {
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  const bf16_t* x = static_cast<const bf16_t*>(a.x);
+  long ldx = a.K;
+  if (a.K % kStep) {   // the b operand has to end in zeros
+    ldx = up64(a.K);
+    bf16_t* xp = reinterpret_cast<bf16_t*>(ws);
+    ws += up256(size_t(a.M) * ldx * 2);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(a.M)), dim3(256), 0, stream, a.K, ldx, x, xp);
+    x = xp;
+  }
+  Product<bf16_t> g = {};
+  g.A[0] = {static_cast<const bf16_t*>(a.w), a.K, 1, a.N};
+  g.B[0] = {x, ldx, 1, a.M};
+  g.K[0] = a.K;
+  return product<kRows, kRows>(g, a.K % 8 != 0, linear_epi<bf16_t>(a), a.N, a.M, reinterpret_cast<float*>(ws), stream);
+}
+
+hipError_t linear_f32(const LinearArgs& a, hipStream_t stream) {
+  Product<float> g = {};
+  g.A[0] = {static_cast<const float*>(a.w), a.K, 1, a.N};
+  g.B[0] = {static_cast<const float*>(a.x), a.K, 1, a.M};
+  g.K[0] = a.K;
+  return launch_tile_f32(g, linear_epi<float>(a), a.N, a.M, stream);
+}
+
+// dz and its chunk sums; `dz` (with its row length) is dy itself where no
+// copy is needed.
+template <typename T>
+hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** dz, long* ld, unsigned char** ws,
+                   hipStream_t stream) {
+  *dz = static_cast<const T*>(a.dy);
+  *ld = a.N;
+  float* part = reinterpret_cast<float*>(*ws);
+  *ws += up256(size_t(dz_chunks(a.M)) * a.N * 4);
+  T* out = nullptr;
+  if (copy) {
+    *ld = dz_stride(a.N);
+    out = reinterpret_cast<T*>(*ws);
+    *ws += up256(size_t(rows) * *ld * sizeof(T));
+    *dz = out;
+  }
+  if (a.N == 0) return hipSuccess;
+  if (rows > 0 && (copy || a.dbias))
+    hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 255) / 256), unsigned((rows + kDzRows - 1) / kDzRows)),
+                       dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, out, *ld,
+                       a.dbias ? part : nullptr);
+  if (a.dbias)
+    hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 255) / 256)), dim3(256), 0, stream, a.N,
+                       dz_chunks(a.M), part, static_cast<T*>(a.dbias));
+  return hipGetLastError();
 }
 
 template <typename T>
-hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
-  const T* dz = static_cast<const T*>(a.dy);
-  long ld = a.N;
+bool aligned4(const void* p, int n) {
+  return n % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
+}
+
+hipError_t linear_backward_f32(const LinearBackwardArgs& a, hipStream_t stream) {
+  const float* dz;
+  long ld;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  float* part = reinterpret_cast<float*>(ws);
-  hipError_t e;
-  if (a.N > 0 && (a.act || a.dbias)) {
-    T* out = nullptr;
-    if (a.act) {
-      ld = dz_stride(a.N);
-      out = reinterpret_cast<T*>(ws + up256(size_t(dz_chunks(a.M)) * a.N * 4));
-      dz = out;
-    }
-    if (a.M > 0)
-      hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((ld + 255) / 256), unsigned(dz_chunks(a.M))), dim3(256), 0,
-                         stream, a.M, a.N, a.act, static_cast<const T*>(a.dy), a.pre, out, ld,
-                         a.dbias ? part : nullptr);
-    if (a.dbias)
-      hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 255) / 256)), dim3(256), 0, stream, a.N,
-                         dz_chunks(a.M), part, static_cast<T*>(a.dbias));
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (a.dx && a.M > 0 && a.K > 0) {
-    Product<T> g = {};
-    g.A[0] = {static_cast<const T*>(a.w), 1, a.K, a.K};
+  hipError_t e = make_dz(a, a.act != 0, a.M, &dz, &ld, &ws, stream);
+  if (e != hipSuccess) return e;
+  if (a.dx) {
+    Product<float> g = {};
+    g.A[0] = {static_cast<const float*>(a.w), 1, a.K, a.K};
     g.B[0] = {dz, ld, 1, a.M};
     g.K[0] = a.N;
-    StoreEpi<T> epi{static_cast<T*>(a.dx), a.K, a.K,
-                    a.K % 4 == 0 && reinterpret_cast<uintptr_t>(a.dx) % (4 * sizeof(T)) == 0};
+    StoreEpi<float> epi{static_cast<float*>(a.dx), a.K, a.K, aligned4<float>(a.dx, a.K)};
     if ((e = launch_tile_f32(g, epi, a.K, a.M, stream)) != hipSuccess) return e;
   }
-  if (a.dw && a.N > 0 && a.K > 0) {
-    Product<T> g = {};
-    g.A[0] = {static_cast<const T*>(a.x), 1, a.K, a.K};
+  if (a.dw) {
+    Product<float> g = {};
+    g.A[0] = {static_cast<const float*>(a.x), 1, a.K, a.K};
     g.B[0] = {dz, 1, ld, a.N};
     g.K[0] = a.M;
-    StoreEpi<T> epi{static_cast<T*>(a.dw), a.K, a.K,
-                    a.K % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % (4 * sizeof(T)) == 0};
+    StoreEpi<float> epi{static_cast<float*>(a.dw), a.K, a.K, aligned4<float>(a.dw, a.K)};
     if ((e = launch_tile_f32(g, epi, a.K, a.N, stream)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// The gradient's products through the same epilogue as the forward one,
+// without bias, activation and residual.
+LinearEpi<bf16_t> plain_epi(void* out, int na) {
+  LinearEpi<bf16_t> epi = {};
+  epi.y = static_cast<bf16_t*>(out);
+  epi.na = na;
+  epi.vec = aligned4<bf16_t>(out, na);
+  return epi;
+}
+
+hipError_t linear_backward_bf16(const LinearBackwardArgs& a, hipStream_t stream) {
+  const bf16_t* dz;
+  long ld;
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  // as b operand dz ends in zeros along both axes
+  const bool copy = a.act != 0 || a.N % kStep != 0 || a.M % kStep != 0;
+  hipError_t e = make_dz(a, copy, up64(a.M), &dz, &ld, &ws, stream);
+  if (e != hipSuccess) return e;
+  float* part = reinterpret_cast<float*>(ws);
+  if (a.dx) {
+    Product<bf16_t> g = {};
+    g.A[0] = {static_cast<const bf16_t*>(a.w), 1, a.K, a.K};
+    g.B[0] = {dz, ld, 1, a.M};
+    g.K[0] = a.N;
+    if ((e = product<kCols, kRows>(g, a.K % 8 != 0, plain_epi(a.dx, a.K), a.K, a.M, part, stream)) != hipSuccess)
+      return e;
+  }
+  if (a.dw) {
+    Product<bf16_t> g = {};
+    g.A[0] = {static_cast<const bf16_t*>(a.x), 1, a.K, a.K};
+    g.B[0] = {dz, 1, ld, a.N};
+    g.K[0] = a.M;
+    if ((e = product<kCols, kCols>(g, a.K % 8 != 0, plain_epi(a.dw, a.K), a.K, a.N, part, stream)) != hipSuccess)
+      return e;
   }
   return hipSuccess;
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(int, int, int, bool) { return 0; }
+size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
+  if (!bf16) return 0;
+  return (K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K);
+}
 
-size_t linear_backward_workspace_bytes(int M, int N, int, bool bf16) {
-  return up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(M) * dz_stride(N) * (bf16 ? 2 : 4));
+size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16) {
+  const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4));
+  if (!bf16 || M == 0 || K == 0) return dz;
+  const size_t dx = split_bytes(K, M, N), dw = split_bytes(K, N, M);
+  return dz + (dx > dw ? dx : dw);
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
-  return a.bf16 ? linear_t<bf16_t>(a, stream) : linear_t<float>(a, stream);
+  return a.bf16 ? linear_bf16(a, stream) : linear_f32(a, stream);
 }
 
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t stream) {
-  return a.bf16 ? linear_backward_t<bf16_t>(a, stream) : linear_backward_t<float>(a, stream);
+  return a.bf16 ? linear_backward_bf16(a, stream) : linear_backward_f32(a, stream);
 }
 
 }  // namespace dspark

@@ -21,6 +21,7 @@
 // not depend on any order of execution.
 #include "launch.h"
 #include "projection.h"
+#include "tile_bf16.h"
 #include "tile_f32.h"
 
 namespace dspark {
@@ -131,21 +132,37 @@ __global__ __launch_bounds__(256) void zero_kernel(size_t n, T* __restrict__ p) 
   for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256) p[i] = from_f32<T>(0.f);
 }
 
-// dh[n] = the row's dX, zero for rows without a label.
+// Rows of dz from count up to the next multiple of 64 are zero: they end the
+// contraction over rows.  grid: (values / 2048, 64).
 template <typename T>
-__global__ __launch_bounds__(256) void dh_kernel(int d, long ld, const int* __restrict__ place,
-                                                 const float* __restrict__ dX, T* __restrict__ dh) {
-  const int n = blockIdx.x, i = place[n];
-  for (int c = threadIdx.x; c < d; c += 256) dh[size_t(n) * d + c] = from_f32<T>(i >= 0 ? dX[size_t(i) * ld + c] : 0.f);
+__global__ __launch_bounds__(256) void zero_dz_kernel(const int* __restrict__ count, long width, T* __restrict__ dz) {
+  const int n = *count, row = n + blockIdx.y;
+  if (row >= ((n + 63) & ~63)) return;
+  const long end = min(width, long(blockIdx.x + 1) * 2048);
+  for (long v = long(blockIdx.x) * 2048 + threadIdx.x; v < end; v += 256) dz[size_t(row) * width + v] = from_f32<T>(0.f);
 }
 
-// dW1[t] = sum of dE over the rows whose previous token is t, in row order.
-// One wave per row; the first row of a token does its sum (the table was
-// zeroed before).
+// dh[n] = the row's sum over splits, in order; zero for rows without a label.
 template <typename T>
-__global__ __launch_bounds__(256) void dw1_kernel(int V, int r, long ld, const int* __restrict__ count,
-                                                  const int* __restrict__ row, const int* __restrict__ prev,
-                                                  const float* __restrict__ dE, T* __restrict__ dW1) {
+__global__ __launch_bounds__(256) void dh_kernel(int d, long ld, int splits, long split, const int* __restrict__ place,
+                                                 const float* __restrict__ dX, T* __restrict__ dh) {
+  const int n = blockIdx.x, i = place[n];
+  for (int c = threadIdx.x; c < d; c += 256) {
+    float v = 0.f;
+    if (i >= 0)
+      for (int s = 0; s < splits; ++s) v += dX[size_t(s) * split + size_t(i) * ld + c];
+    dh[size_t(n) * d + c] = from_f32<T>(v);
+  }
+}
+
+// dW1[t] = sum of dE over the rows whose previous token is t, in row order,
+// each row's splits in order.  One wave per row; the first row of a token
+// does its sum (the table was zeroed before).
+template <typename T>
+__global__ __launch_bounds__(256) void dw1_kernel(int V, int r, long ld, int splits, long split,
+                                                  const int* __restrict__ count, const int* __restrict__ row,
+                                                  const int* __restrict__ prev, const float* __restrict__ dE,
+                                                  T* __restrict__ dW1) {
   const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, n = *count;
   if (i >= n) return;
   const int t = min(max(prev[row[i]], 0), V - 1);
@@ -161,17 +178,29 @@ __global__ __launch_bounds__(256) void dw1_kernel(int V, int r, long ld, const i
       while (mask) {
         const int b = __builtin_ctzll(mask);
         mask &= mask - 1;
-        if (c < r) s += dE[size_t(j + b) * ld + c];
+        if (c < r)
+          for (int q = 0; q < splits; ++q) s += dE[size_t(q) * split + size_t(j + b) * ld + c];
       }
     }
     if (c < r) dW1[size_t(t) * r + c] = from_f32<T>(s);
   }
 }
 
+// W2 with rows padded to a multiple of 64 tokens (zeros), for vocabularies
+// whose rows are not 16-byte aligned.  grid: (tokens / 1024, r).
+__global__ __launch_bounds__(256) void pad_w2_kernel(int V, long ld, const bf16_t* __restrict__ W2,
+                                                     bf16_t* __restrict__ out) {
+  const long v0 = long(blockIdx.x) * 1024;
+  for (long v = v0 + threadIdx.x; v < v0 + 1024 && v < ld; v += 256)
+    out[size_t(blockIdx.y) * ld + v] = v < V ? W2[size_t(blockIdx.y) * V + v] : bf16_t(0);
+}
+
 // What the forward and the backward call carve out of the workspace.
 struct Layout {
-  size_t row, place, X, stat, zlab, dz, dX, total;
+  size_t row, place, X, W2, stat, zlab, dz, dXh, dXe, total;
   int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
+  long w2_ld;                // row length of W2 as the products read it
+  int splits_h, splits_e;    // of the contraction over a piece's tokens
 };
 
 Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
@@ -189,6 +218,11 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
   L.row = take(size_t(N) * 4);
   L.place = take(size_t(N) * 4);
   L.X = take(size_t(L.rows) * (L.dp + L.rp) * elem);
+  L.w2_ld = V;
+  if (bf16 && r && V % 8) {
+    L.w2_ld = long(up(V, 64));
+    L.W2 = take(size_t(r) * L.w2_ld * 2);
+  }
   if (!backward) {
     L.stat = take((size_t(V) + kTileF32 - 1) / kTileF32 * N * sizeof(float2));
     L.zlab = take(size_t(N) * 4);
@@ -197,8 +231,11 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     const size_t most = kPieceBytes / (size_t(L.rows) * elem);
     const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
     L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
+    L.splits_h = bf16 && d && N ? splits_for(d, N, L.width) : 1;
+    L.splits_e = bf16 && r && N ? splits_for(r, N, L.width) : 1;
     L.dz = take(size_t(L.rows) * L.width * elem);
-    L.dX = take(size_t(L.rows) * (L.dp + L.rp) * 4);
+    L.dXh = take(size_t(L.splits_h) * L.rows * L.dp * 4);
+    L.dXe = take(size_t(L.splits_e) * L.rows * L.rp * 4);
   }
   L.total = at;
   return L;
@@ -209,6 +246,7 @@ struct Parts {
   Layout L;
   int *count, *row, *place;
   T* X;
+  const T* W2;
   int kx;
 };
 
@@ -220,11 +258,17 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t st
   p.row = reinterpret_cast<int*>(ws + L.row);
   p.place = reinterpret_cast<int*>(ws + L.place);
   p.X = reinterpret_cast<T*>(ws + L.X);
+  p.W2 = static_cast<const T*>(a.W2);
   p.kx = L.dp + L.rp;
   hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
   if (p.kx && a.N)
     hipLaunchKernelGGL((gather_kernel<T>), dim3(unsigned(up(a.N, 64))), dim3(256), 0, stream, a.V, a.d, L.dp, a.r,
                        L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X);
+  if (L.W2) {
+    p.W2 = reinterpret_cast<T*>(ws + L.W2);
+    hipLaunchKernelGGL(pad_w2_kernel, dim3(unsigned((L.w2_ld + 1023) / 1024), unsigned(a.r)), dim3(256), 0, stream,
+                       a.V, L.w2_ld, static_cast<const bf16_t*>(a.W2), reinterpret_cast<bf16_t*>(ws + L.W2));
+  }
   return hipGetLastError();
 }
 
@@ -232,14 +276,14 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t st
 template <typename T>
 Product<T> logits(const LossArgs& a, const Parts<T>& p, int v0, int nv) {
   Product<T> g = {};
+  g.B[0] = g.B[1] = {p.X, p.kx, 1, p.L.rows};
   if (a.d) {
     g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, a.d, 1, nv};
-    g.B[0] = {p.X, p.kx, 1, p.L.rows};
     g.K[0] = a.d;
   }
   if (a.r) {
-    g.A[1] = {static_cast<const T*>(a.W2) + v0, 1, a.V, nv};
-    g.B[1] = {p.X + p.L.dp, p.kx, 1, p.L.rows};
+    g.A[1] = {p.W2 + v0, 1, p.L.w2_ld, nv};
+    g.B[1].p = p.X + p.L.dp;
     g.K[1] = a.r;
   }
   g.nb = p.count;
@@ -252,6 +296,23 @@ BaseLogits<T> base_logits(const LossArgs& a, const Parts<T>& p, int v0, int nv, 
   return {static_cast<const T*>(a.U), p.row, a.V, v0, nv, a.V % 4 == 0 && at % (4 * sizeof(T)) == 0};
 }
 
+// One product by the storage type: bf16 on the bf16 matrix instruction
+// (layouts of the operands given), fp32 on the fp32 one.  make(shape) gives
+// the epilogue; any: rows of the a operand are not 16-byte aligned.
+template <int LA0, int LA1, int LB, class Make>
+hipError_t multiply(const Product<bf16_t>& g, bool any, const Make& make, int na, int nb, int splits,
+                    hipStream_t stream) {
+  return any ? launch_bf16<LA0, LA1, LB, true>(g, make, na, nb, splits, stream)
+             : launch_bf16<LA0, LA1, LB, false>(g, make, na, nb, splits, stream);
+}
+struct ShapeF32 {
+  static constexpr int BM = kTileF32, BN = kTileF32, WA = 2;
+};
+template <int LA0, int LA1, int LB, class Make>
+hipError_t multiply(const Product<float>& g, bool, const Make& make, int na, int nb, int, hipStream_t stream) {
+  return launch_tile_f32(g, make(ShapeF32()), na, nb, stream);
+}
+
 template <typename T>
 hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
   const Layout L = layout(a.N, a.V, a.d, a.r, a.bf16, false);
@@ -261,10 +322,15 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   float2* stat = reinterpret_cast<float2*>(ws + L.stat);
   float* zlab = reinterpret_cast<float*>(ws + L.zlab);
-  StatsEpi<T, 2, kTileF32> epi{base_logits(a, p, 0, a.V, nullptr), a.label, stat, a.N, zlab};
-  if ((e = launch_tile_f32(logits(a, p, 0, a.V), epi, a.V, a.N, stream)) != hipSuccess) return e;
-  hipLaunchKernelGGL(join_kernel, dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, stream, a.N,
-                     (a.V + kTileF32 - 1) / kTileF32, p.place, stat, long(a.N), zlab, a.nll, a.lse);
+  int bm = 0;
+  auto make = [&](auto shape) {
+    bm = shape.BM;
+    return StatsEpi<T, shape.WA, shape.BN>{base_logits(a, p, 0, a.V, nullptr), a.label, stat, a.N, zlab};
+  };
+  if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N, 1, stream)) != hipSuccess)
+    return e;
+  hipLaunchKernelGGL(join_kernel, dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, stream, a.N, (a.V + bm - 1) / bm,
+                     p.place, stat, long(a.N), zlab, a.nll, a.lse);
   return hipGetLastError();
 }
 
@@ -276,58 +342,67 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   T* dz = reinterpret_cast<T*>(ws + L.dz);
-  float* dX = reinterpret_cast<float*>(ws + L.dX);
+  float *dXh = reinterpret_cast<float*>(ws + L.dXh), *dXe = reinterpret_cast<float*>(ws + L.dXe);
+  const long split_h = long(L.rows) * L.dp, split_e = long(L.rows) * L.rp;
   T *dU = static_cast<T*>(a.dU), *dWo = static_cast<T*>(a.dWo), *dW2 = static_cast<T*>(a.dW2);
-  const bool rows_h = a.dh != nullptr, rows_e = a.dW1 != nullptr;
+  const bool any = a.d % 8 != 0;
   if (dU && a.N)
     hipLaunchKernelGGL((zero_rows_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.V, p.place, dU);
+  if (dWo || dW2)
+    hipLaunchKernelGGL((zero_dz_kernel<T>), dim3(unsigned(L.width + 2047) / 2048, 64), dim3(256), 0, stream, p.count,
+                       long(L.width), dz);
   for (int v0 = 0; v0 < a.V; v0 += L.width) {
     const int nv = a.V - v0 < L.width ? a.V - v0 : L.width;
-    GradEpi<T> grad{base_logits(a, p, v0, nv, dU), a.label, a.lse_in, a.g, dz, L.width, dU};
-    if ((e = launch_tile_f32(logits(a, p, v0, nv), grad, nv, a.N, stream)) != hipSuccess) return e;
+    auto grad = [&](auto) {
+      return GradEpi<T>{base_logits(a, p, v0, nv, dU), a.label, a.lse_in, a.g, dz, L.width, dU};
+    };
+    if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N, 1, stream)) != hipSuccess) return e;
     const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
-    if (rows_h) {
+    if (a.dh) {
       Product<T> g = {};
       g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, 1, a.d, a.d};
       g.B[0] = dz_rows;
       g.K[0] = nv;
       g.nb = p.count;
-      if ((e = launch_tile_f32(g, AddEpi{dX, p.kx, a.d, v0 == 0}, a.d, a.N, stream)) != hipSuccess) return e;
+      auto add = [&](auto) { return AddEpi{dXh, L.dp, a.d, v0 == 0, split_h}; };
+      if ((e = multiply<kCols, kCols, kRows>(g, any, add, a.d, a.N, L.splits_h, stream)) != hipSuccess) return e;
     }
-    if (rows_e) {
+    if (a.dW1) {
       Product<T> g = {};
-      g.A[0] = {static_cast<const T*>(a.W2) + v0, a.V, 1, a.r};
+      g.A[0] = {p.W2 + v0, L.w2_ld, 1, a.r};
       g.B[0] = dz_rows;
       g.K[0] = nv;
       g.nb = p.count;
-      if ((e = launch_tile_f32(g, AddEpi{dX + L.dp, p.kx, a.r, v0 == 0}, a.r, a.N, stream)) != hipSuccess) return e;
+      auto add = [&](auto) { return AddEpi{dXe, L.rp, a.r, v0 == 0, split_e}; };
+      if ((e = multiply<kRows, kRows, kRows>(g, false, add, a.r, a.N, L.splits_e, stream)) != hipSuccess) return e;
     }
     if (dWo) {
       Product<T> g = {};
       g.A[0] = {p.X, 1, p.kx, a.d};
       g.B[0] = dz_tokens;
       g.k0 = p.count;
-      StoreEpi<T> epi{dWo + size_t(v0) * a.d, a.d, a.d,
-                      a.d % 4 == 0 && reinterpret_cast<uintptr_t>(dWo) % (4 * sizeof(T)) == 0};
-      if ((e = launch_tile_f32(g, epi, a.d, nv, stream)) != hipSuccess) return e;
+      const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(dWo) % (4 * sizeof(T)) == 0;
+      auto store = [&](auto) { return StoreEpi<T>{dWo + size_t(v0) * a.d, a.d, a.d, vec}; };
+      if ((e = multiply<kCols, kCols, kCols>(g, false, store, a.d, nv, 1, stream)) != hipSuccess) return e;
     }
     if (dW2) {
       Product<T> g = {};
       g.A[0] = dz_tokens;
       g.B[0] = {p.X + L.dp, 1, p.kx, a.r};
       g.k0 = p.count;
-      StoreEpi<T> epi{dW2 + v0, a.V, nv, a.V % 4 == 0 && reinterpret_cast<uintptr_t>(dW2) % (4 * sizeof(T)) == 0};
-      if ((e = launch_tile_f32(g, epi, nv, a.r, stream)) != hipSuccess) return e;
+      const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(dW2) % (4 * sizeof(T)) == 0;
+      auto store = [&](auto) { return StoreEpi<T>{dW2 + v0, a.V, nv, vec}; };
+      if ((e = multiply<kCols, kCols, kCols>(g, false, store, nv, a.r, 1, stream)) != hipSuccess) return e;
     }
   }
   if (a.dh && a.N)
-    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(p.kx), p.place, dX,
-                       static_cast<T*>(a.dh));
+    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(L.dp), L.splits_h, split_h,
+                       p.place, dXh, static_cast<T*>(a.dh));
   if (a.dW1) {
     hipLaunchKernelGGL((zero_kernel<T>), dim3(2048), dim3(256), 0, stream, size_t(a.V) * a.r, static_cast<T*>(a.dW1));
     if (a.N)
-      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned((a.N + 3) / 4)), dim3(256), 0, stream, a.V, a.r, long(p.kx),
-                         p.count, p.row, a.prev, dX + L.dp, static_cast<T*>(a.dW1));
+      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned((a.N + 3) / 4)), dim3(256), 0, stream, a.V, a.r, long(L.rp),
+                         L.splits_e, split_e, p.count, p.row, a.prev, dXe, static_cast<T*>(a.dW1));
   }
   return hipGetLastError();
 }

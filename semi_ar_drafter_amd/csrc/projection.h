@@ -153,32 +153,32 @@ struct LinearEpi {
   int act, na;
   bool vec;   // rows of na values keep four-value alignment
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
     acc_zero(acc);
   }
+  // four values from (b, a) on, n of them inside the row
+  __device__ __forceinline__ void finish(f32x4_t v, int b, int a, int n) const {
+    if (bias) v += load4(bias + a, n, false);
+    const size_t at = size_t(b) * na + a;
+    if (pre) store4(pre + at, v, n, vec);
+    if (act) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = act_value(act, v[e]);
+    }
+    if (residual) v += load4(residual + at, n, vec);
+    store4(y + at, v, n, vec);
+  }
   template <int FM, int FN>
-  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int a = t.a0 + 16 * i + 4 * (lane >> 4);
       if (a >= na) continue;
-      const int n = na - a;
-      f32x4_t bv = {0.f, 0.f, 0.f, 0.f};
-      if (bias) bv = load4(bias + a, n, false);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int b = t.b0 + 16 * j + (lane & 15);
-        if (b >= t.nb) continue;
-        f32x4_t v = acc[i][j] + bv;
-        const size_t at = size_t(b) * na + a;
-        if (pre) store4(pre + at, v, n, vec);
-        if (act) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = act_value(act, v[e]);
-        }
-        if (residual) v += load4(residual + at, n, vec);
-        store4(y + at, v, n, vec);
+        if (b < t.nb) finish(acc[i][j], b, a, na - a);
       }
     }
   }
@@ -192,11 +192,11 @@ struct StoreEpi {
   int na;
   bool vec;
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
     acc_zero(acc);
   }
   template <int FM, int FN>
-  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -218,8 +218,9 @@ struct AddEpi {
   long ld;
   int na;
   bool first;
+  long split = 0;   // split s of the contraction sums into sum + s * split
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
     acc_zero(acc);
     if (first) return;
     const int lane = threadIdx.x & 63;
@@ -230,12 +231,12 @@ struct AddEpi {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int b = t.b0 + 16 * j + (lane & 15);
-        if (b < t.nb) acc[i][j] = load4(sum + size_t(b) * ld + a, na - a, true);
+        if (b < t.nb) acc[i][j] = load4(sum + blockIdx.y * split + size_t(b) * ld + a, na - a, true);
       }
     }
   }
   template <int FM, int FN>
-  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -244,7 +245,7 @@ struct AddEpi {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int b = t.b0 + 16 * j + (lane & 15);
-        if (b < t.nb) store4(sum + size_t(b) * ld + a, acc[i][j], na - a, true);
+        if (b < t.nb) store4(sum + blockIdx.y * split + size_t(b) * ld + a, acc[i][j], na - a, true);
       }
     }
   }
@@ -261,7 +262,7 @@ struct BaseLogits {
   int v0, na;
   bool vec;   // v0 and V keep four-value alignment
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
     acc_zero(acc);
     if (!U) return;
     const int lane = threadIdx.x & 63;
@@ -291,11 +292,11 @@ struct StatsEpi {
   long stat_ld;
   float* zlab;
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
     base.init(acc, t);
   }
   template <int FM, int FN>
-  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void* lds) const {
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void* lds) const {
     const int lane = threadIdx.x & 63;
     float2* part = static_cast<float2*>(lds);   // [WAVES_A][BN]
     const float ninf = -__builtin_huge_valf();
@@ -345,8 +346,8 @@ struct StatsEpi {
 
 // Gradient of the loss by the logits, of one piece of the vocabulary:
 // dz[b][a] = g (exp(z - lse) - [a is the label]), rounded to T because the
-// next products take it in T; b beyond the rows in use get 0 (they end the
-// contraction of the weight gradients).  dU, if asked for, gets the same.
+// next products take it in T.  Rows of dz behind the last one in use are left
+// alone; dU, if asked for, gets the same values.
 template <typename T>
 struct GradEpi {
   BaseLogits<T> base;
@@ -357,19 +358,19 @@ struct GradEpi {
   long dz_ld;
   T* dU;
   template <int FM, int FN>
-  __device__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
     base.init(acc, t);
   }
   template <int FM, int FN>
-  __device__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int b = t.b0 + 16 * j + (lane & 15);
-      const bool in = b < t.nb;
-      const int row = in ? base.row[b] : 0;
-      const int y = in ? label[row] - base.v0 : -1;
-      const float l = in ? lse[row] : 0.f, gb = in ? g[row] : 0.f;
+      if (b >= t.nb) continue;
+      const int row = base.row[b];
+      const int y = label[row] - base.v0;
+      const float l = lse[row], gb = g[row];
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int a = t.a0 + 16 * i + 4 * (lane >> 4);
@@ -377,11 +378,11 @@ struct GradEpi {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float p = exp_of<T>(acc[i][j][e] - l);
-          v[e] = in && a + e < base.na ? gb * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
+          v[e] = a + e < base.na ? gb * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
         }
         // the piece's width dz_ld is a multiple of the tile: every a of the tile is inside it
         store4(dz + size_t(b) * dz_ld + a, v, 4, true);
-        if (dU && in && a < base.na) store4(dU + size_t(row) * base.V + base.v0 + a, v, base.na - a, base.vec);
+        if (dU && a < base.na) store4(dU + size_t(row) * base.V + base.v0 + a, v, base.na - a, base.vec);
       }
     }
   }

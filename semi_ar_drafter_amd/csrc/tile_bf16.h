@@ -1,0 +1,387 @@
+// Matrix product of bf16 operands on v_mfma_f32_16x16x32_bf16, tiles staged
+// through LDS by direct-to-LDS loads.
+//
+// A step covers 64 of the contraction.  Each operand is stored with either
+// the contraction contiguous (kRows: one row per a) or the a axis contiguous
+// (kCols: one row per k), and is staged as it is stored:
+//   kRows  LDS [a][64 k], 128 bytes a row; a fragment is one ds_read_b128.
+//          The 16-byte chunk c of row a lies at place c ^ (a & 7), so the 16
+//          rows of a fragment read fall on all banks.
+//   kCols  LDS [64 k][a]; a fragment is two ds_read_b64_tr_b16, which
+//          transpose 4 k x 16 a on the way out.  32-byte pair p of row k lies
+//          at p ^ (k & 3) (in rows of four pairs or more), so the four rows of
+//          one read fall on all banks.
+// The exchange is made on the global side (each lane picks which chunk it
+// loads), because a direct-to-LDS load always writes lane after lane.
+//
+// Requirements, all met by the callers: bases 16-byte aligned; the b operand
+// rows of a multiple of 8 values, zero from K to the next multiple of 64
+// (kRows: the columns, kCols: the rows), so that whatever finite values the a
+// operand repeats there do not count.  The a operand either has rows of a
+// multiple of 8 values (direct loads), or any row length (ANY: loads to
+// registers at element alignment, then LDS).
+#pragma once
+#include "projection.h"
+
+namespace dspark {
+
+enum Layout2 { kRows = 0, kCols = 1 };
+constexpr int kStep = 64;
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) unsigned char lds_u8_t;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+}
+// lane j: 16 bytes from base + off (per lane) to lds + 16 j
+__device__ __forceinline__ void buffer_to_lds16(rsrc_t r, unsigned char* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+}
+#endif
+
+template <int N> __device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Tile shape: BM along a, BN along b, WA x WB waves, S stages in LDS.
+template <int BM_, int BN_, int WA_, int WB_, int S_>
+struct TileShape {
+  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_, S = S_;
+  static constexpr int waves = WA * WB, threads = 64 * waves;
+  static constexpr int FM = BM / WA / 16, FN = BN / WB / 16;
+  static constexpr int a_bytes = BM * kStep * 2, b_bytes = BN * kStep * 2;
+  static constexpr int stage = a_bytes + b_bytes, lds = S * stage;
+  static constexpr int la = a_bytes / 1024, lb = b_bytes / 1024;   // 1 KiB wave loads per step
+};
+
+// Bits of k that move the pairs of a kCols row of `rows` values.
+constexpr int pair_mask(int rows) { return rows >= 64 ? 3 : rows / 16 - 1; }
+
+// Number of wave loads of `n` that wave w of `waves` issues: a fixed count per
+// wave, so that waits can count them (surplus waves repeat the last one).
+constexpr int loads_per_wave(int n, int waves) { return (n + waves - 1) / waves; }
+
+// One operand's staging by one wave: per-lane byte offsets from the tile's
+// base, fixed over the steps.
+template <int LAYOUT, int ROWS, int LOADS, int WAVES>
+struct Stager {
+  uint32_t off[LOADS];
+
+  // first: the tile's first row along the operand's axis; n: its size; ld: row
+  // length in values; w: wave.
+  __device__ __forceinline__ void init(int first, int n, long ld, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int unit = min(w * LOADS + i, ROWS / 8 - 1);
+      if (LAYOUT == kRows) {
+        const int r = unit * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+        // rows behind the last one repeat it: their results are not stored
+        off[i] = uint32_t(min(r, n - 1 - first)) * uint32_t(ld * 2) + uint32_t(c) * 16;
+      } else {
+        constexpr int per = ROWS / 8;   // 16-byte chunks in a row of the tile
+        const int at = unit * 64 + lane, k = at / per, p = at % per;
+        const int c = p ^ ((k & pair_mask(ROWS)) << 1);
+        // chunks behind the last one repeat it
+        off[i] = uint32_t(k) * uint32_t(ld * 2) + uint32_t(min(c, (n - first + 7) / 8 - 1)) * 16;
+      }
+    }
+  }
+  __device__ __forceinline__ static int unit_of(int w, int i) { return min(w * LOADS + i, ROWS / 8 - 1); }
+
+  // The last step when K is no multiple of 64: chunks (kRows) or rows (kCols)
+  // behind K repeat the last one.  left: K minus the step's first k.
+  __device__ __forceinline__ uint32_t tail(int i, int w, int lane, long ld, int left) const {
+    if (LAYOUT == kRows) {
+      const int c = (lane & 7) ^ (lane >> 3), last = (left - 1) / 8;
+      return c > last ? off[i] - uint32_t(c - last) * 16 : off[i];
+    }
+    constexpr int per = ROWS / 8;
+    const int k = (unit_of(w, i) * 64 + lane) / per;
+    return k >= left ? off[i] - uint32_t(k - (left - 1)) * uint32_t(ld * 2) : off[i];
+  }
+};
+
+// 16 bytes at element alignment, not past `end`.
+__device__ __forceinline__ u32x4_t load_any(const bf16_t* p, const bf16_t* end) {
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (p + 8 <= end) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    bf16_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (p + i < end) e[i] = p[i];
+    __builtin_memcpy(&v, e, 16);
+  }
+  return v;
+}
+
+// Fragments of one 32-deep half step.
+template <int LAYOUT, int ROWS, int F>
+__device__ __forceinline__ void read_frags(bf16x8_t (&f)[F], const unsigned char* lds, int first, int half, int lane) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int q = lane >> 4, l = lane & 15;
+  if (LAYOUT == kRows) {
+    const unsigned char* p = lds + (first + l) * 128 + (((half * 4 + q) ^ (l & 7)) * 16);
+#pragma unroll
+    for (int i = 0; i < F; ++i) f[i] = *reinterpret_cast<const bf16x8_t*>(p + i * 2048);
+  } else {
+    const int s = l >> 2;
+    const unsigned char* row = lds + (half * 32 + q * 8 + s) * (ROWS * 2) + (l & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int pair = (first / 16 + i) ^ (s & pair_mask(ROWS));
+      const unsigned char* p = row + pair * 32;
+      s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+      s16x4_t hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ROWS * 2));
+      const s16x8_t both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      f[i] = __builtin_bit_cast(bf16x8_t, both);
+    }
+  }
+#endif
+}
+
+// Place of tile `id` of a grid of tiles_a x tiles_b: workgroups go round the
+// eight XCDs, so each XCD takes a contiguous run of tiles; inside a run, up to
+// eight tiles of b share their tile of a in the XCD's L2.
+__device__ __forceinline__ void tile_place(int id, int tiles_a, int tiles_b, int* ta, int* tb) {
+  const int n = tiles_a * tiles_b, q = n >> 3, r = n & 7, x = id & 7, at = id >> 3;
+  const int t = (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + at;
+  const int group = 8 * tiles_a, g = t / group, in = t - g * group;
+  const int wide = min(8, tiles_b - 8 * g);
+  *ta = in / wide;
+  *tb = 8 * g + in - *ta * wide;
+}
+
+// grid: x tiles, y splits of the contraction.  LA0, LA1: layout of the a
+// operand in the two parts of the contraction; LB of b.
+template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi>
+__global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> g, Epi epi, int na, int nb) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NA = loads_per_wave(Sh::la, Sh::waves), NB = loads_per_wave(Sh::lb, Sh::waves);
+  constexpr bool two = LA0 != LA1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tile_a, tile_b;
+  tile_place(blockIdx.x, (na + Sh::BM - 1) / Sh::BM, (nb + Sh::BN - 1) / Sh::BN, &tile_a, &tile_b);
+  const int a_first = tile_a * Sh::BM, b_first = tile_b * Sh::BN;
+  if (g.nb) nb = *g.nb;
+  if (b_first >= nb) return;   // all its rows are behind the last one in use
+  const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
+  const int T0 = (K0 + kStep - 1) / kStep, T = T0 + (K1 + kStep - 1) / kStep;
+  const int t_begin = int(long(T) * blockIdx.y / gridDim.y), t_end = int(long(T) * (blockIdx.y + 1) / gridDim.y);
+
+  TileAt at;
+  at.wave_a = wave / Sh::WB;
+  at.wave_b = wave % Sh::WB;
+  at.a0 = a_first + at.wave_a * (Sh::BM / Sh::WA);
+  at.b0 = b_first + at.wave_b * (Sh::BN / Sh::WB);
+  at.nb = nb;
+  at.tile_a = tile_a;
+
+  Stager<LA0, Sh::BM, NA, Sh::waves> sa0;
+  Stager<LA1, Sh::BM, NA, Sh::waves> sa1;
+  Stager<LB, Sh::BN, NB, Sh::waves> sb;
+  const long lda0 = LA0 == kRows ? g.A[0].sa : g.A[0].sk, lda1 = LA1 == kRows ? g.A[1].sa : g.A[1].sk;
+  const long ldb0 = LB == kRows ? g.B[0].sa : g.B[0].sk;
+  sa0.init(a_first, g.A[0].n, lda0, wave, lane);
+  sa1.init(a_first, g.A[1].n, lda1, wave, lane);
+  sb.init(b_first, g.B[0].n, ldb0, wave, lane);
+  const bf16_t* a0 = g.A[0].p + (LA0 == kRows ? long(a_first) * lda0 : long(a_first));
+  const bf16_t* a1 = g.A[1].p + (LA1 == kRows ? long(a_first) * lda1 : long(a_first));
+  const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(b_first) * ldb0 : long(b_first));
+  const bf16_t* b1 = g.B[1].p + (LB == kRows ? long(b_first) * ldb0 : long(b_first));   // both parts of b share ldb
+  u32x4_t held[ANY ? NA : 1];
+
+  auto issue = [&](int t) {
+    unsigned char* st = smem + (t % Sh::S) * Sh::stage;
+    const bool second = t >= T0;
+    const int k = (second ? t - T0 : t) * kStep;
+    {
+      const rsrc_t rb = make_rsrc((second ? b1 : b0) + (LB == kRows ? long(k) : long(k) * ldb0));
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        buffer_to_lds16(rb, st + Sh::a_bytes + sb.unit_of(wave, i) * 1024, sb.off[i]);
+    }
+    const int left = (second ? K1 : K0) - k;
+    if (ANY) {
+      if (!second) {
+        const bf16_t* p = a0 + (LA0 == kRows ? long(k) : long(k) * lda0);
+        const bf16_t* end = g.A[0].p + (LA0 == kRows ? long(g.A[0].n - 1) * lda0 + K0 : long(K0 - 1) * lda0 + g.A[0].n);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+          const uint32_t o = left < kStep ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
+          held[i] = load_any(reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(p) + o), end);
+          if (LA0 == kRows && left < kStep) {   // values behind K belong to the next row
+            const int c = (lane & 7) ^ (lane >> 3), keep = left - min(c, (left - 1) / 8) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e >= keep) held[i][e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+        return;
+      }
+    }
+    if (!two || !second) {
+      const rsrc_t ra = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * (second ? lda1 : lda0)));
+      if (left < kStep) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+          buffer_to_lds16(ra, st + sa0.unit_of(wave, i) * 1024,
+                          second ? sa1.tail(i, wave, lane, lda1, left) : sa0.tail(i, wave, lane, lda0, left));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+          buffer_to_lds16(ra, st + sa0.unit_of(wave, i) * 1024, second ? sa1.off[i] : sa0.off[i]);
+      }
+    } else {
+      const rsrc_t ra = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
+      if (left < kStep) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+          buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.tail(i, wave, lane, lda1, left));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.off[i]);
+      }
+    }
+  };
+  // ANY: what issue() holds in registers goes to LDS
+  auto put = [&](int t) {
+    if (!ANY || t >= T0) return;
+    unsigned char* st = smem + (t % Sh::S) * Sh::stage;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      *reinterpret_cast<u32x4_t*>(st + sa0.unit_of(wave, i) * 1024 + lane * 16) = held[i];
+  };
+
+  f32x4_t acc[Sh::FM][Sh::FN];
+  // the first stages are on their way while the accumulators are set up
+#pragma unroll
+  for (int s = 0; s < Sh::S - 1; ++s)
+    if (t_begin + s < t_end) {
+      issue(t_begin + s);
+      put(t_begin + s);
+    }
+  epi.init(acc, at);
+
+  constexpr int per_step = NA + NB;
+  for (int t = t_begin; t < t_end; ++t) {
+    // this wave's loads of step t have landed (later steps may be on their way)
+    if (ANY || Sh::S == 2 || t_end - t - 1 < Sh::S - 2)
+      wait_vm<0>();
+    else
+      wait_vm<per_step*(Sh::S - 2)>();
+    lds_wait();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + Sh::S - 1 < t_end) issue(t + Sh::S - 1);
+    const unsigned char* st = smem + (t % Sh::S) * Sh::stage;
+    const int wa = at.wave_a * (Sh::BM / Sh::WA), wb = at.wave_b * (Sh::BN / Sh::WB);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      bf16x8_t a[Sh::FM], b[Sh::FN];
+      read_frags<LB, Sh::BN>(b, st + Sh::a_bytes, wb, half, lane);
+      if (two && t >= T0)
+        read_frags<LA1, Sh::BM>(a, st, wa, half, lane);
+      else
+        read_frags<LA0, Sh::BM>(a, st, wa, half, lane);
+#pragma unroll
+      for (int i = 0; i < Sh::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < Sh::FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    }
+    if (ANY && t + 1 < t_end) put(t + 1);
+  }
+  __syncthreads();
+  epi.done(acc, at, smem);
+#endif
+}
+
+template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi>
+hipError_t launch_tile_bf16(const Product<bf16_t>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
+  static_assert(!ANY || Sh::S == 2, "register staging is double buffered");
+  if (na <= 0 || nb <= 0) return hipSuccess;
+  const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
+  auto* kernel = &tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, Sh::lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads),
+                     Sh::lds, stream, g, epi, na, nb);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Choice of the tile
+// ---------------------------------------------------------------------------
+// Few rows: bound by reading the a operand once, so narrow tiles with a deep
+// ring, several workgroups per compute unit.  Many rows: 256 x 256, where one
+// step's 128 MFMAs per SIMD cover the loads of the next.
+using Tile16 = TileShape<128, 16, 4, 1, 4>;
+using Tile32 = TileShape<128, 32, 4, 1, 3>;
+using Tile64 = TileShape<128, 64, 2, 2, 3>;
+using Tile128 = TileShape<128, 128, 2, 2, 2>;
+using Tile256 = TileShape<256, 256, 2, 4, 2>;
+using Tile16Any = TileShape<128, 16, 4, 1, 2>;
+using Tile32Any = TileShape<128, 32, 4, 1, 2>;
+using Tile64Any = TileShape<128, 64, 2, 2, 2>;
+
+constexpr int kComputeUnits = 256;
+
+inline int tiles_of(int na, int nb, int bm, int bn) {
+  const long n = long((na + bm - 1) / bm) * ((nb + bn - 1) / bn);
+  return n > 1 << 30 ? 1 << 30 : int(n);
+}
+// 0..4: index of the tile for na x nb outputs.
+inline int tile_choice(int na, int nb) {
+  if (nb <= 16) return 0;
+  if (nb <= 32) return 1;
+  if (nb <= 64) return 2;
+  return tiles_of(na, nb, 256, 256) >= 3 * kComputeUnits / 4 ? 4 : 3;
+}
+inline int tile_bm(int choice) { return choice == 4 ? 256 : 128; }
+inline int tile_bn(int choice) { return choice == 4 ? 256 : choice == 3 ? 128 : 16 << choice; }
+
+// Splits of a contraction of K values so that about two workgroups per
+// compute unit have work, each with at least four steps.
+inline int splits_for(int na, int nb, long K) {
+  const int c = tile_choice(na, nb);
+  const int tiles = tiles_of(na, nb, tile_bm(c), tile_bn(c));
+  const long steps = (K + kStep - 1) / kStep;
+  long s = 2 * kComputeUnits / tiles;
+  if (s > steps / 4) s = steps / 4;
+  return s < 1 ? 1 : s > 64 ? 64 : int(s);
+}
+
+// MakeEpi<Shape>()(…) gives the epilogue for a tile shape (its statistics
+// depend on the shape).
+template <int LA0, int LA1, int LB, bool ANY, class MakeEpi>
+hipError_t launch_bf16(const Product<bf16_t>& g, const MakeEpi& make, int na, int nb, int splits, hipStream_t stream) {
+  if constexpr (ANY) {
+    switch (tile_choice(na, nb)) {
+      case 0: return launch_tile_bf16<Tile16Any, LA0, LA1, LB, true>(g, make(Tile16Any()), na, nb, splits, stream);
+      case 1: return launch_tile_bf16<Tile32Any, LA0, LA1, LB, true>(g, make(Tile32Any()), na, nb, splits, stream);
+      case 2: return launch_tile_bf16<Tile64Any, LA0, LA1, LB, true>(g, make(Tile64Any()), na, nb, splits, stream);
+      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, true>(g, make(Tile128()), na, nb, splits, stream);
+      default: return launch_tile_bf16<Tile256, LA0, LA1, LB, true>(g, make(Tile256()), na, nb, splits, stream);
+    }
+  } else {
+    switch (tile_choice(na, nb)) {
+      case 0: return launch_tile_bf16<Tile16, LA0, LA1, LB, false>(g, make(Tile16()), na, nb, splits, stream);
+      case 1: return launch_tile_bf16<Tile32, LA0, LA1, LB, false>(g, make(Tile32()), na, nb, splits, stream);
+      case 2: return launch_tile_bf16<Tile64, LA0, LA1, LB, false>(g, make(Tile64()), na, nb, splits, stream);
+      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, splits, stream);
+      default: return launch_tile_bf16<Tile256, LA0, LA1, LB, false>(g, make(Tile256()), na, nb, splits, stream);
+    }
+  }
+}
+
+}  // namespace dspark

@@ -23,9 +23,7 @@ __global__ __launch_bounds__(256) void tile_f32_kernel(Product<T> g, Epi epi, in
   if (g.nb) nb = *g.nb;
   const int tile_a = blockIdx.x / tiles_b, tile_b = blockIdx.x % tiles_b;
   const int a_first = tile_a * kTileF32, b_first = tile_b * kTileF32;
-  // a tile whose rows are all behind the last one in use; the rows up to the
-  // next multiple of 64 still get their zeros from GradEpi
-  if (b_first >= ((nb + 63) & ~63)) return;
+  if (b_first >= nb) return;   // all its rows are behind the last one in use
   TileAt t;
   t.wave_a = wave >> 1;
   t.wave_b = wave & 1;
