@@ -69,6 +69,7 @@ __global__ __launch_bounds__(256) void join_splits_kernel(int M, int N, int spli
   if (at >= long(M) * quads) return;
   const int b = int(at / quads), a = int(at % quads) * 4, n = N - a;
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
   for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + (size_t(s) * M + b) * ld + a);
   epi.finish(v, b, a, n);
 }
@@ -79,8 +80,8 @@ inline long dz_stride(int N) { return up64(N); }
 inline int dz_chunks(int M) { return (M + kDzRows - 1) / kDzRows; }
 
 // Splits of a bf16 product's contraction into partial sums [split][rows][up64(na)].
-inline size_t split_bytes(int na, int nb, long K) {
-  const int s = splits_for(na, nb, K);
+inline size_t split_bytes(int na, int nb, long K, bool any) {
+  const int s = splits_for(na, nb, K, any);
   return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
 }
 
@@ -102,7 +103,7 @@ LinearEpi<T> linear_epi(const LinearArgs& a) {
 template <int LA, int LB>
 hipError_t product(const Product<bf16_t>& g, bool any, const LinearEpi<bf16_t>& epi, int na, int nb, float* part,
                    hipStream_t stream) {
-  const int splits = splits_for(na, nb, g.K[0]);
+  const int splits = splits_for(na, nb, g.K[0], any);
   hipError_t e;
   if (splits == 1) {
     auto make = [&](auto) { return epi; };
@@ -245,13 +246,13 @@ hipError_t linear_backward_bf16(const LinearBackwardArgs& a, hipStream_t stream)
 
 size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
   if (!bf16) return 0;
-  return (K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K);
+  return (K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K, K % 8 != 0);
 }
 
 size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16) {
   const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4));
   if (!bf16 || M == 0 || K == 0) return dz;
-  const size_t dx = split_bytes(K, M, N), dw = split_bytes(K, N, M);
+  const size_t dx = split_bytes(K, M, N, K % 8 != 0), dw = split_bytes(K, N, M, K % 8 != 0);
   return dz + (dx > dw ? dx : dw);
 }
 

@@ -63,12 +63,13 @@ __global__ __launch_bounds__(1024) void compact_kernel(int N, int V, const int* 
 }
 
 // X[i] = [h[row[i]] | 0 | W1[prev[row[i]]] | 0]; rows from count up to the
-// next multiple of 64 are zero.  One workgroup per row.
+// next multiple of 64 are zero.  token[i] = prev[row[i]], clamped.  One
+// workgroup per row.
 template <typename T>
 __global__ __launch_bounds__(256) void gather_kernel(int V, int d, int dp, int r, int rp, const int* __restrict__ count,
                                                      const int* __restrict__ row, const int* __restrict__ prev,
                                                      const T* __restrict__ h, const T* __restrict__ W1,
-                                                     T* __restrict__ X) {
+                                                     T* __restrict__ X, int* __restrict__ token) {
   const int i = blockIdx.x, n = *count;
   if (i >= ((n + 63) & ~63)) return;
   T* x = X + size_t(i) * (dp + rp);
@@ -81,34 +82,44 @@ __global__ __launch_bounds__(256) void gather_kernel(int V, int d, int dp, int r
   }
   if (rp) {
     const int t = used ? min(max(prev[src], 0), V - 1) : 0;
+    if (used && threadIdx.x == 0) token[i] = t;
     const T* wr = W1 + size_t(t) * r;
     for (int c = threadIdx.x; c < rp; c += 256) x[dp + c] = used && c < r ? wr[c] : zero;
   }
 }
 
-// lse and nll of every row from the tiles' statistics, a fixed order: 16
-// lanes per row, 16 rows per workgroup.
+// lse and nll of every row from the tiles' statistics, in a fixed order: LANES
+// threads per row, each taking every LANES-th tile, then joined pairwise.
+template <int LANES>
 __global__ __launch_bounds__(256) void join_kernel(int N, int tiles, const int* __restrict__ place,
                                                    const float2* __restrict__ stat, long stat_ld,
                                                    const float* __restrict__ zlab, float* __restrict__ nll,
                                                    float* __restrict__ lse) {
-  const int n = blockIdx.x * 16 + (threadIdx.x >> 4), first = threadIdx.x & 15;
+  constexpr int ROWS = 256 / LANES;   // neighbouring threads take neighbouring rows
+  __shared__ float2 part[256];
+  const int n = blockIdx.x * ROWS + threadIdx.x % ROWS, first = threadIdx.x / ROWS;
   const int i = n < N ? place[n] : -1;
   const float ninf = -__builtin_huge_valf();
   float m = ninf, s = 0.f;
-  if (i >= 0)
-    for (int t = first; t < tiles; t += 16) {
+  if (i >= 0) {
+#pragma unroll 4
+    for (int t = first; t < tiles; t += LANES) {
       const float2 q = stat[size_t(t) * stat_ld + i];
       const float top = fmaxf(m, q.x), ref = top == ninf ? 0.f : top;
       s = s * __expf(m - ref) + q.y * __expf(q.x - ref);
       m = top;
     }
-#pragma unroll
-  for (int x = 1; x < 16; x *= 2) {
-    const float om = __shfl_xor(m, x, 64), os = __shfl_xor(s, x, 64);
-    const float top = fmaxf(m, om), ref = top == ninf ? 0.f : top;
-    s = s * __expf(m - ref) + os * __expf(om - ref);
-    m = top;
+  }
+  part[threadIdx.x] = make_float2(m, s);
+  for (int x = LANES / 2; x >= 1; x /= 2) {
+    __syncthreads();
+    if (first < x) {
+      const float2 o = part[threadIdx.x + x * ROWS];
+      const float top = fmaxf(m, o.x), ref = top == ninf ? 0.f : top;
+      s = s * __expf(m - ref) + o.y * __expf(o.x - ref);
+      m = top;
+      part[threadIdx.x] = make_float2(m, s);
+    }
   }
   if (n < N && first == 0) {
     // nll from the maximum, not from the rounded lse: where the label has
@@ -149,40 +160,81 @@ __global__ __launch_bounds__(256) void dh_kernel(int d, long ld, int splits, lon
   const int n = blockIdx.x, i = place[n];
   for (int c = threadIdx.x; c < d; c += 256) {
     float v = 0.f;
-    if (i >= 0)
+    if (i >= 0) {
+#pragma unroll 8
       for (int s = 0; s < splits; ++s) v += dX[size_t(s) * split + size_t(i) * ld + c];
+    }
     dh[size_t(n) * d + c] = from_f32<T>(v);
   }
 }
 
-// dW1[t] = sum of dE over the rows whose previous token is t, in row order,
-// each row's splits in order.  One wave per row; the first row of a token
-// does its sum (the table was zeroed before).
-template <typename T>
-__global__ __launch_bounds__(256) void dw1_kernel(int V, int r, long ld, int splits, long split,
-                                                  const int* __restrict__ count, const int* __restrict__ row,
-                                                  const int* __restrict__ prev, const float* __restrict__ dE,
-                                                  T* __restrict__ dW1) {
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, n = *count;
-  if (i >= n) return;
-  const int t = min(max(prev[row[i]], 0), V - 1);
-  for (int j = 0; j < i; j += 64) {
-    const bool same = j + lane < i && min(max(prev[row[j + lane]], 0), V - 1) == t;
-    if (__any(same)) return;
+// dE of every row in use: its splits, in order, into the first one's place.
+__global__ __launch_bounds__(256) void join_e_kernel(long ld, int splits, long split, const int* __restrict__ count,
+                                                     float* __restrict__ dE) {
+  const int i = blockIdx.x;
+  if (i >= *count) return;
+  for (int c = threadIdx.x; c < ld; c += 256) {
+    float v = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) v += dE[size_t(s) * split + size_t(i) * ld + c];
+    dE[size_t(i) * ld + c] = v;
   }
-  for (int c0 = 0; c0 < r; c0 += 64) {
-    const int c = c0 + lane;
+}
+
+// dW1[t] = sum of dE over the rows whose previous token is t.  One workgroup
+// per row; the token's first row does the sum (the table was zeroed before).
+// Its rows are listed in LDS, kSegment rows at a time, and added in four
+// interleaved sums (a frequent token has hundreds of rows: their loads are
+// all independent), joined in order.
+constexpr int kSegment = 2048;
+template <typename T>
+__global__ __launch_bounds__(1024) void dw1_kernel(int r, long ld, const int* __restrict__ count,
+                                                   const int* __restrict__ token, const float* __restrict__ dE,
+                                                   T* __restrict__ dW1) {
+  __shared__ int list[kSegment];
+  __shared__ int found, waves[16];
+  __shared__ float sums[1024];
+  const int i = blockIdx.x, n = *count, tid = threadIdx.x, lane = tid & 63;
+  if (i >= n) return;
+  const int t = token[i];
+  if (tid == 0) found = 0;
+  __syncthreads();
+  bool earlier = false;
+  for (int j = tid; j < i; j += 1024) earlier |= token[j] == t;
+  if (earlier) found = 1;
+  __syncthreads();
+  if (found) return;
+  const int c = tid & 255, phase = tid >> 8;
+  for (int c0 = 0; c0 < r; c0 += 256) {
     float s = 0.f;
-    for (int j = i; j < n; j += 64) {
-      uint64_t mask = __ballot(j + lane < n && min(max(prev[row[j + lane]], 0), V - 1) == t);
-      while (mask) {
-        const int b = __builtin_ctzll(mask);
-        mask &= mask - 1;
-        if (c < r)
-          for (int q = 0; q < splits; ++q) s += dE[size_t(q) * split + size_t(j + b) * ld + c];
+    for (int j0 = i; j0 < n; j0 += kSegment) {
+      int len = 0;   // the segment's rows with this token, in order
+      for (int half = 0; half < kSegment / 1024; ++half) {
+        const int j = j0 + half * 1024 + tid;
+        const bool same = j < n && token[j] == t;
+        const uint64_t mask = __ballot(same);
+        __syncthreads();
+        if (lane == 0) waves[tid >> 6] = __builtin_popcountll(mask);
+        __syncthreads();
+        int before = len;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+          if (w < (tid >> 6)) before += waves[w];
+          len += waves[w];
+        }
+        if (same) list[before + __builtin_popcountll(mask & ((1ull << lane) - 1))] = j;
+      }
+      __syncthreads();
+      if (c0 + c < r) {
+#pragma unroll 4
+        for (int q = phase; q < len; q += 4) s += dE[size_t(list[q]) * ld + c0 + c];
       }
     }
-    if (c < r) dW1[size_t(t) * r + c] = from_f32<T>(s);
+    __syncthreads();
+    sums[tid] = s;
+    __syncthreads();
+    if (tid < 256 && c0 + c < r)
+      dW1[size_t(t) * r + c0 + c] = from_f32<T>((sums[c] + sums[256 + c]) + (sums[512 + c] + sums[768 + c]));
   }
 }
 
@@ -197,7 +249,7 @@ __global__ __launch_bounds__(256) void pad_w2_kernel(int V, long ld, const bf16_
 
 // What the forward and the backward call carve out of the workspace.
 struct Layout {
-  size_t row, place, X, W2, stat, zlab, dz, dXh, dXe, total;
+  size_t row, place, token, X, W2, stat, zlab, dz, dXh, dXe, total;
   int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
   long w2_ld;                // row length of W2 as the products read it
   int splits_h, splits_e;    // of the contraction over a piece's tokens
@@ -217,6 +269,7 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
   };
   L.row = take(size_t(N) * 4);
   L.place = take(size_t(N) * 4);
+  L.token = take(size_t(N) * 4);
   L.X = take(size_t(L.rows) * (L.dp + L.rp) * elem);
   L.w2_ld = V;
   if (bf16 && r && V % 8) {
@@ -231,8 +284,8 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     const size_t most = kPieceBytes / (size_t(L.rows) * elem);
     const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
     L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
-    L.splits_h = bf16 && d && N ? splits_for(d, N, L.width) : 1;
-    L.splits_e = bf16 && r && N ? splits_for(r, N, L.width) : 1;
+    L.splits_h = bf16 && d && N ? splits_for(d, N, L.width, d % 8 != 0) : 1;
+    L.splits_e = bf16 && r && N ? splits_for(r, N, L.width, false) : 1;
     L.dz = take(size_t(L.rows) * L.width * elem);
     L.dXh = take(size_t(L.splits_h) * L.rows * L.dp * 4);
     L.dXe = take(size_t(L.splits_e) * L.rows * L.rp * 4);
@@ -244,7 +297,7 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
 template <typename T>
 struct Parts {
   Layout L;
-  int *count, *row, *place;
+  int *count, *row, *place, *token;
   T* X;
   const T* W2;
   int kx;
@@ -257,13 +310,14 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t st
   p.count = reinterpret_cast<int*>(ws);
   p.row = reinterpret_cast<int*>(ws + L.row);
   p.place = reinterpret_cast<int*>(ws + L.place);
+  p.token = reinterpret_cast<int*>(ws + L.token);
   p.X = reinterpret_cast<T*>(ws + L.X);
   p.W2 = static_cast<const T*>(a.W2);
   p.kx = L.dp + L.rp;
   hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
   if (p.kx && a.N)
     hipLaunchKernelGGL((gather_kernel<T>), dim3(unsigned(up(a.N, 64))), dim3(256), 0, stream, a.V, a.d, L.dp, a.r,
-                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X);
+                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X, p.token);
   if (L.W2) {
     p.W2 = reinterpret_cast<T*>(ws + L.W2);
     hipLaunchKernelGGL(pad_w2_kernel, dim3(unsigned((L.w2_ld + 1023) / 1024), unsigned(a.r)), dim3(256), 0, stream,
@@ -329,8 +383,15 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
   };
   if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N, 1, stream)) != hipSuccess)
     return e;
-  hipLaunchKernelGGL(join_kernel, dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, stream, a.N, (a.V + bm - 1) / bm,
-                     p.place, stat, long(a.N), zlab, a.nll, a.lse);
+  // few rows: all threads of a workgroup on one row's tiles; many: neighbours
+  // in a wave read neighbouring rows
+  const int tiles = (a.V + bm - 1) / bm;
+  if (a.N <= 512)
+    hipLaunchKernelGGL((join_kernel<256>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.N, tiles, p.place, stat,
+                       long(a.N), zlab, a.nll, a.lse);
+  else
+    hipLaunchKernelGGL((join_kernel<16>), dim3(unsigned((a.N + 15) / 16)), dim3(256), 0, stream, a.N, tiles, p.place,
+                       stat, long(a.N), zlab, a.nll, a.lse);
   return hipGetLastError();
 }
 
@@ -400,9 +461,13 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
                        p.place, dXh, static_cast<T*>(a.dh));
   if (a.dW1) {
     hipLaunchKernelGGL((zero_kernel<T>), dim3(2048), dim3(256), 0, stream, size_t(a.V) * a.r, static_cast<T*>(a.dW1));
-    if (a.N)
-      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned((a.N + 3) / 4)), dim3(256), 0, stream, a.V, a.r, long(L.rp),
-                         L.splits_e, split_e, p.count, p.row, a.prev, dXe, static_cast<T*>(a.dW1));
+    if (a.N) {
+      if (L.splits_e > 1)
+        hipLaunchKernelGGL(join_e_kernel, dim3(unsigned(a.N)), dim3(256), 0, stream, long(L.rp), L.splits_e, split_e,
+                           p.count, dXe);
+      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned(a.N)), dim3(1024), 0, stream, a.r, long(L.rp), p.count,
+                         p.token, dXe, static_cast<T*>(a.dW1));
+    }
   }
   return hipGetLastError();
 }

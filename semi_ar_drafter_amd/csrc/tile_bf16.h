@@ -1,16 +1,16 @@
 // Matrix product of bf16 operands on v_mfma_f32_16x16x32_bf16, tiles staged
 // through LDS by direct-to-LDS loads.
 //
-// A step covers 64 of the contraction.  Each operand is stored with either
-// the contraction contiguous (kRows: one row per a) or the a axis contiguous
-// (kCols: one row per k), and is staged as it is stored:
-//   kRows  LDS [a][64 k], 128 bytes a row; a fragment is one ds_read_b128.
-//          The 16-byte chunk c of row a lies at place c ^ (a & 7), so the 16
-//          rows of a fragment read fall on all banks.
-//   kCols  LDS [64 k][a]; a fragment is two ds_read_b64_tr_b16, which
-//          transpose 4 k x 16 a on the way out.  32-byte pair p of row k lies
-//          at p ^ (k & 3) (in rows of four pairs or more), so the four rows of
-//          one read fall on all banks.
+// A step covers K = 64 or 32 of the contraction.  Each operand is stored with
+// either the contraction contiguous (kRows: one row per a) or the a axis
+// contiguous (kCols: one row per k), and is staged as it is stored:
+//   kRows  LDS [a][K]; a fragment is one ds_read_b128.  16-byte chunk c of row
+//          a lies at place c ^ (a & 7) (K = 64) or c ^ (a / 4 & 3) (K = 32), so
+//          that any 16 rows of one chunk fall on all 64 banks.
+//   kCols  LDS [K][a]; a fragment is two ds_read_b64_tr_b16, which transpose
+//          4 k x 16 a on the way out.  32-byte pair p of row k lies at p ^
+//          pair_turn(k), so that the eight rows that half a wave reads (k to
+//          k + 3 and k + 8 to k + 11) fall on all banks.
 // The exchange is made on the global side (each lane picks which chunk it
 // loads), because a direct-to-LDS load always writes lane after lane.
 //
@@ -26,7 +26,7 @@
 namespace dspark {
 
 enum Layout2 { kRows = 0, kCols = 1 };
-constexpr int kStep = 64;
+constexpr int kStep = 64;   // both operands' padding along the contraction
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -47,19 +47,27 @@ template <int N> __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Tile shape: BM along a, BN along b, WA x WB waves, S stages in LDS.
-template <int BM_, int BN_, int WA_, int WB_, int S_>
+// Tile shape: BM along a, BN along b, WA x WB waves, steps of K, S of them in
+// LDS.
+template <int BM_, int BN_, int WA_, int WB_, int K_, int S_>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_, K = K_, S = S_;
   static constexpr int waves = WA * WB, threads = 64 * waves;
-  static constexpr int FM = BM / WA / 16, FN = BN / WB / 16;
-  static constexpr int a_bytes = BM * kStep * 2, b_bytes = BN * kStep * 2;
+  static constexpr int FM = BM / WA / 16, FN = BN / WB / 16, FK = K / 32;
+  static constexpr int a_bytes = BM * K * 2, b_bytes = BN * K * 2;
   static constexpr int stage = a_bytes + b_bytes, lds = S * stage;
   static constexpr int la = a_bytes / 1024, lb = b_bytes / 1024;   // 1 KiB wave loads per step
 };
 
-// Bits of k that move the pairs of a kCols row of `rows` values.
-constexpr int pair_mask(int rows) { return rows >= 64 ? 3 : rows / 16 - 1; }
+// Where the pairs of row k of a kCols tile of `rows` values are turned: bank
+// = (32-byte pair of the row + rows / 16 * k) mod 8, and k, k + 1, k + 2,
+// k + 3, k + 8, .. k + 11 have to differ (as far as the row has pairs).
+__device__ __forceinline__ constexpr int pair_turn(int rows, int k) {
+  return rows >= 128 ? (k & 3) | ((k >> 3 & 1) << 2) : rows == 64 ? (k >> 1 & 1) | ((k >> 3 & 1) << 1)
+         : rows == 32 ? k >> 3 & 1 : 0;
+}
+// Turn of the chunks of row a of a kRows tile.
+__device__ __forceinline__ constexpr int chunk_turn(int K, int a) { return K == 64 ? a & 7 : a >> 2 & 3; }
 
 // Number of wave loads of `n` that wave w of `waves` issues: a fixed count per
 // wave, so that waits can count them (surplus waves repeat the last one).
@@ -67,43 +75,55 @@ constexpr int loads_per_wave(int n, int waves) { return (n + waves - 1) / waves;
 
 // One operand's staging by one wave: per-lane byte offsets from the tile's
 // base, fixed over the steps.
-template <int LAYOUT, int ROWS, int LOADS, int WAVES>
+template <int LAYOUT, int ROWS, int K, int LOADS>
 struct Stager {
+  static constexpr int units = ROWS * K / 512;   // 1 KiB each
+  static constexpr int chunks = LAYOUT == kRows ? K / 8 : ROWS / 8;   // in a row of LDS
   uint32_t off[LOADS];
+
+  __device__ __forceinline__ static int unit_of(int w, int i) { return min(w * LOADS + i, units - 1); }
+  // the chunk of its row that a lane loads in any unit (kRows)
+  __device__ __forceinline__ static int chunk_of(int lane) {
+    return (lane % chunks) ^ chunk_turn(K, lane / chunks);
+  }
 
   // first: the tile's first row along the operand's axis; n: its size; ld: row
   // length in values; w: wave.
   __device__ __forceinline__ void init(int first, int n, long ld, int w, int lane) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int unit = min(w * LOADS + i, ROWS / 8 - 1);
+      const int row = (unit_of(w, i) * 64 + lane) / chunks;
       if (LAYOUT == kRows) {
-        const int r = unit * 8 + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
         // rows behind the last one repeat it: their results are not stored
-        off[i] = uint32_t(min(r, n - 1 - first)) * uint32_t(ld * 2) + uint32_t(c) * 16;
+        off[i] = uint32_t(min(row, n - 1 - first)) * uint32_t(ld * 2) + uint32_t(chunk_of(lane)) * 16;
       } else {
-        constexpr int per = ROWS / 8;   // 16-byte chunks in a row of the tile
-        const int at = unit * 64 + lane, k = at / per, p = at % per;
-        const int c = p ^ ((k & pair_mask(ROWS)) << 1);
+        const int c = (unit_of(w, i) * 64 + lane) % chunks ^ (pair_turn(ROWS, row) << 1);
         // chunks behind the last one repeat it
-        off[i] = uint32_t(k) * uint32_t(ld * 2) + uint32_t(min(c, (n - first + 7) / 8 - 1)) * 16;
+        off[i] = uint32_t(row) * uint32_t(ld * 2) + uint32_t(min(c, (n - first + 7) / 8 - 1)) * 16;
       }
     }
   }
-  __device__ __forceinline__ static int unit_of(int w, int i) { return min(w * LOADS + i, ROWS / 8 - 1); }
 
-  // The last step when K is no multiple of 64: chunks (kRows) or rows (kCols)
-  // behind K repeat the last one.  left: K minus the step's first k.
+  // The last step when K is no divisor of the contraction: chunks (kRows) or
+  // rows (kCols) behind its end repeat the last one.  left: what is left of it.
   __device__ __forceinline__ uint32_t tail(int i, int w, int lane, long ld, int left) const {
     if (LAYOUT == kRows) {
-      const int c = (lane & 7) ^ (lane >> 3), last = (left - 1) / 8;
+      const int c = chunk_of(lane), last = (left - 1) / 8;
       return c > last ? off[i] - uint32_t(c - last) * 16 : off[i];
     }
-    constexpr int per = ROWS / 8;
-    const int k = (unit_of(w, i) * 64 + lane) / per;
+    const int k = (unit_of(w, i) * 64 + lane) / chunks;
     return k >= left ? off[i] - uint32_t(k - (left - 1)) * uint32_t(ld * 2) : off[i];
   }
 };
+
+// What every wave has waited for is visible to all behind it.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
 
 // 16 bytes at element alignment, not past `end`.
 __device__ __forceinline__ u32x4_t load_any(const bf16_t* p, const bf16_t* end) {
@@ -120,21 +140,21 @@ __device__ __forceinline__ u32x4_t load_any(const bf16_t* p, const bf16_t* end) 
   return v;
 }
 
-// Fragments of one 32-deep half step.
-template <int LAYOUT, int ROWS, int F>
+// Fragments of 32 of a step's K, from `half` * 32 on.
+template <int LAYOUT, int ROWS, int K, int F>
 __device__ __forceinline__ void read_frags(bf16x8_t (&f)[F], const unsigned char* lds, int first, int half, int lane) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int q = lane >> 4, l = lane & 15;
   if (LAYOUT == kRows) {
-    const unsigned char* p = lds + (first + l) * 128 + (((half * 4 + q) ^ (l & 7)) * 16);
+    const unsigned char* p = lds + (first + l) * (K * 2) + (((half * 4 + q) ^ chunk_turn(K, l)) * 16);
 #pragma unroll
-    for (int i = 0; i < F; ++i) f[i] = *reinterpret_cast<const bf16x8_t*>(p + i * 2048);
+    for (int i = 0; i < F; ++i) f[i] = *reinterpret_cast<const bf16x8_t*>(p + i * 32 * K);
   } else {
-    const int s = l >> 2;
-    const unsigned char* row = lds + (half * 32 + q * 8 + s) * (ROWS * 2) + (l & 3) * 8;
+    const int k = half * 32 + q * 8 + (l >> 2);   // and k + 4, which turns the same way
+    const unsigned char* row = lds + k * (ROWS * 2) + (l & 3) * 8;
 #pragma unroll
     for (int i = 0; i < F; ++i) {
-      const int pair = (first / 16 + i) ^ (s & pair_mask(ROWS));
+      const int pair = (first / 16 + i) ^ pair_turn(ROWS, k);
       const unsigned char* p = row + pair * 32;
       s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
       s16x4_t hi =
@@ -173,7 +193,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   if (g.nb) nb = *g.nb;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
   const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
-  const int T0 = (K0 + kStep - 1) / kStep, T = T0 + (K1 + kStep - 1) / kStep;
+  const int T0 = (K0 + Sh::K - 1) / Sh::K, T = T0 + (K1 + Sh::K - 1) / Sh::K;
   const int t_begin = int(long(T) * blockIdx.y / gridDim.y), t_end = int(long(T) * (blockIdx.y + 1) / gridDim.y);
 
   TileAt at;
@@ -184,9 +204,9 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   at.nb = nb;
   at.tile_a = tile_a;
 
-  Stager<LA0, Sh::BM, NA, Sh::waves> sa0;
-  Stager<LA1, Sh::BM, NA, Sh::waves> sa1;
-  Stager<LB, Sh::BN, NB, Sh::waves> sb;
+  Stager<LA0, Sh::BM, Sh::K, NA> sa0;
+  Stager<LA1, Sh::BM, Sh::K, NA> sa1;
+  Stager<LB, Sh::BN, Sh::K, NB> sb;
   const long lda0 = LA0 == kRows ? g.A[0].sa : g.A[0].sk, lda1 = LA1 == kRows ? g.A[1].sa : g.A[1].sk;
   const long ldb0 = LB == kRows ? g.B[0].sa : g.B[0].sk;
   sa0.init(a_first, g.A[0].n, lda0, wave, lane);
@@ -198,10 +218,11 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   const bf16_t* b1 = g.B[1].p + (LB == kRows ? long(b_first) * ldb0 : long(b_first));   // both parts of b share ldb
   u32x4_t held[ANY ? NA : 1];
 
+  // sends off the loads of step t
   auto issue = [&](int t) {
     unsigned char* st = smem + (t % Sh::S) * Sh::stage;
     const bool second = t >= T0;
-    const int k = (second ? t - T0 : t) * kStep;
+    const int k = (second ? t - T0 : t) * Sh::K;
     {
       const rsrc_t rb = make_rsrc((second ? b1 : b0) + (LB == kRows ? long(k) : long(k) * ldb0));
 #pragma unroll
@@ -215,10 +236,10 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
         const bf16_t* end = g.A[0].p + (LA0 == kRows ? long(g.A[0].n - 1) * lda0 + K0 : long(K0 - 1) * lda0 + g.A[0].n);
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
-          const uint32_t o = left < kStep ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
+          const uint32_t o = left < Sh::K ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
           held[i] = load_any(reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(p) + o), end);
-          if (LA0 == kRows && left < kStep) {   // values behind K belong to the next row
-            const int c = (lane & 7) ^ (lane >> 3), keep = left - min(c, (left - 1) / 8) * 8;
+          if (LA0 == kRows && left < Sh::K) {   // values behind K belong to the next row
+            const int keep = left - min(sa0.chunk_of(lane), (left - 1) / 8) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (e >= keep) held[i][e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
@@ -229,7 +250,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
     }
     if (!two || !second) {
       const rsrc_t ra = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * (second ? lda1 : lda0)));
-      if (left < kStep) {
+      if (left < Sh::K) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
           buffer_to_lds16(ra, st + sa0.unit_of(wave, i) * 1024,
@@ -241,13 +262,14 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
       }
     } else {
       const rsrc_t ra = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
-      if (left < kStep) {
+      if (left < Sh::K) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
           buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.tail(i, wave, lane, lda1, left));
       } else {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.off[i]);
+        for (int i = 0; i < NA; ++i)
+          buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.off[i]);
       }
     }
   };
@@ -260,8 +282,32 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
       *reinterpret_cast<u32x4_t*>(st + sa0.unit_of(wave, i) * 1024 + lane * 16) = held[i];
   };
 
+  const int wa = at.wave_a * (Sh::BM / Sh::WA), wb = at.wave_b * (Sh::BN / Sh::WB);
+  bf16x8_t fa[Sh::FK][Sh::FM], fb[Sh::FK][Sh::FN];   // a step's fragments
   f32x4_t acc[Sh::FM][Sh::FN];
-  // the first stages are on their way while the accumulators are set up
+  auto read = [&](int t) {
+    const unsigned char* st = smem + (t % Sh::S) * Sh::stage;
+#pragma unroll
+    for (int half = 0; half < Sh::FK; ++half) {
+      read_frags<LB, Sh::BN, Sh::K>(fb[half], st + Sh::a_bytes, wb, half, lane);
+      if (two && t >= T0)
+        read_frags<LA1, Sh::BM, Sh::K>(fa[half], st, wa, half, lane);
+      else
+        read_frags<LA0, Sh::BM, Sh::K>(fa[half], st, wa, half, lane);
+    }
+  };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int half = 0; half < Sh::FK; ++half)
+#pragma unroll
+      for (int i = 0; i < Sh::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < Sh::FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][i], fb[half][j], acc[i][j], 0, 0, 0);
+  };
+  // A ring of S stages, one barrier a step; other workgroups of the compute
+  // unit multiply while this one waits.
+  constexpr int per_step = NA + NB;
 #pragma unroll
   for (int s = 0; s < Sh::S - 1; ++s)
     if (t_begin + s < t_end) {
@@ -269,40 +315,221 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
       put(t_begin + s);
     }
   epi.init(acc, at);
-
-  constexpr int per_step = NA + NB;
   for (int t = t_begin; t < t_end; ++t) {
-    // this wave's loads of step t have landed (later steps may be on their way)
+    // this wave's loads of step t have landed; later steps' may be on their way
     if (ANY || Sh::S == 2 || t_end - t - 1 < Sh::S - 2)
       wait_vm<0>();
     else
       wait_vm<per_step*(Sh::S - 2)>();
     lds_wait();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
+    meet();
     if (t + Sh::S - 1 < t_end) issue(t + Sh::S - 1);
-    const unsigned char* st = smem + (t % Sh::S) * Sh::stage;
-    const int wa = at.wave_a * (Sh::BM / Sh::WA), wb = at.wave_b * (Sh::BN / Sh::WB);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      bf16x8_t a[Sh::FM], b[Sh::FN];
-      read_frags<LB, Sh::BN>(b, st + Sh::a_bytes, wb, half, lane);
-      if (two && t >= T0)
-        read_frags<LA1, Sh::BM>(a, st, wa, half, lane);
-      else
-        read_frags<LA0, Sh::BM>(a, st, wa, half, lane);
-#pragma unroll
-      for (int i = 0; i < Sh::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < Sh::FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-    }
+    read(t);
+    multiply();
     if (ANY && t + 1 < t_end) put(t + 1);
   }
   __syncthreads();
   epi.done(acc, at, smem);
 #endif
+}
+
+// The 256 x 256 tile: 8 waves of 128 x 64, two per SIMD, one workgroup per
+// compute unit, steps of 64.  Waves 0 to 3 ("lead") hold the first 128 of a,
+// waves 4 to 7 the others; every SIMD has one of each.
+//
+// The two halves take turns: while one multiplies (64 MFMAs, 1024 cycles),
+// the other reads its fragments from LDS.  In phase p the lead half reads step
+// p / 2 (p even) or multiplies it (p odd); the other is one phase behind.
+//
+// Loads run at all times, because a step's 64 KiB take most of a step to
+// arrive: rows of 128 bytes come at 35 to 50 bytes a cycle into a compute unit
+// (64-byte rows at 18, measured), and a step at the full MFMA rate is 2048
+// cycles.  A wave sends off one load after every eighth MFMA; sent off in one
+// burst they hold up the reads and MFMAs behind them.  LDS holds two steps of
+// each half's rows of a (a half overwrites its own as soon as it has read
+// them) and three steps of b: 64 + 96 KiB.  In its MFMAs of step t a wave loads
+// its half's a of step t + 2, and half of b: the lead of step t + 2, the other
+// half (by then step t has been read by all) of step t + 3.  At their end it
+// waits for what it sent off one step before.
+struct Tile256 {
+  static constexpr int BM = 256, BN = 256, WA = 2, WB = 4;
+  static constexpr int a_half = 128 * kStep * 2, b_step = 256 * kStep * 2;
+  static constexpr int lds = 4 * a_half + 3 * b_step;
+};
+
+// Byte offset of what `lane` loads in unit `unit` (1 KiB) of a tile of ROWS
+// rows (of a, or values of one k), not held in registers.  last_row, last_chunk:
+// kRows: last row of the operand, from the tile's first, and (as the step's
+// end needs it) last chunk; kCols: the same with the roles exchanged.
+template <int LAYOUT, int ROWS>
+__device__ __forceinline__ uint32_t unit_offset(int unit, int lane, uint32_t ld2, int last_row, int last_chunk) {
+  constexpr int chunks = LAYOUT == kRows ? kStep / 8 : ROWS / 8;
+  const int at = unit * 64 + lane, row = at / chunks;
+  const int c = (at % chunks) ^ (LAYOUT == kRows ? chunk_turn(kStep, row) : pair_turn(ROWS, row) << 1);
+  return uint32_t(min(row, last_row)) * ld2 + uint32_t(min(c, last_chunk)) * 16;
+}
+
+template <int LA0, int LA1, int LB, class Epi>
+__global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi, int na, int nb) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Tile256 Sh;
+  constexpr bool two = LA0 != LA1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tile_a, tile_b;
+  tile_place(blockIdx.x, (na + 255) / 256, (nb + 255) / 256, &tile_a, &tile_b);
+  const int a_first = tile_a * 256, b_first = tile_b * 256;
+  if (g.nb) nb = *g.nb;
+  if (b_first >= nb) return;   // all its rows are behind the last one in use
+  const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
+  const int T0 = (K0 + kStep - 1) / kStep, T = T0 + (K1 + kStep - 1) / kStep;
+  const int t_begin = int(long(T) * blockIdx.y / gridDim.y), t_end = int(long(T) * (blockIdx.y + 1) / gridDim.y);
+
+  TileAt at;
+  at.wave_a = wave >> 2;
+  at.wave_b = wave & 3;
+  at.a0 = a_first + at.wave_a * 128;
+  at.b0 = b_first + at.wave_b * 64;
+  at.nb = nb;
+  at.tile_a = tile_a;
+  const bool lead = wave < 4;
+  const int w4 = wave & 3;
+
+  const long lda0 = LA0 == kRows ? g.A[0].sa : g.A[0].sk, lda1 = LA1 == kRows ? g.A[1].sa : g.A[1].sk;
+  const long ldb = LB == kRows ? g.B[0].sa : g.B[0].sk;   // of both parts of b
+  // a half that lies wholly behind the operand's end repeats its last row
+  const int n0 = g.A[0].n, n1 = g.A[1].n, nbo = g.B[0].n;
+  const int f0 = min(at.a0, LA0 == kRows ? n0 - 1 : (n0 - 1) & ~7), f1 = min(at.a0, LA1 == kRows ? n1 - 1 : (n1 - 1) & ~7);
+  const bf16_t* a0 = g.A[0].p + (LA0 == kRows ? long(f0) * lda0 : long(f0));
+  const bf16_t* a1 = g.A[1].p + (LA1 == kRows ? long(f1) * lda1 : long(f1));
+  const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(b_first) * ldb : long(b_first));
+  const bf16_t* b1 = g.B[1].p + (LB == kRows ? long(b_first) * ldb : long(b_first));
+
+  // What a step's loads need besides the lane offsets: made while fragments
+  // are on their way, so that little but the loads stands between the MFMAs.
+  uint32_t off_a[4], off_b[4];
+  rsrc_t rsrc_a, rsrc_b;
+  unsigned char *lds_a, *lds_b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    off_b[i] = LB == kRows
+        ? unit_offset<LB, 256>(wave * 4 + i, lane, uint32_t(ldb * 2), nbo - 1 - b_first, kStep / 8 - 1)
+        : unit_offset<LB, 256>(wave * 4 + i, lane, uint32_t(ldb * 2), kStep - 1, (nbo - 1 - b_first) / 8);
+  auto prepare_a = [&](int t, bool fresh) {   // this wave's four of its half's 16 units
+    const bool second = t >= T0;
+    const int k = (second ? t - T0 : t) * kStep, left = (second ? K1 : K0) - k;
+    lds_a = smem + ((t & 1) * 2 + at.wave_a) * Sh::a_half + w4 * 4096;
+    if (!two || !second) {
+      const long ld = second ? lda1 : lda0;
+      rsrc_a = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * ld));
+      if (fresh || t == T0 || left < kStep) {
+        const int n = second ? n1 - f1 : n0 - f0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          off_a[i] = LA0 == kRows
+              ? unit_offset<LA0, 128>(w4 * 4 + i, lane, uint32_t(ld * 2), n - 1, (min(left, kStep) - 1) / 8)
+              : unit_offset<LA0, 128>(w4 * 4 + i, lane, uint32_t(ld * 2), left - 1, (n - 1) / 8);
+      }
+    } else {
+      rsrc_a = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
+      if (fresh || t == T0 || left < kStep) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          off_a[i] = LA1 == kRows
+              ? unit_offset<LA1, 128>(w4 * 4 + i, lane, uint32_t(lda1 * 2), n1 - f1 - 1, (min(left, kStep) - 1) / 8)
+              : unit_offset<LA1, 128>(w4 * 4 + i, lane, uint32_t(lda1 * 2), left - 1, (n1 - f1 - 1) / 8);
+      }
+    }
+  };
+  auto prepare_b = [&](int t) {   // this wave's four of all 32 units
+    const bool second = t >= T0;
+    const int k = (second ? t - T0 : t) * kStep;
+    rsrc_b = make_rsrc((second ? b1 : b0) + (LB == kRows ? long(k) : long(k) * ldb));
+    lds_b = smem + 4 * Sh::a_half + (t % 3) * Sh::b_step + wave * 4096;
+  };
+  auto load_a = [&](int i) { buffer_to_lds16(rsrc_a, lds_a + i * 1024, off_a[i]); };
+  auto load_b = [&](int i) { buffer_to_lds16(rsrc_b, lds_b + i * 1024, off_b[i]); };
+
+  bf16x8_t fa[2][8], fb[2][4];   // a step's fragments
+  f32x4_t acc[8][4];
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const int t = t_begin + s;
+    if (t >= t_end) break;
+    if (s < 2) {
+      prepare_a(t, true);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_a(i);
+    }
+    if (s < 2 || !lead) {
+      prepare_b(t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_b(i);
+    }
+  }
+  epi.init(acc, at);
+  if (t_begin < t_end) {
+    wait_vm<0>();
+    meet();
+    if (!lead) meet();   // phase 0 of the second half
+    for (int t = t_begin; t < t_end; ++t) {
+      const unsigned char* sa = smem + ((t & 1) * 2 + at.wave_a) * Sh::a_half;
+      const unsigned char* sb = smem + 4 * Sh::a_half + (t % 3) * Sh::b_step;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        read_frags<LB, 256, kStep>(fb[half], sb, at.wave_b * 64, half, lane);
+        if (two && t >= T0)
+          read_frags<LA1, 128, kStep>(fa[half], sa, 0, half, lane);
+        else
+          read_frags<LA0, 128, kStep>(fa[half], sa, 0, half, lane);
+      }
+      const int next_a = t + 2, next_b = lead ? t + 2 : t + 3;
+      if (next_a < t_end) prepare_a(next_a, false);
+      if (next_b < t_end) prepare_b(next_b);
+      lds_wait();
+      meet();
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int half = n >> 3, i = n & 7;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][i], fb[half][j], acc[i][j], 0, 0, 0);
+        if (n % 2 == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (n < 8) {
+            if (next_a < t_end) load_a(n / 2);
+          } else {
+            if (next_b < t_end) load_b(n / 2 - 4);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      __builtin_amdgcn_s_setprio(0);
+      if (next_b < t_end)
+        wait_vm<8>();   // all but what this step sent off
+      else
+        wait_vm<0>();
+      meet();
+    }
+    if (lead) meet();
+  }
+  __syncthreads();
+  epi.done(acc, at, smem);
+#endif
+}
+
+template <int LA0, int LA1, int LB, class Epi>
+hipError_t launch_tile256(const Product<bf16_t>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
+  if (na <= 0 || nb <= 0) return hipSuccess;
+  const unsigned tiles = unsigned((na + 255) / 256) * unsigned((nb + 255) / 256);
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&tile256_kernel<LA0, LA1, LB, Epi>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, Tile256::lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((tile256_kernel<LA0, LA1, LB, Epi>), dim3(tiles, unsigned(splits)), dim3(512), Tile256::lds,
+                     stream, g, epi, na, nb);
+  return hipGetLastError();
 }
 
 template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi>
@@ -325,14 +552,13 @@ hipError_t launch_tile_bf16(const Product<bf16_t>& g, const Epi& epi, int na, in
 // Few rows: bound by reading the a operand once, so narrow tiles with a deep
 // ring, several workgroups per compute unit.  Many rows: 256 x 256, where one
 // step's 128 MFMAs per SIMD cover the loads of the next.
-using Tile16 = TileShape<128, 16, 4, 1, 4>;
-using Tile32 = TileShape<128, 32, 4, 1, 3>;
-using Tile64 = TileShape<128, 64, 2, 2, 3>;
-using Tile128 = TileShape<128, 128, 2, 2, 2>;
-using Tile256 = TileShape<256, 256, 2, 4, 2>;
-using Tile16Any = TileShape<128, 16, 4, 1, 2>;
-using Tile32Any = TileShape<128, 32, 4, 1, 2>;
-using Tile64Any = TileShape<128, 64, 2, 2, 2>;
+using Tile16 = TileShape<128, 16, 4, 1, 64, 4>;
+using Tile32 = TileShape<128, 32, 4, 1, 64, 3>;
+using Tile64 = TileShape<128, 64, 2, 2, 64, 3>;
+using Tile128 = TileShape<128, 128, 2, 2, 64, 2>;
+using Tile16Any = TileShape<128, 16, 4, 1, 64, 2>;
+using Tile32Any = TileShape<128, 32, 4, 1, 64, 2>;
+using Tile64Any = TileShape<128, 64, 2, 2, 64, 2>;
 
 constexpr int kComputeUnits = 256;
 
@@ -340,11 +566,13 @@ inline int tiles_of(int na, int nb, int bm, int bn) {
   const long n = long((na + bm - 1) / bm) * ((nb + bn - 1) / bn);
   return n > 1 << 30 ? 1 << 30 : int(n);
 }
-// 0..4: index of the tile for na x nb outputs.
-inline int tile_choice(int na, int nb) {
+// 0..4: index of the tile for na x nb outputs; any: register staging, which
+// the large tile has no registers left for.
+inline int tile_choice(int na, int nb, bool any) {
   if (nb <= 16) return 0;
   if (nb <= 32) return 1;
   if (nb <= 64) return 2;
+  if (any) return 3;
   return tiles_of(na, nb, 256, 256) >= 3 * kComputeUnits / 4 ? 4 : 3;
 }
 inline int tile_bm(int choice) { return choice == 4 ? 256 : 128; }
@@ -352,8 +580,8 @@ inline int tile_bn(int choice) { return choice == 4 ? 256 : choice == 3 ? 128 : 
 
 // Splits of a contraction of K values so that about two workgroups per
 // compute unit have work, each with at least four steps.
-inline int splits_for(int na, int nb, long K) {
-  const int c = tile_choice(na, nb);
+inline int splits_for(int na, int nb, long K, bool any) {
+  const int c = tile_choice(na, nb, any);
   const int tiles = tiles_of(na, nb, tile_bm(c), tile_bn(c));
   const long steps = (K + kStep - 1) / kStep;
   long s = 2 * kComputeUnits / tiles;
@@ -366,20 +594,19 @@ inline int splits_for(int na, int nb, long K) {
 template <int LA0, int LA1, int LB, bool ANY, class MakeEpi>
 hipError_t launch_bf16(const Product<bf16_t>& g, const MakeEpi& make, int na, int nb, int splits, hipStream_t stream) {
   if constexpr (ANY) {
-    switch (tile_choice(na, nb)) {
+    switch (tile_choice(na, nb, ANY)) {
       case 0: return launch_tile_bf16<Tile16Any, LA0, LA1, LB, true>(g, make(Tile16Any()), na, nb, splits, stream);
       case 1: return launch_tile_bf16<Tile32Any, LA0, LA1, LB, true>(g, make(Tile32Any()), na, nb, splits, stream);
       case 2: return launch_tile_bf16<Tile64Any, LA0, LA1, LB, true>(g, make(Tile64Any()), na, nb, splits, stream);
-      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, true>(g, make(Tile128()), na, nb, splits, stream);
-      default: return launch_tile_bf16<Tile256, LA0, LA1, LB, true>(g, make(Tile256()), na, nb, splits, stream);
+      default: return launch_tile_bf16<Tile128, LA0, LA1, LB, true>(g, make(Tile128()), na, nb, splits, stream);
     }
   } else {
-    switch (tile_choice(na, nb)) {
+    switch (tile_choice(na, nb, ANY)) {
       case 0: return launch_tile_bf16<Tile16, LA0, LA1, LB, false>(g, make(Tile16()), na, nb, splits, stream);
       case 1: return launch_tile_bf16<Tile32, LA0, LA1, LB, false>(g, make(Tile32()), na, nb, splits, stream);
       case 2: return launch_tile_bf16<Tile64, LA0, LA1, LB, false>(g, make(Tile64()), na, nb, splits, stream);
       case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, splits, stream);
-      default: return launch_tile_bf16<Tile256, LA0, LA1, LB, false>(g, make(Tile256()), na, nb, splits, stream);
+      default: return launch_tile256<LA0, LA1, LB>(g, make(Tile256()), na, nb, splits, stream);
     }
   }
 }
