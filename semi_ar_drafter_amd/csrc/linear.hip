@@ -14,40 +14,62 @@ namespace dspark {
 
 namespace {
 
-constexpr int kDzRows = 64;   // rows per workgroup of dz_kernel
+constexpr int kDzRows = 32;   // rows per workgroup of dz_kernel
 
 // dz[m][n] = T(dy act'(pre)) into rows of ld values (columns N..ld and rows
 // M..rows zero), and part[chunk][n] = the chunk's sum of dz over its rows, in
-// fp32, before the rounding to T.  256 threads, one column each.
+// fp32, before the rounding to T.  256 threads, four columns each; vec: rows
+// of N values keep four-value alignment.
 template <typename T>
 __global__ __launch_bounds__(256) void dz_kernel(int M, int rows, int N, int act, const T* __restrict__ dy,
                                                  const float* __restrict__ pre, T* __restrict__ dz, long ld,
-                                                 float* __restrict__ part) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
+                                                 float* __restrict__ part, bool vec) {
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int m0 = blockIdx.y * kDzRows, m1 = min(rows, m0 + kDzRows);
   if (n >= ld) return;
-  float s = 0.f;
+  const int left = N - n;
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int m = m0; m < m1; ++m) {
-    float v = 0.f;
-    if (m < M && n < N) {
-      v = to_f32(dy[size_t(m) * N + n]);
-      if (act) v *= act_slope(act, pre[size_t(m) * N + n]);
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (m < M && left > 0) {
+      v = load4(dy + size_t(m) * N + n, left, vec);
+      if (act) {
+        const f32x4_t z = load4(pre + size_t(m) * N + n, left, vec);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= act_slope<T>(act, z[e]);
+      }
     }
-    if (dz) dz[size_t(m) * ld + n] = from_f32<T>(v);
+    // a row of dz is dy's own (no copy) or ld long, a multiple of 64
+    if (dz) store4(dz + size_t(m) * ld + n, v, 4, true);
     s += v;
   }
-  if (part && n < N) part[size_t(blockIdx.y) * N + n] = s;
+  if (part) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) part[size_t(blockIdx.y) * N + n + e] = s[e];
+  }
 }
 
-// dbias[n] = sum over chunks, in chunk order.
+// dbias[n] = sum over chunks: 8 threads per column take every eighth chunk
+// each, then join in order.  32 columns per workgroup.
 template <typename T>
 __global__ __launch_bounds__(256) void dbias_kernel(int N, int chunks, const float* __restrict__ part,
                                                     T* __restrict__ dbias) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float sums[8][32];
+  const int c = threadIdx.x & 31, q = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
   float s = 0.f;
-  for (int c = 0; c < chunks; ++c) s += part[size_t(c) * N + n];
-  dbias[n] = from_f32<T>(s);
+  if (n < N) {
+#pragma unroll 8
+    for (int i = q; i < chunks; i += 8) s += part[size_t(i) * N + n];
+  }
+  sums[q][c] = s;
+  __syncthreads();
+  if (q == 0 && n < N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sums[i][c];
+    dbias[n] = from_f32<T>(s);
+  }
 }
 
 // dst[r][0..ld) = src[r][0..n), zeros behind: rows whose length is no multiple
@@ -71,13 +93,15 @@ __global__ __launch_bounds__(256) void join_splits_kernel(int M, int N, int spli
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
   for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + (size_t(s) * M + b) * ld + a);
-  epi.finish(v, b, a, n);
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  epi.finish(v, epi.bias ? load4(epi.bias + a, n, epi.vec) : zero,
+             epi.residual ? load4(epi.residual + size_t(b) * N + a, n, epi.vec) : zero, b, a, n);
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 inline long up64(long x) { return (x + 63) / 64 * 64; }
 inline long dz_stride(int N) { return up64(N); }
-inline int dz_chunks(int M) { return (M + kDzRows - 1) / kDzRows; }
+inline int dz_chunks(int M) { return int((up64(M) + kDzRows - 1) / kDzRows); }
 
 // Splits of a bf16 product's contraction into partial sums [split][rows][up64(na)].
 inline size_t split_bytes(int na, int nb, long K, bool any) {
@@ -94,7 +118,8 @@ LinearEpi<T> linear_epi(const LinearArgs& a) {
   epi.pre = a.pre;
   epi.act = a.act;
   epi.na = a.N;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.residual);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.residual) |
+                       reinterpret_cast<uintptr_t>(a.bias);
   epi.vec = a.N % 4 == 0 && at % (4 * sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
   return epi;
 }
@@ -165,12 +190,13 @@ hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** 
   }
   if (a.N == 0) return hipSuccess;
   if (rows > 0 && (copy || a.dbias))
-    hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 255) / 256), unsigned((rows + kDzRows - 1) / kDzRows)),
+    hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 1023) / 1024), unsigned((rows + kDzRows - 1) / kDzRows)),
                        dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, out, *ld,
-                       a.dbias ? part : nullptr);
+                       a.dbias ? part : nullptr,
+                       a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0);
   if (a.dbias)
-    hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 255) / 256)), dim3(256), 0, stream, a.N,
-                       dz_chunks(a.M), part, static_cast<T*>(a.dbias));
+    hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 31) / 32)), dim3(256), 0, stream, a.N,
+                       rows > 0 ? int((rows + kDzRows - 1) / kDzRows) : 0, part, static_cast<T*>(a.dbias));
   return hipGetLastError();
 }
 

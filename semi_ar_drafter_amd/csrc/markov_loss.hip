@@ -62,27 +62,42 @@ __global__ __launch_bounds__(1024) void compact_kernel(int N, int V, const int* 
   if (tid == 1023) *count = sums[1023];
 }
 
+// What the products' epilogues need of every row in use, by compact row.
+struct RowData {
+  const int* label_in;
+  const float *lse_in, *g_in;   // of the gradient only
+  int *label, *token;
+  float *lse, *g;
+};
+
 // X[i] = [h[row[i]] | 0 | W1[prev[row[i]]] | 0]; rows from count up to the
-// next multiple of 64 are zero.  token[i] = prev[row[i]], clamped.  One
-// workgroup per row.
+// next multiple of 64 are zero.  rows.token[i] = prev[row[i]], clamped; label,
+// lse and g of the row.  One workgroup per row.
 template <typename T>
 __global__ __launch_bounds__(256) void gather_kernel(int V, int d, int dp, int r, int rp, const int* __restrict__ count,
                                                      const int* __restrict__ row, const int* __restrict__ prev,
                                                      const T* __restrict__ h, const T* __restrict__ W1,
-                                                     T* __restrict__ X, int* __restrict__ token) {
+                                                     T* __restrict__ X, RowData rows) {
   const int i = blockIdx.x, n = *count;
   if (i >= ((n + 63) & ~63)) return;
   T* x = X + size_t(i) * (dp + rp);
   const bool used = i < n;
   const int src = used ? row[i] : 0;
   const T zero = from_f32<T>(0.f);
+  if (used && threadIdx.x == 0) {
+    rows.label[i] = rows.label_in[src];
+    if (rows.lse_in) {
+      rows.lse[i] = rows.lse_in[src];
+      rows.g[i] = rows.g_in[src];
+    }
+  }
   if (dp) {
     const T* hr = h + size_t(src) * d;
     for (int c = threadIdx.x; c < dp; c += 256) x[c] = used && c < d ? hr[c] : zero;
   }
   if (rp) {
     const int t = used ? min(max(prev[src], 0), V - 1) : 0;
-    if (used && threadIdx.x == 0) token[i] = t;
+    if (used && threadIdx.x == 0) rows.token[i] = t;
     const T* wr = W1 + size_t(t) * r;
     for (int c = threadIdx.x; c < rp; c += 256) x[dp + c] = used && c < r ? wr[c] : zero;
   }
@@ -249,7 +264,7 @@ __global__ __launch_bounds__(256) void pad_w2_kernel(int V, long ld, const bf16_
 
 // What the forward and the backward call carve out of the workspace.
 struct Layout {
-  size_t row, place, token, X, W2, stat, zlab, dz, dXh, dXe, total;
+  size_t row, place, token, label, lse, g, X, W2, stat, zlab, dz, dXh, dXe, total;
   int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
   long w2_ld;                // row length of W2 as the products read it
   int splits_h, splits_e;    // of the contraction over a piece's tokens
@@ -270,6 +285,11 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
   L.row = take(size_t(N) * 4);
   L.place = take(size_t(N) * 4);
   L.token = take(size_t(N) * 4);
+  L.label = take(size_t(N) * 4);
+  if (backward) {
+    L.lse = take(size_t(N) * 4);
+    L.g = take(size_t(N) * 4);
+  }
   L.X = take(size_t(L.rows) * (L.dp + L.rp) * elem);
   L.w2_ld = V;
   if (bf16 && r && V % 8) {
@@ -297,7 +317,8 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
 template <typename T>
 struct Parts {
   Layout L;
-  int *count, *row, *place, *token;
+  int *count, *row, *place;
+  RowData rows;
   T* X;
   const T* W2;
   int kx;
@@ -310,14 +331,20 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t st
   p.count = reinterpret_cast<int*>(ws);
   p.row = reinterpret_cast<int*>(ws + L.row);
   p.place = reinterpret_cast<int*>(ws + L.place);
-  p.token = reinterpret_cast<int*>(ws + L.token);
+  p.rows.label_in = a.label;
+  p.rows.lse_in = a.lse_in;
+  p.rows.g_in = a.g;
+  p.rows.label = reinterpret_cast<int*>(ws + L.label);
+  p.rows.token = reinterpret_cast<int*>(ws + L.token);
+  p.rows.lse = reinterpret_cast<float*>(ws + L.lse);
+  p.rows.g = reinterpret_cast<float*>(ws + L.g);
   p.X = reinterpret_cast<T*>(ws + L.X);
   p.W2 = static_cast<const T*>(a.W2);
   p.kx = L.dp + L.rp;
   hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
-  if (p.kx && a.N)
+  if (a.N)
     hipLaunchKernelGGL((gather_kernel<T>), dim3(unsigned(up(a.N, 64))), dim3(256), 0, stream, a.V, a.d, L.dp, a.r,
-                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X, p.token);
+                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X, p.rows);
   if (L.W2) {
     p.W2 = reinterpret_cast<T*>(ws + L.W2);
     hipLaunchKernelGGL(pad_w2_kernel, dim3(unsigned((L.w2_ld + 1023) / 1024), unsigned(a.r)), dim3(256), 0, stream,
@@ -379,7 +406,7 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
   int bm = 0;
   auto make = [&](auto shape) {
     bm = shape.BM;
-    return StatsEpi<T, shape.WA, shape.BN>{base_logits(a, p, 0, a.V, nullptr), a.label, stat, a.N, zlab};
+    return StatsEpi<T, shape.WA, shape.BN>{base_logits(a, p, 0, a.V, nullptr), p.rows.label, stat, a.N, zlab};
   };
   if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N, 1, stream)) != hipSuccess)
     return e;
@@ -415,7 +442,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
   for (int v0 = 0; v0 < a.V; v0 += L.width) {
     const int nv = a.V - v0 < L.width ? a.V - v0 : L.width;
     auto grad = [&](auto) {
-      return GradEpi<T>{base_logits(a, p, v0, nv, dU), a.label, a.lse_in, a.g, dz, L.width, dU};
+      return GradEpi<T>{base_logits(a, p, v0, nv, dU), p.rows.label, p.rows.lse, p.rows.g, dz, L.width, dU};
     };
     if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N, 1, stream)) != hipSuccess) return e;
     const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
@@ -466,7 +493,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL(join_e_kernel, dim3(unsigned(a.N)), dim3(256), 0, stream, long(L.rp), L.splits_e, split_e,
                            p.count, dXe);
       hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned(a.N)), dim3(1024), 0, stream, a.r, long(L.rp), p.count,
-                         p.token, dXe, static_cast<T*>(a.dW1));
+                         p.rows.token, dXe, static_cast<T*>(a.dW1));
     }
   }
   return hipGetLastError();

@@ -75,6 +75,20 @@ __device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n, bool vec) {
     if (i < n) p[i] = f32_to_bf16(v[i]);
 }
 
+// Four stored values as they lie in memory, and widened: a tile's loads are
+// all sent off before the first is used.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+  f32x4_t v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const f32x4_t*>(p); }
+  __device__ __forceinline__ f32x4_t wide() const { return v; }
+};
+template <> struct Raw4<bf16_t> {
+  u32x2_t v;
+  __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u32x2_t*>(p); }
+  __device__ __forceinline__ f32x4_t wide() const { return f32x4_t{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])}; }
+};
+
 // exp(x), x <= 0: for fp32 storage to the last bit or two; for bf16 storage by
 // the hardware's base-2 exponential, whose argument rounding costs |x| 2^-23
 // relative, far below the half step 2^-8 that dz is rounded by.
@@ -113,19 +127,53 @@ struct TileAt {
 // ---------------------------------------------------------------------------
 // Activations
 // ---------------------------------------------------------------------------
+// The normal distribution's integral P(z) and density times sqrt(2 pi),
+// exp(-z^2 / 2).  fp32 storage takes the library's error function.  For bf16
+// storage Abramowitz and Stegun 7.1.26, within 1e-7 of P: erfc(x) = (t (a1 +
+// t (a2 + ..))) exp(-x^2), t = 1 / (1 + p x), x = |z| / sqrt 2, which shares
+// its exponential with the density (about 15 instructions instead of 60).
+template <typename T> __device__ __forceinline__ float normal_cdf(float z, float* e);
+template <> __device__ __forceinline__ float normal_cdf<float>(float z, float* e) {
+  *e = expf(-0.5f * z * z);
+  return 0.5f * (1.f + erff(z * 0.70710678118654752f));
+}
+template <> __device__ __forceinline__ float normal_cdf<bf16_t>(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  *e = __expf(-x * x);
+  float q = 1.061405429f;
+  q = q * t - 1.453152027f;
+  q = q * t + 1.421413741f;
+  q = q * t - 0.284496736f;
+  q = q * t + 0.254829592f;
+  const float tail = 0.5f * q * t * *e;   // P(-|z|)
+  return z < 0.f ? tail : 1.f - tail;
+}
+template <typename T> __device__ __forceinline__ float sigmoid(float z);
+template <> __device__ __forceinline__ float sigmoid<float>(float z) { return 1.f / (1.f + expf(-z)); }
+template <> __device__ __forceinline__ float sigmoid<bf16_t>(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+}
+
+template <typename T>
 __device__ __forceinline__ float act_value(int act, float z) {
+  float e;
   if (act == 1) return z > 0.f ? z : 0.f;
-  if (act == 2) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (act == 3) return z / (1.f + __expf(-z));
+  if (act == 2) return z * normal_cdf<T>(z, &e);
+  if (act == 3) return z * sigmoid<T>(z);
   return z;
 }
 // d act / dz
+template <typename T>
 __device__ __forceinline__ float act_slope(int act, float z) {
   if (act == 1) return z > 0.f ? 1.f : 0.f;
-  if (act == 2)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  if (act == 2) {
+    float e;
+    const float c = normal_cdf<T>(z, &e);
+    return c + z * 0.39894228040143268f * e;
+  }
   if (act == 3) {
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = sigmoid<T>(z);
     return s + z * s * (1.f - s);
   }
   return 1.f;
@@ -151,34 +199,67 @@ struct LinearEpi {
   T* y;
   float* pre;
   int act, na;
-  bool vec;   // rows of na values keep four-value alignment
+  bool vec;   // rows of na values keep four-value alignment, and so does bias
   template <int FM, int FN>
   __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
     acc_zero(acc);
   }
-  // four values from (b, a) on, n of them inside the row
-  __device__ __forceinline__ void finish(f32x4_t v, int b, int a, int n) const {
-    if (bias) v += load4(bias + a, n, false);
+  // four values from (b, a) on, n of them inside the row; bias and residual
+  // already widened
+  __device__ __forceinline__ void finish(f32x4_t v, f32x4_t bv, f32x4_t rv, int b, int a, int n) const {
+    v += bv;
     const size_t at = size_t(b) * na + a;
     if (pre) store4(pre + at, v, n, vec);
     if (act) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_value(act, v[e]);
+      for (int e = 0; e < 4; ++e) v[e] = act_value<T>(act, v[e]);
     }
-    if (residual) v += load4(residual + at, n, vec);
+    if (residual) v += rv;
     store4(y + at, v, n, vec);
   }
   template <int FM, int FN>
   __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
+    const int a_lane = t.a0 + 4 * (lane >> 4), b_lane = t.b0 + (lane & 15);
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    if (vec && t.a0 + 16 * FM <= na && t.b0 + 16 * FN <= t.nb) {   // the wave's part lies inside
+      Raw4<T> bv[FM];
+      if (bias) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) bv[i].load(bias + a_lane + 16 * i);
+      }
+      // two columns of tiles at a time: their residuals are on the way together
+      constexpr int G = FN % 2 ? 1 : 2;
+#pragma unroll
+      for (int j0 = 0; j0 < FN; j0 += G) {
+        Raw4<T> rv[G][FM];
+        if (residual) {
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+              rv[j][i].load(residual + size_t(b_lane + 16 * (j0 + j)) * na + a_lane + 16 * i);
+        }
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+            finish(acc[i][j0 + j], bias ? bv[i].wide() : zero, residual ? rv[j][i].wide() : zero,
+                   b_lane + 16 * (j0 + j), a_lane + 16 * i, 4);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      const int a = a_lane + 16 * i;
       if (a >= na) continue;
+      const f32x4_t bv = bias ? load4(bias + a, na - a, false) : zero;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int b = t.b0 + 16 * j + (lane & 15);
-        if (b < t.nb) finish(acc[i][j], b, a, na - a);
+        const int b = b_lane + 16 * j;
+        if (b >= t.nb) continue;
+        const f32x4_t rv = residual ? load4(residual + size_t(b) * na + a, na - a, vec) : zero;
+        finish(acc[i][j], bv, rv, b, a, na - a);
       }
     }
   }
@@ -265,18 +346,28 @@ struct BaseLogits {
   __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt& t) const {
     acc_zero(acc);
     if (!U) return;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, a0 = t.a0 + 4 * (lane >> 4);
+    const T* u[FN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int b = t.b0 + 16 * j + (lane & 15);
-      if (b >= t.nb) continue;
-      const T* u = U + size_t(row[b]) * V + v0;
+    for (int j = 0; j < FN; ++j)   // rows behind the last one read it again
+      u[j] = U + size_t(row[min(t.b0 + 16 * j + (lane & 15), t.nb - 1)]) * V + v0 + a0;
+    if (vec && t.a0 + 16 * FM <= na) {
+      Raw4<T> raw[FM][FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int a = t.a0 + 16 * i + 4 * (lane >> 4);
-        if (a < na) acc[i][j] = load4(u + a, na - a, vec);
-      }
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) raw[i][j].load(u[j] + 16 * i);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[i][j] = raw[i][j].wide();
+      return;
     }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        if (a0 + 16 * i < na) acc[i][j] = load4(u[j] + 16 * i, na - a0 - 16 * i, vec);
   }
 };
 
@@ -287,7 +378,7 @@ struct BaseLogits {
 template <typename T, int WAVES_A, int BN>
 struct StatsEpi {
   BaseLogits<T> base;
-  const int* label;   // [N], by original row
+  const int* label;   // by compact row, as lse and g below
   float2* stat;       // [tiles][stat_ld]
   long stat_ld;
   float* zlab;
@@ -300,10 +391,13 @@ struct StatsEpi {
     const int lane = threadIdx.x & 63;
     float2* part = static_cast<float2*>(lds);   // [WAVES_A][BN]
     const float ninf = -__builtin_huge_valf();
+    int labels[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) labels[j] = label[min(t.b0 + 16 * j + (lane & 15), t.nb - 1)];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int b = t.b0 + 16 * j + (lane & 15);
-      const int y = b < t.nb ? label[base.row[b]] - base.v0 : -1;
+      const int y = b < t.nb ? labels[j] - base.v0 : -1;
       float m = ninf;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -364,25 +458,33 @@ struct GradEpi {
   template <int FM, int FN>
   __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;
+    int labels[FN];
+    float lses[FN], gs[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int b = min(t.b0 + 16 * j + (lane & 15), t.nb - 1);
+      labels[j] = label[b] - base.v0;
+      lses[j] = lse[b];
+      gs[j] = g[b];
+    }
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int b = t.b0 + 16 * j + (lane & 15);
       if (b >= t.nb) continue;
-      const int row = base.row[b];
-      const int y = label[row] - base.v0;
-      const float l = lse[row], gb = g[row];
+      const int y = labels[j];
+      T* u = dU ? dU + size_t(base.row[b]) * base.V + base.v0 : nullptr;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int a = t.a0 + 16 * i + 4 * (lane >> 4);
         f32x4_t v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p = exp_of<T>(acc[i][j][e] - l);
-          v[e] = a + e < base.na ? gb * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
+          const float p = exp_of<T>(acc[i][j][e] - lses[j]);
+          v[e] = a + e < base.na ? gs[j] * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
         }
         // the piece's width dz_ld is a multiple of the tile: every a of the tile is inside it
         store4(dz + size_t(b) * dz_ld + a, v, 4, true);
-        if (dU && a < base.na) store4(dU + size_t(row) * base.V + base.v0 + a, v, base.na - a, base.vec);
+        if (dU && a < base.na) store4(u + a, v, base.na - a, base.vec);
       }
     }
   }

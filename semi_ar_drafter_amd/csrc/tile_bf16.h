@@ -578,15 +578,26 @@ inline int tile_choice(int na, int nb, bool any) {
 inline int tile_bm(int choice) { return choice == 4 ? 256 : 128; }
 inline int tile_bn(int choice) { return choice == 4 ? 256 : choice == 3 ? 128 : 16 << choice; }
 
-// Splits of a contraction of K values so that about two workgroups per
-// compute unit have work, each with at least four steps.
+// Splits of a contraction of K values whose products are summed in fp32
+// afterwards.  A compute unit works through its tiles one after the other (two
+// side by side with the smaller tiles), so the time goes with the number of
+// rounds, which splits make finer; each costs the writing and reading of its
+// tile in fp32, about what twelve steps of a 256 x 256 tile take.
 inline int splits_for(int na, int nb, long K, bool any) {
   const int c = tile_choice(na, nb, any);
-  const int tiles = tiles_of(na, nb, tile_bm(c), tile_bn(c));
+  const long tiles = tiles_of(na, nb, tile_bm(c), tile_bn(c)), slots = c == 4 ? kComputeUnits : 2 * kComputeUnits;
   const long steps = (K + kStep - 1) / kStep;
-  long s = 2 * kComputeUnits / tiles;
-  if (s > steps / 4) s = steps / 4;
-  return s < 1 ? 1 : s > 64 ? 64 : int(s);
+  const double extra = c == 4 ? 12 : 4;
+  int best = 1;
+  double least = double((tiles + slots - 1) / slots) * (steps + (K > 0 ? 0 : 1));
+  for (int s = 2; s <= 64 && s * 4 <= steps; ++s) {
+    const double cost = double((tiles * s + slots - 1) / slots) * ((steps + s - 1) / s + extra);
+    if (cost < least * 0.97) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // MakeEpi<Shape>()(…) gives the epilogue for a tile shape (its statistics
