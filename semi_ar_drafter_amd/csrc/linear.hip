@@ -103,9 +103,10 @@ inline long up64(long x) { return (x + 63) / 64 * 64; }
 inline long dz_stride(int N) { return up64(N); }
 inline int dz_chunks(int M) { return int((up64(M) + kDzRows - 1) / kDzRows); }
 
-// Splits of a bf16 product's contraction into partial sums [split][rows][up64(na)].
-inline size_t split_bytes(int na, int nb, long K, bool any) {
-  const int s = splits_for(na, nb, K, any);
+// Splits of a product's contraction into partial sums [split][rows][up64(na)].
+inline size_t split_bytes(int na, int nb, long K, bool bf16, bool any) {
+  if (na == 0 || nb == 0) return 0;
+  const int s = bf16 ? splits_for(na, nb, K, any) : f32_splits(na, nb, K);
   return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
 }
 
@@ -124,24 +125,27 @@ LinearEpi<T> linear_epi(const LinearArgs& a) {
   return epi;
 }
 
-// A product into epi, or by way of split partial sums in `part`.
-template <int LA, int LB>
-hipError_t product(const Product<bf16_t>& g, bool any, const LinearEpi<bf16_t>& epi, int na, int nb, float* part,
+// A product into epi, or by way of split partial sums in `part`; LA, LB and
+// any are for bf16 (fp32 kernels read any layout).
+template <int LA, int LB, typename T>
+hipError_t product(const Product<T>& g, bool any, const LinearEpi<T>& epi, int na, int nb, float* part,
                    hipStream_t stream) {
-  const int splits = splits_for(na, nb, g.K[0], any);
-  hipError_t e;
-  if (splits == 1) {
-    auto make = [&](auto) { return epi; };
-    return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, 1, stream)
-               : launch_bf16<LA, LA, LB, false>(g, make, na, nb, 1, stream);
-  }
+  if (na == 0 || nb == 0) return hipSuccess;
+  constexpr bool bf16 = sizeof(T) == 2;
+  const int splits = bf16 ? splits_for(na, nb, g.K[0], any) : f32_splits(na, nb, g.K[0]);
+  auto run = [&](auto&& make) {
+    if constexpr (bf16)
+      return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, splits, stream)
+                 : launch_bf16<LA, LA, LB, false>(g, make, na, nb, splits, stream);
+    else
+      return launch_f32(g, make, na, nb, splits, stream);
+  };
+  if (splits == 1) return run([&](auto) { return epi; });
   const long ld = up64(na);
-  auto make = [&](auto) { return AddEpi{part, ld, na, true, long(nb) * ld}; };
-  e = any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, splits, stream)
-          : launch_bf16<LA, LA, LB, false>(g, make, na, nb, splits, stream);
+  const hipError_t e = run([&](auto) { return AddEpi{part, ld, na, true, long(nb) * ld}; });
   if (e != hipSuccess) return e;
   const long quads = long(nb) * ((na + 3) / 4);
-  hipLaunchKernelGGL((join_splits_kernel<bf16_t>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, stream, nb, na,
+  hipLaunchKernelGGL((join_splits_kernel<T>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, stream, nb, na,
                      splits, part, ld, epi);
   return hipGetLastError();
 }
@@ -169,7 +173,7 @@ hipError_t linear_f32(const LinearArgs& a, hipStream_t stream) {
   g.A[0] = {static_cast<const float*>(a.w), a.K, 1, a.N};
   g.B[0] = {static_cast<const float*>(a.x), a.K, 1, a.M};
   g.K[0] = a.K;
-  return launch_tile_f32(g, linear_epi<float>(a), a.N, a.M, stream);
+  return product<kRows, kRows>(g, false, linear_epi<float>(a), a.N, a.M, static_cast<float*>(a.ws), stream);
 }
 
 // dz and its chunk sums; `dz` (with its row length) is dy itself where no
@@ -205,65 +209,41 @@ bool aligned4(const void* p, int n) {
   return n % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
 }
 
-hipError_t linear_backward_f32(const LinearBackwardArgs& a, hipStream_t stream) {
-  const float* dz;
-  long ld;
-  unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  hipError_t e = make_dz(a, a.act != 0, a.M, &dz, &ld, &ws, stream);
-  if (e != hipSuccess) return e;
-  if (a.dx) {
-    Product<float> g = {};
-    g.A[0] = {static_cast<const float*>(a.w), 1, a.K, a.K};
-    g.B[0] = {dz, ld, 1, a.M};
-    g.K[0] = a.N;
-    StoreEpi<float> epi{static_cast<float*>(a.dx), a.K, a.K, aligned4<float>(a.dx, a.K)};
-    if ((e = launch_tile_f32(g, epi, a.K, a.M, stream)) != hipSuccess) return e;
-  }
-  if (a.dw) {
-    Product<float> g = {};
-    g.A[0] = {static_cast<const float*>(a.x), 1, a.K, a.K};
-    g.B[0] = {dz, 1, ld, a.N};
-    g.K[0] = a.M;
-    StoreEpi<float> epi{static_cast<float*>(a.dw), a.K, a.K, aligned4<float>(a.dw, a.K)};
-    if ((e = launch_tile_f32(g, epi, a.K, a.N, stream)) != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 // The gradient's products through the same epilogue as the forward one,
 // without bias, activation and residual.
-LinearEpi<bf16_t> plain_epi(void* out, int na) {
-  LinearEpi<bf16_t> epi = {};
-  epi.y = static_cast<bf16_t*>(out);
+template <typename T>
+LinearEpi<T> plain_epi(void* out, int na) {
+  LinearEpi<T> epi = {};
+  epi.y = static_cast<T*>(out);
   epi.na = na;
-  epi.vec = aligned4<bf16_t>(out, na);
+  epi.vec = aligned4<T>(out, na);
   return epi;
 }
 
-hipError_t linear_backward_bf16(const LinearBackwardArgs& a, hipStream_t stream) {
-  const bf16_t* dz;
+template <typename T>
+hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
+  const T* dz;
   long ld;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  // as b operand dz ends in zeros along both axes
-  const bool copy = a.act != 0 || a.N % kStep != 0 || a.M % kStep != 0;
-  hipError_t e = make_dz(a, copy, up64(a.M), &dz, &ld, &ws, stream);
+  // as bf16 b operand dz ends in zeros along both axes
+  const bool copy = a.act != 0 || (a.bf16 && (a.N % kStep != 0 || a.M % kStep != 0));
+  hipError_t e = make_dz(a, copy, a.bf16 ? up64(a.M) : long(a.M), &dz, &ld, &ws, stream);
   if (e != hipSuccess) return e;
   float* part = reinterpret_cast<float*>(ws);
+  const bool any = a.K % 8 != 0;
   if (a.dx) {
-    Product<bf16_t> g = {};
-    g.A[0] = {static_cast<const bf16_t*>(a.w), 1, a.K, a.K};
+    Product<T> g = {};
+    g.A[0] = {static_cast<const T*>(a.w), 1, a.K, a.K};
     g.B[0] = {dz, ld, 1, a.M};
     g.K[0] = a.N;
-    if ((e = product<kCols, kRows>(g, a.K % 8 != 0, plain_epi(a.dx, a.K), a.K, a.M, part, stream)) != hipSuccess)
-      return e;
+    if ((e = product<kCols, kRows>(g, any, plain_epi<T>(a.dx, a.K), a.K, a.M, part, stream)) != hipSuccess) return e;
   }
   if (a.dw) {
-    Product<bf16_t> g = {};
-    g.A[0] = {static_cast<const bf16_t*>(a.x), 1, a.K, a.K};
+    Product<T> g = {};
+    g.A[0] = {static_cast<const T*>(a.x), 1, a.K, a.K};
     g.B[0] = {dz, 1, ld, a.N};
     g.K[0] = a.M;
-    if ((e = product<kCols, kCols>(g, a.K % 8 != 0, plain_epi(a.dw, a.K), a.K, a.N, part, stream)) != hipSuccess)
-      return e;
+    if ((e = product<kCols, kCols>(g, any, plain_epi<T>(a.dw, a.K), a.K, a.N, part, stream)) != hipSuccess) return e;
   }
   return hipSuccess;
 }
@@ -271,14 +251,12 @@ hipError_t linear_backward_bf16(const LinearBackwardArgs& a, hipStream_t stream)
 }  // namespace
 
 size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
-  if (!bf16) return 0;
-  return (K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K, K % 8 != 0);
+  return (bf16 && K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K, bf16, K % 8 != 0);
 }
 
 size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16) {
   const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4));
-  if (!bf16 || M == 0 || K == 0) return dz;
-  const size_t dx = split_bytes(K, M, N, K % 8 != 0), dw = split_bytes(K, N, M, K % 8 != 0);
+  const size_t dx = split_bytes(K, M, N, bf16, K % 8 != 0), dw = split_bytes(K, N, M, bf16, K % 8 != 0);
   return dz + (dx > dw ? dx : dw);
 }
 
@@ -287,7 +265,7 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t stream) {
-  return a.bf16 ? linear_backward_bf16(a, stream) : linear_backward_f32(a, stream);
+  return a.bf16 ? linear_backward_t<bf16_t>(a, stream) : linear_backward_t<float>(a, stream);
 }
 
 }  // namespace dspark

@@ -33,6 +33,7 @@ inline size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 // Largest width of a piece's dz array, in bytes.
 constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr int kPieceAlign = 256;
+constexpr int kLeastTile = 64;   // along the vocabulary
 
 // Lists the rows that have a label, in order: row[i] = n, place[n] = i or -1.
 // One workgroup; each thread takes a run of rows.
@@ -297,15 +298,19 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     L.W2 = take(size_t(r) * L.w2_ld * 2);
   }
   if (!backward) {
-    L.stat = take((size_t(V) + kTileF32 - 1) / kTileF32 * N * sizeof(float2));
+    L.stat = take((size_t(V) + kLeastTile - 1) / kLeastTile * N * sizeof(float2));
     L.zlab = take(size_t(N) * 4);
   } else {
     const size_t full = up(V, kPieceAlign);
     const size_t most = kPieceBytes / (size_t(L.rows) * elem);
     const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
     L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
-    L.splits_h = bf16 && d && N ? splits_for(d, N, L.width, d % 8 != 0) : 1;
-    L.splits_e = bf16 && r && N ? splits_for(r, N, L.width, false) : 1;
+    auto splits = [&](int na, bool any) {
+      if (!na || !N) return 1;
+      return bf16 ? splits_for(na, N, L.width, any) : f32_splits(na, N, L.width);
+    };
+    L.splits_h = splits(d, d % 8 != 0);
+    L.splits_e = splits(r, false);
     L.dz = take(size_t(L.rows) * L.width * elem);
     L.dXh = take(size_t(L.splits_h) * L.rows * L.dp * 4);
     L.dXe = take(size_t(L.splits_e) * L.rows * L.rp * 4);
@@ -386,12 +391,10 @@ hipError_t multiply(const Product<bf16_t>& g, bool any, const Make& make, int na
   return any ? launch_bf16<LA0, LA1, LB, true>(g, make, na, nb, splits, stream)
              : launch_bf16<LA0, LA1, LB, false>(g, make, na, nb, splits, stream);
 }
-struct ShapeF32 {
-  static constexpr int BM = kTileF32, BN = kTileF32, WA = 2;
-};
 template <int LA0, int LA1, int LB, class Make>
-hipError_t multiply(const Product<float>& g, bool, const Make& make, int na, int nb, int, hipStream_t stream) {
-  return launch_tile_f32(g, make(ShapeF32()), na, nb, stream);
+hipError_t multiply(const Product<float>& g, bool, const Make& make, int na, int nb, int splits,
+                    hipStream_t stream) {
+  return launch_f32(g, make, na, nb, splits, stream);
 }
 
 template <typename T>

@@ -1,85 +1,198 @@
-// Matrix product on the fp32 matrix instruction (v_mfma_f32_16x16x4_f32) for
-// any type, layout, size and alignment: operands are read element by element
-// with bounds checks and widened to fp32 on the way into LDS.
+// Matrix product of fp32 operands on v_mfma_f32_16x16x4_f32, for any layout,
+// size and alignment.
+//
+// A step covers 32 of the contraction.  Each operand's step goes through
+// registers (16-byte loads at element alignment, sent off a step ahead) into
+// one of two LDS buffers, as it is stored:
+//   kRows  [a][32 k], 128 bytes a row; one ds_read_b128 gives a lane four
+//          consecutive k, the operands of four MFMAs (the contraction's order
+//          is free as long as both operands agree: MFMA e takes k = 16 half +
+//          4 (lane / 16) + e).  16-byte chunk c of row a lies at c ^ (a & 7).
+//   kCols  [32 k][a]; four ds_read_b32, each 16 neighbouring a of four k that
+//          are four rows apart: rows are padded by 4 so that these fall on
+//          different banks.
 #pragma once
 #include "projection.h"
 
 namespace dspark {
 
-constexpr int kTileF32 = 128;   // tile along a and along b
-constexpr int kTileF32K = 16;   // contraction per step
-constexpr int kTileF32Pad = kTileF32 + 4;
-constexpr int kTileF32Lds = 2 * kTileF32K * kTileF32Pad;   // floats
+constexpr int kStepF32 = 32;
 
-// 256 threads = 2 x 2 waves, 64 x 64 of C each.  One workgroup per tile,
-// tiles of b fastest.
-template <typename T, class Epi>
-__global__ __launch_bounds__(256) void tile_f32_kernel(Product<T> g, Epi epi, int na, int nb) {
-  __shared__ float lds[kTileF32Lds];
-  float* As = lds;
-  float* Bs = lds + kTileF32K * kTileF32Pad;
+// Tile: BM along a, BN along b, WA x WB waves.
+template <int BM_, int BN_, int WA_, int WB_>
+struct TileF32 {
+  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_;
+  static constexpr int threads = 64 * WA * WB, FM = BM / WA / 16, FN = BN / WB / 16;
+  // bytes of one operand's step, in either layout
+  static constexpr int bytes(int rows) { return (rows + 4) * kStepF32 * 4; }
+  static constexpr int stage = bytes(BM) + bytes(BN), lds = 2 * stage;
+};
+
+// One operand's step: `ROWS` rows of a by 32 of k, LOADS 16-byte chunks per thread.
+template <int ROWS, int THREADS>
+struct StepF32 {
+  static constexpr int chunks = ROWS * kStepF32 / 4, loads = (chunks + THREADS - 1) / THREADS;
+  f32x4_t v[loads];
+
+  __device__ __forceinline__ void load(const Operand<float>& o, int first, int k0, int K, int tid) {
+#pragma unroll
+    for (int i = 0; i < loads; ++i) {
+      const int at = tid + i * THREADS;
+      if (chunks % THREADS && at >= chunks) break;
+      f32x4_t r = {0.f, 0.f, 0.f, 0.f};
+      int n;           // values of the chunk that exist
+      const float* p;
+      if (o.sk == 1) {
+        const int a = first + at / 8, k = k0 + at % 8 * 4;
+        n = a < o.n ? K - k : 0;
+        p = o.p + long(a) * o.sa + k;
+      } else {
+        const int k = k0 + at / (ROWS / 4), a = first + at % (ROWS / 4) * 4;
+        n = k < K ? o.n - a : 0;
+        p = o.p + long(k) * o.sk + a;
+      }
+      if (n >= 4) {
+        __builtin_memcpy(&r, p, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < n) r[e] = p[e];
+      }
+      v[i] = r;
+    }
+  }
+  __device__ __forceinline__ void put(float* lds, bool rows, int tid) const {
+#pragma unroll
+    for (int i = 0; i < loads; ++i) {
+      const int at = tid + i * THREADS;
+      if (chunks % THREADS && at >= chunks) break;
+      float* d;
+      if (rows) {
+        const int a = at / 8;
+        d = lds + a * 32 + ((at % 8) ^ (a & 7)) * 4;
+      } else {
+        d = lds + at / (ROWS / 4) * (ROWS + 4) + at % (ROWS / 4) * 4;
+      }
+      *reinterpret_cast<f32x4_t*>(d) = v[i];
+    }
+  }
+};
+
+// One fragment: a lane's values for the four MFMAs of 16 of k.
+template <int ROWS>
+__device__ __forceinline__ f32x4_t frag_f32(const float* lds, bool rows, int a, int half, int lane) {
+  const int l = lane & 15, q = lane >> 4;
+  if (rows) return *reinterpret_cast<const f32x4_t*>(lds + (a + l) * 32 + (((half * 4 + q) ^ (l & 7)) * 4));
+  f32x4_t r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = lds[(half * 16 + q * 4 + e) * (ROWS + 4) + a + l];
+  return r;
+}
+
+// grid: x tiles (of b fastest), y splits of the contraction.
+template <class Sh, class Epi>
+__global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g, Epi epi, int na, int nb) {
+  extern __shared__ __align__(128) float smem_f32[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tiles_b = (nb + kTileF32 - 1) / kTileF32;
+  const int tiles_b = (nb + Sh::BN - 1) / Sh::BN;
   if (g.nb) nb = *g.nb;
   const int tile_a = blockIdx.x / tiles_b, tile_b = blockIdx.x % tiles_b;
-  const int a_first = tile_a * kTileF32, b_first = tile_b * kTileF32;
+  const int a_first = tile_a * Sh::BM, b_first = tile_b * Sh::BN;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
+  const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
+  const int T0 = (K0 + kStepF32 - 1) / kStepF32, T = T0 + (K1 + kStepF32 - 1) / kStepF32;
+  const int t_begin = int(long(T) * blockIdx.y / gridDim.y), t_end = int(long(T) * (blockIdx.y + 1) / gridDim.y);
   TileAt t;
-  t.wave_a = wave >> 1;
-  t.wave_b = wave & 1;
-  t.a0 = a_first + 64 * t.wave_a;
-  t.b0 = b_first + 64 * t.wave_b;
+  t.wave_a = wave / Sh::WB;
+  t.wave_b = wave % Sh::WB;
+  t.a0 = a_first + t.wave_a * (Sh::BM / Sh::WA);
+  t.b0 = b_first + t.wave_b * (Sh::BN / Sh::WB);
   t.nb = nb;
   t.tile_a = tile_a;
-  f32x4_t acc[4][4];
+
+  StepF32<Sh::BM, Sh::threads> sa;
+  StepF32<Sh::BN, Sh::threads> sb;
+  auto load = [&](int s) {
+    const int part = s >= T0;
+    const int k = (part ? s - T0 : s) * kStepF32, K = part ? K1 : K0;
+    sa.load(g.A[part], a_first, k, K, tid);
+    sb.load(g.B[part], b_first, k, K, tid);
+  };
+  if (t_begin < t_end) load(t_begin);
+  f32x4_t acc[Sh::FM][Sh::FN];
   epi.init(acc, t);
-  for (int part = 0; part < 2; ++part) {
-    const int K = part == 0 && g.k0 ? *g.k0 : g.K[part];
-    const Operand<T>&A = g.A[part], &B = g.B[part];
-    for (int k0 = 0; k0 < K; k0 += kTileF32K) {
-      __syncthreads();
+  for (int s = t_begin; s < t_end; ++s) {
+    const int part = s >= T0;
+    const bool rows_a = g.A[part].sk == 1, rows_b = g.B[part].sk == 1;
+    float* A = smem_f32 + (s & 1) * (Sh::stage / 4);
+    float* B = A + Sh::bytes(Sh::BM) / 4;
+    sa.put(A, rows_a, tid);
+    sb.put(B, rows_b, tid);
+    // one barrier a step: the buffer written next was read before this one
+    __syncthreads();
+    if (s + 1 < t_end) load(s + 1);
 #pragma unroll
-      for (int op = 0; op < 2; ++op) {
-        const Operand<T>& O = op ? B : A;
-        float* S = op ? Bs : As;
-        const int first = op ? b_first : a_first;
+    for (int half = 0; half < 2; ++half) {
+      f32x4_t a[Sh::FM], b[Sh::FN];
 #pragma unroll
-        for (int i = 0; i < kTileF32 * kTileF32K / 256; ++i) {
-          const int e = tid + 256 * i;
-          const int c = O.sk == 1 ? e / kTileF32K : e % kTileF32;
-          const int k = O.sk == 1 ? e % kTileF32K : e / kTileF32;
-          float v = 0.f;
-          if (first + c < O.n && k0 + k < K) v = to_f32(O.p[long(first + c) * O.sa + long(k0 + k) * O.sk]);
-          S[k * kTileF32Pad + c] = v;
-        }
-      }
-      __syncthreads();
+      for (int i = 0; i < Sh::FM; ++i)
+        a[i] = frag_f32<Sh::BM>(A, rows_a, t.wave_a * (Sh::BM / Sh::WA) + 16 * i, half, lane);
 #pragma unroll
-      for (int kk = 0; kk < kTileF32K; kk += 4) {
-        const int row = (kk + (lane >> 4)) * kTileF32Pad + (lane & 15);
-        float a[4], b[4];
+      for (int j = 0; j < Sh::FN; ++j)
+        b[j] = frag_f32<Sh::BN>(B, rows_b, t.wave_b * (Sh::BN / Sh::WB) + 16 * j, half, lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = As[row + 64 * t.wave_a + 16 * i];
-          b[i] = Bs[row + 64 * t.wave_b + 16 * i];
-        }
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Sh::FM; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[j], acc[i][j], 0, 0, 0);
-      }
+          for (int j = 0; j < Sh::FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][e], b[j][e], acc[i][j], 0, 0, 0);
     }
   }
   __syncthreads();
-  epi.done(acc, t, lds);
+  epi.done(acc, t, smem_f32);
 }
 
-template <typename T, class Epi>
-hipError_t launch_tile_f32(const Product<T>& g, const Epi& epi, int na, int nb, hipStream_t stream) {
-  if (na <= 0 || nb <= 0) return hipSuccess;
-  const unsigned tiles = unsigned((na + kTileF32 - 1) / kTileF32) * unsigned((nb + kTileF32 - 1) / kTileF32);
-  hipLaunchKernelGGL((tile_f32_kernel<T, Epi>), dim3(tiles), dim3(256), 0, stream, g, epi, na, nb);
+using WideF32 = TileF32<128, 128, 2, 2>;
+using MidF32 = TileF32<64, 64, 2, 2>;
+using SlimF32 = TileF32<64, 16, 4, 1>;
+
+// 0: few rows; 1: too few wide tiles for the compute units; 2: wide.
+inline int f32_choice(int na, int nb) {
+  if (nb <= 16) return 0;
+  const long wide = long((na + 127) / 128) * ((nb + 127) / 128);
+  return wide >= 192 ? 2 : 1;
+}
+// Splits of a contraction into fp32 sums, for about two workgroups per
+// compute unit, each with at least two steps.
+inline int f32_splits(int na, int nb, long K) {
+  const int c = f32_choice(na, nb), bm = c == 2 ? 128 : 64, bn = c == 2 ? 128 : c == 1 ? 64 : 16;
+  const long tiles = long((na + bm - 1) / bm) * ((nb + bn - 1) / bn), steps = (K + kStepF32 - 1) / kStepF32;
+  long s = 512 / tiles;
+  if (s > steps / 2) s = steps / 2;
+  return s < 1 ? 1 : s > 64 ? 64 : int(s);
+}
+
+template <class Sh, class Epi>
+hipError_t launch_tile_f32(const Product<float>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
+  const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_f32_kernel<Sh, Epi>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, Sh::lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((tile_f32_kernel<Sh, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads), Sh::lds, stream, g,
+                     epi, na, nb);
   return hipGetLastError();
+}
+
+// make(shape) gives the epilogue.
+template <class Make>
+hipError_t launch_f32(const Product<float>& g, const Make& make, int na, int nb, int splits, hipStream_t stream) {
+  if (na <= 0 || nb <= 0) return hipSuccess;
+  switch (f32_choice(na, nb)) {
+    case 0: return launch_tile_f32<SlimF32>(g, make(SlimF32()), na, nb, splits, stream);
+    case 1: return launch_tile_f32<MidF32>(g, make(MidF32()), na, nb, splits, stream);
+    default: return launch_tile_f32<WideF32>(g, make(WideF32()), na, nb, splits, stream);
+  }
 }
 
 }  // namespace dspark
