@@ -7,7 +7,9 @@ RuntimeError: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -571,12 +573,22 @@ def verify(tokens, target, lens, out=None):
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
 
+def _is(t, name, dtype, shape, device):
+    """_need() for calls of a few microseconds: one test of all that has to
+    hold, the reasons only where it does not."""
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape, device)
+
+
 def _storage(t, name):
     torch = _torch()
     _need(t, name)
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    if t.dtype is torch.bfloat16:
+        return DSPARK_BF16
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 or bfloat16")
-    return DSPARK_BF16 if t.dtype == torch.bfloat16 else DSPARK_F32
+    return DSPARK_F32
 
 
 def _act(act):
@@ -587,18 +599,29 @@ def _act(act):
 
 def _optional(t, name, dtype, shape, device):
     if t is not None:
-        _need(t, name, dtype, shape, device)
+        _is(t, name, dtype, shape, device)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(name, *sizes):
+    """dspark_<name>_workspace_bytes of these sizes."""
+    return int(getattr(load(), f"dspark_{name}_workspace_bytes")(*sizes))
+
+
+def _raw_stream(device):
+    """Handle of `device`'s current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _scratch(nbytes, device, kind, workspace):
     """(pointer, bytes) of the workspace of a call on `device`'s current stream."""
     if workspace is not None:
         _need(workspace, "workspace", _torch().uint8, None, device)
-        return _ptr(workspace), ctypes.c_size_t(workspace.numel())
+        return workspace.data_ptr(), workspace.numel()
     if nbytes == 0:
-        return _ptr(None), ctypes.c_size_t(0)
+        return None, 0
     ws = _captured(nbytes, device) or _workspace(nbytes, device, kind)
-    return _ptr(ws), ctypes.c_size_t(ws.numel())
+    return ws.data_ptr(), ws.numel()
 
 
 class _Buffer:
@@ -619,10 +642,21 @@ def _captured(nbytes, device, zero=False):
     return _Buffer((torch.zeros if zero else torch.empty)(nbytes, dtype=torch.uint8, device=device))
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(device):
     """The device the operands live on becomes the current one, so that its
     current stream takes the launches."""
-    return _torch().cuda.device(device)
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return torch.cuda.device(device)
+
+
+def _at(t):
+    """A tensor's address as the C ABI takes it (None: a null pointer)."""
+    return None if t is None else t.data_ptr()
 
 
 def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None, workspace=None):
@@ -638,7 +672,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     M, K = x.shape
     N = w.shape[0]
     dev = x.device
-    _need(w, "w", x.dtype, (N, K), dev)
+    _is(w, "w", x.dtype, (N, K), dev)
     _optional(bias, "bias", x.dtype, (N,), dev)
     _optional(residual, "residual", x.dtype, (M, N), dev)
     _optional(pre, "pre", torch.float32, (M, N), dev)
@@ -646,9 +680,9 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     a = _act(act)
     with _on(dev):
         y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
-        ws, n = _scratch(int(lib.dspark_linear_workspace_bytes(M, N, K, dt)), dev, "linear", workspace)
-        _check(lib.dspark_linear(M, N, K, dt, _ptr(x), _ptr(w), _ptr(bias), a, _ptr(residual), _ptr(y), _ptr(pre),
-                                 ws, n, _stream()))
+        ws, n = _scratch(_bytes("linear", M, N, K, dt), dev, "linear", workspace)
+        _check(lib.dspark_linear(M, N, K, dt, _at(x), _at(w), _at(bias), a, _at(residual), _at(y), _at(pre),
+                                 ws, n, _raw_stream(dev)))
     return y
 
 
@@ -662,8 +696,8 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     M, K = x.shape
     N = w.shape[0]
     dev = x.device
-    _need(w, "w", x.dtype, (N, K), dev)
-    _need(dy, "dy", x.dtype, (M, N), dev)
+    _is(w, "w", x.dtype, (N, K), dev)
+    _is(dy, "dy", x.dtype, (M, N), dev)
     a = _act(act)
     if a and pre is None:
         raise ValueError("an activation's gradient needs pre")
@@ -673,10 +707,10 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     with _on(dev):
         new = lambda name, *sh: torch.empty(sh, dtype=x.dtype, device=dev) if name in need else None  # noqa: E731
         dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
-        ws, n = _scratch(int(lib.dspark_linear_backward_workspace_bytes(M, N, K, dt)), dev, "linear_backward",
+        ws, n = _scratch(_bytes("linear_backward", M, N, K, dt), dev, "linear_backward",
                          workspace)
-        _check(lib.dspark_linear_backward(M, N, K, dt, _ptr(dy), _ptr(x), _ptr(w), a, _ptr(pre), _ptr(dx), _ptr(dw),
-                                          _ptr(db), ws, n, _stream()))
+        _check(lib.dspark_linear_backward(M, N, K, dt, _at(dy), _at(x), _at(w), a, _at(pre), _at(dx), _at(dw),
+                                          _at(db), ws, n, _raw_stream(dev)))
     return dx, dw, db
 
 
@@ -695,7 +729,7 @@ def _loss_inputs(label, U, h, Wo, prev, W1, W2):
     d = Wo.shape[1] if Wo is not None else 0
     r = W2.shape[0] if W2 is not None else 0
     dev = first.device
-    _need(label, "label", torch.int32, (N,), dev)
+    _is(label, "label", torch.int32, (N,), dev)
     _optional(U, "U", first.dtype, (N, V), dev)
     _optional(h, "h", first.dtype, (N, d), dev)
     _optional(Wo, "Wo", first.dtype, (V, d), dev)
@@ -719,11 +753,11 @@ def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out
         if out is None:
             out = (torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev))
         nll, lse = out
-        _need(nll, "nll", torch.float32, (N,), dev)
-        _need(lse, "lse", torch.float32, (N,), dev)
-        ws, n = _scratch(int(lib.dspark_markov_loss_workspace_bytes(N, V, d, r, dt)), dev, "markov_loss", workspace)
-        _check(lib.dspark_markov_loss(N, V, d, r, dt, _ptr(label), _ptr(U), _ptr(h), _ptr(Wo), _ptr(prev), _ptr(W1),
-                                      _ptr(W2), _ptr(nll), _ptr(lse), ws, n, _stream()))
+        _is(nll, "nll", torch.float32, (N,), dev)
+        _is(lse, "lse", torch.float32, (N,), dev)
+        ws, n = _scratch(_bytes("markov_loss", N, V, d, r, dt), dev, "markov_loss", workspace)
+        _check(lib.dspark_markov_loss(N, V, d, r, dt, _at(label), _at(U), _at(h), _at(Wo), _at(prev), _at(W1),
+                                      _at(W2), _at(nll), _at(lse), ws, n, _raw_stream(dev)))
     return nll, lse
 
 
@@ -736,8 +770,8 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
     torch = _torch()
     lib = load()
     N, V, d, r, dt, dev, dtype = _loss_inputs(label, U, h, Wo, prev, W1, W2)
-    _need(g, "g", torch.float32, (N,), dev)
-    _need(lse, "lse", torch.float32, (N,), dev)
+    _is(g, "g", torch.float32, (N,), dev)
+    _is(lse, "lse", torch.float32, (N,), dev)
     shapes = {}
     if U is not None:
         shapes["dU"] = (N, V)
@@ -751,11 +785,11 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
             raise ValueError(f"no input for the gradient {k}")
     with _on(dev):
         grads = {k: torch.empty(shapes[k], dtype=dtype, device=dev) for k in need}
-        ws, n = _scratch(int(lib.dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dt)), dev,
+        ws, n = _scratch(_bytes("markov_loss_backward", N, V, d, r, dt), dev,
                          "markov_loss_backward", workspace)
         _check(lib.dspark_markov_loss_backward(
-            N, V, d, r, dt, _ptr(g), _ptr(lse), _ptr(label), _ptr(U), _ptr(h), _ptr(Wo), _ptr(prev), _ptr(W1),
-            _ptr(W2), *[_ptr(grads.get(k)) for k in ("dU", "dh", "dWo", "dW1", "dW2")], ws, n, _stream()))
+            N, V, d, r, dt, _at(g), _at(lse), _at(label), _at(U), _at(h), _at(Wo), _at(prev), _at(W1),
+            _at(W2), *[_at(grads.get(k)) for k in ("dU", "dh", "dWo", "dW1", "dW2")], ws, n, _raw_stream(dev)))
     return grads
 
 

@@ -81,6 +81,78 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(int n, long ld, const bf1
   for (int i = threadIdx.x; i < ld; i += 256) d[i] = i < n ? s[i] : bf16_t(0);
 }
 
+// A few rows (M <= 16): the weights are read once, straight into the matrix
+// instruction's operand registers (a lane takes 16 bytes of one of 16 rows of
+// w), and the rows of x come the same way out of the caches.  Each of WAVES
+// waves takes a share of the contraction; LDS joins them.  16 output features
+// per workgroup.  Any K: rows need element alignment only, and the last 32 of
+// the contraction are masked.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(int M, int N, int K, const bf16_t* __restrict__ x,
+                                                              const bf16_t* __restrict__ w, LinearEpi<bf16_t> epi) {
+  __shared__ f32x4_t part[WAVES][64];
+#if defined(__HIP_DEVICE_COMPILE__)
+  // uniform: matrix instructions ignore the lane mask, so nothing around them may diverge
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int a0 = blockIdx.x * 16;
+  const int full = K / 32;   // whole steps of 32
+  const int s0 = full * wave / WAVES, s1 = full * (wave + 1) / WAVES;
+  const bf16_t* pw = w + long(min(a0 + l, N - 1)) * K + q * 8;
+  const bf16_t* px = x + long(min(l, M - 1)) * K + q * 8;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  auto step = [&](u32x4_t a, u32x4_t b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc,
+                                                  0, 0, 0);
+  };
+  int s = s0;
+  constexpr int U = 8;   // steps in flight: 8 KiB of weights per wave
+  for (; s + U <= s1; s += U) {
+    u32x4_t a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) __builtin_memcpy(&a[u], pw + (s + u) * 32, 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u) __builtin_memcpy(&b[u], px + (s + u) * 32, 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(a[u], b[u]);
+  }
+  if (s < s1) {
+    u32x4_t a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < s1) {
+        __builtin_memcpy(&a[u], pw + (s + u) * 32, 16);
+        __builtin_memcpy(&b[u], px + (s + u) * 32, 16);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < s1) step(a[u], b[u]);
+  }
+  if (wave == WAVES - 1 && full * 32 < K) {   // the rest, zero behind the row's end
+    const int n = K - full * 32 - q * 8;
+    uint32_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) {
+        a[e >> 1] |= uint32_t(pw[full * 32 + e]) << (16 * (e & 1));
+        b[e >> 1] |= uint32_t(px[full * 32 + e]) << (16 * (e & 1));
+      }
+    step(u32x4_t{a[0], a[1], a[2], a[3]}, u32x4_t{b[0], b[1], b[2], b[3]});
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) acc += part[v][lane];
+    const int a = a0 + 4 * q, n = N - a;
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    if (l < M && n > 0)
+      epi.finish(acc, epi.bias ? load4(epi.bias + a, n, epi.vec) : zero,
+                 epi.residual ? load4(epi.residual + size_t(l) * N + a, n, epi.vec) : zero, l, a, n);
+  }
+#endif
+}
+
 // y = act(sum over splits + bias) + residual, the splits in order: four
 // values per thread.
 template <typename T>
@@ -106,7 +178,7 @@ inline int dz_chunks(int M) { return int((up64(M) + kDzRows - 1) / kDzRows); }
 // Splits of a product's contraction into partial sums [split][rows][up64(na)].
 inline size_t split_bytes(int na, int nb, long K, bool bf16, bool any) {
   if (na == 0 || nb == 0) return 0;
-  const int s = bf16 ? splits_for(na, nb, K, any) : f32_splits(na, nb, K);
+  const int s = bf16 ? plan_for(na, nb, K, any, true).splits : f32_splits(na, nb, K);
   return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
 }
 
@@ -132,11 +204,12 @@ hipError_t product(const Product<T>& g, bool any, const LinearEpi<T>& epi, int n
                    hipStream_t stream) {
   if (na == 0 || nb == 0) return hipSuccess;
   constexpr bool bf16 = sizeof(T) == 2;
-  const int splits = bf16 ? splits_for(na, nb, g.K[0], any) : f32_splits(na, nb, g.K[0]);
+  const Plan plan = bf16 ? plan_for(na, nb, g.K[0], any, true) : Plan{0, f32_splits(na, nb, g.K[0])};
+  const int splits = plan.splits;
   auto run = [&](auto&& make) {
     if constexpr (bf16)
-      return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, splits, stream)
-                 : launch_bf16<LA, LA, LB, false>(g, make, na, nb, splits, stream);
+      return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, plan, stream)
+                 : launch_bf16<LA, LA, LB, false>(g, make, na, nb, plan, stream);
     else
       return launch_f32(g, make, na, nb, splits, stream);
   };
@@ -150,7 +223,27 @@ hipError_t product(const Product<T>& g, bool any, const LinearEpi<T>& epi, int n
   return hipGetLastError();
 }
 
+// Where few_rows_kernel beats the tiles (per call, in a graph): for one row
+// always (4096 x 2560: 6.0 us against 10.0, 65536 x 4096: 92 against 107); for
+// sixteen, whose rows of x come in 64-byte pieces at the same rate as the
+// weights, up to 8192 features (11.7 us against 13.3; at 16384 20.7 against
+// 19.1).  Rows that are not 16-byte aligned halve both: 8192 x 2561, one row
+// 19 us against 20, sixteen 33 against 21.
+bool few_rows(int M, int N, int K) {
+  return K % 8 == 0 ? M <= 4 || (M <= 16 && N <= 8192) : M <= 16 && N * M <= 32768;
+}
+
 hipError_t linear_bf16(const LinearArgs& a, hipStream_t stream) {
+  if (few_rows(a.M, a.N, a.K)) {
+    const bf16_t *x = static_cast<const bf16_t*>(a.x), *w = static_cast<const bf16_t*>(a.w);
+    const dim3 grid(unsigned((a.N + 15) / 16));
+    // more waves share the contraction where there are too few workgroups to fill the compute units
+    if (a.N <= 16 * 2 * kComputeUnits)
+      hipLaunchKernelGGL((few_rows_kernel<8>), grid, dim3(512), 0, stream, a.M, a.N, a.K, x, w, linear_epi<bf16_t>(a));
+    else
+      hipLaunchKernelGGL((few_rows_kernel<4>), grid, dim3(256), 0, stream, a.M, a.N, a.K, x, w, linear_epi<bf16_t>(a));
+    return hipGetLastError();
+  }
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   const bf16_t* x = static_cast<const bf16_t*>(a.x);
   long ldx = a.K;
@@ -251,6 +344,7 @@ hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
+  if (bf16 && few_rows(M, N, K)) return 0;
   return (bf16 && K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K, bf16, K % 8 != 0);
 }
 

@@ -268,7 +268,7 @@ struct Layout {
   size_t row, place, token, label, lse, g, X, W2, stat, zlab, dz, dXh, dXe, total;
   int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
   long w2_ld;                // row length of W2 as the products read it
-  int splits_h, splits_e;    // of the contraction over a piece's tokens
+  Plan h, e;                 // of the contractions over a piece's tokens
 };
 
 Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
@@ -305,15 +305,15 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     const size_t most = kPieceBytes / (size_t(L.rows) * elem);
     const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
     L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
-    auto splits = [&](int na, bool any) {
-      if (!na || !N) return 1;
-      return bf16 ? splits_for(na, N, L.width, any) : f32_splits(na, N, L.width);
+    auto plan = [&](int na, bool any) {
+      if (!na || !N) return Plan{0, 1};
+      return bf16 ? plan_for(na, N, L.width, any, true) : Plan{0, f32_splits(na, N, L.width)};
     };
-    L.splits_h = splits(d, d % 8 != 0);
-    L.splits_e = splits(r, false);
+    L.h = plan(d, d % 8 != 0);
+    L.e = plan(r, false);
     L.dz = take(size_t(L.rows) * L.width * elem);
-    L.dXh = take(size_t(L.splits_h) * L.rows * L.dp * 4);
-    L.dXe = take(size_t(L.splits_e) * L.rows * L.rp * 4);
+    L.dXh = take(size_t(L.h.splits) * L.rows * L.dp * 4);
+    L.dXe = take(size_t(L.e.splits) * L.rows * L.rp * 4);
   }
   L.total = at;
   return L;
@@ -386,15 +386,15 @@ BaseLogits<T> base_logits(const LossArgs& a, const Parts<T>& p, int v0, int nv, 
 // (layouts of the operands given), fp32 on the fp32 one.  make(shape) gives
 // the epilogue; any: rows of the a operand are not 16-byte aligned.
 template <int LA0, int LA1, int LB, class Make>
-hipError_t multiply(const Product<bf16_t>& g, bool any, const Make& make, int na, int nb, int splits,
+hipError_t multiply(const Product<bf16_t>& g, bool any, const Make& make, int na, int nb, Plan plan,
                     hipStream_t stream) {
-  return any ? launch_bf16<LA0, LA1, LB, true>(g, make, na, nb, splits, stream)
-             : launch_bf16<LA0, LA1, LB, false>(g, make, na, nb, splits, stream);
+  return any ? launch_bf16<LA0, LA1, LB, true>(g, make, na, nb, plan, stream)
+             : launch_bf16<LA0, LA1, LB, false>(g, make, na, nb, plan, stream);
 }
 template <int LA0, int LA1, int LB, class Make>
-hipError_t multiply(const Product<float>& g, bool, const Make& make, int na, int nb, int splits,
+hipError_t multiply(const Product<float>& g, bool, const Make& make, int na, int nb, Plan plan,
                     hipStream_t stream) {
-  return launch_f32(g, make, na, nb, splits, stream);
+  return launch_f32(g, make, na, nb, plan.splits, stream);
 }
 
 template <typename T>
@@ -411,7 +411,8 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
     bm = shape.BM;
     return StatsEpi<T, shape.WA, shape.BN>{base_logits(a, p, 0, a.V, nullptr), p.rows.label, stat, a.N, zlab};
   };
-  if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N, 1, stream)) != hipSuccess)
+  if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N,
+                                         plan_for(a.V, a.N, a.d + a.r, a.d % 8 != 0, false), stream)) != hipSuccess)
     return e;
   // few rows: all threads of a workgroup on one row's tiles; many: neighbours
   // in a wave read neighbouring rows
@@ -447,7 +448,8 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
     auto grad = [&](auto) {
       return GradEpi<T>{base_logits(a, p, v0, nv, dU), p.rows.label, p.rows.lse, p.rows.g, dz, L.width, dU};
     };
-    if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N, 1, stream)) != hipSuccess) return e;
+    if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N,
+                                           plan_for(nv, a.N, a.d + a.r, any, false), stream)) != hipSuccess) return e;
     const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
     if (a.dh) {
       Product<T> g = {};
@@ -456,7 +458,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       g.K[0] = nv;
       g.nb = p.count;
       auto add = [&](auto) { return AddEpi{dXh, L.dp, a.d, v0 == 0, split_h}; };
-      if ((e = multiply<kCols, kCols, kRows>(g, any, add, a.d, a.N, L.splits_h, stream)) != hipSuccess) return e;
+      if ((e = multiply<kCols, kCols, kRows>(g, any, add, a.d, a.N, L.h, stream)) != hipSuccess) return e;
     }
     if (a.dW1) {
       Product<T> g = {};
@@ -465,7 +467,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       g.K[0] = nv;
       g.nb = p.count;
       auto add = [&](auto) { return AddEpi{dXe, L.rp, a.r, v0 == 0, split_e}; };
-      if ((e = multiply<kRows, kRows, kRows>(g, false, add, a.r, a.N, L.splits_e, stream)) != hipSuccess) return e;
+      if ((e = multiply<kRows, kRows, kRows>(g, false, add, a.r, a.N, L.e, stream)) != hipSuccess) return e;
     }
     if (dWo) {
       Product<T> g = {};
@@ -474,7 +476,8 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       g.k0 = p.count;
       const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(dWo) % (4 * sizeof(T)) == 0;
       auto store = [&](auto) { return StoreEpi<T>{dWo + size_t(v0) * a.d, a.d, a.d, vec}; };
-      if ((e = multiply<kCols, kCols, kCols>(g, false, store, a.d, nv, 1, stream)) != hipSuccess) return e;
+      if ((e = multiply<kCols, kCols, kCols>(g, false, store, a.d, nv,
+                                             plan_for(a.d, nv, a.N, false, false), stream)) != hipSuccess) return e;
     }
     if (dW2) {
       Product<T> g = {};
@@ -483,17 +486,18 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       g.k0 = p.count;
       const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(dW2) % (4 * sizeof(T)) == 0;
       auto store = [&](auto) { return StoreEpi<T>{dW2 + v0, a.V, nv, vec}; };
-      if ((e = multiply<kCols, kCols, kCols>(g, false, store, nv, a.r, 1, stream)) != hipSuccess) return e;
+      if ((e = multiply<kCols, kCols, kCols>(g, false, store, nv, a.r,
+                                             plan_for(nv, a.r, a.N, false, false), stream)) != hipSuccess) return e;
     }
   }
   if (a.dh && a.N)
-    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(L.dp), L.splits_h, split_h,
+    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(L.dp), L.h.splits, split_h,
                        p.place, dXh, static_cast<T*>(a.dh));
   if (a.dW1) {
     hipLaunchKernelGGL((zero_kernel<T>), dim3(2048), dim3(256), 0, stream, size_t(a.V) * a.r, static_cast<T*>(a.dW1));
     if (a.N) {
-      if (L.splits_e > 1)
-        hipLaunchKernelGGL(join_e_kernel, dim3(unsigned(a.N)), dim3(256), 0, stream, long(L.rp), L.splits_e, split_e,
+      if (L.e.splits > 1)
+        hipLaunchKernelGGL(join_e_kernel, dim3(unsigned(a.N)), dim3(256), 0, stream, long(L.rp), L.e.splits, split_e,
                            p.count, dXe);
       hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned(a.N)), dim3(1024), 0, stream, a.r, long(L.rp), p.count,
                          p.rows.token, dXe, static_cast<T*>(a.dW1));

@@ -562,62 +562,63 @@ using Tile64Any = TileShape<128, 64, 2, 2, 64, 2>;
 
 constexpr int kComputeUnits = 256;
 
-inline int tiles_of(int na, int nb, int bm, int bn) {
-  const long n = long((na + bm - 1) / bm) * ((nb + bn - 1) / bn);
-  return n > 1 << 30 ? 1 << 30 : int(n);
-}
-// 0..4: index of the tile for na x nb outputs; any: register staging, which
-// the large tile has no registers left for.
-inline int tile_choice(int na, int nb, bool any) {
-  if (nb <= 16) return 0;
-  if (nb <= 32) return 1;
-  if (nb <= 64) return 2;
-  if (any) return 3;
-  return tiles_of(na, nb, 256, 256) >= 3 * kComputeUnits / 4 ? 4 : 3;
-}
-inline int tile_bm(int choice) { return choice == 4 ? 256 : 128; }
-inline int tile_bn(int choice) { return choice == 4 ? 256 : choice == 3 ? 128 : 16 << choice; }
+// Which tile a product takes (0 .. 4: Tile16 .. Tile256) and into how many
+// fp32 sums its contraction is split.
+struct Plan {
+  int tile, splits;
+};
 
-// Splits of a contraction of K values whose products are summed in fp32
-// afterwards.  A compute unit works through its tiles one after the other (two
-// side by side with the smaller tiles), so the time goes with the number of
-// rounds, which splits make finer; each costs the writing and reading of its
-// tile in fp32, about what twelve steps of a 256 x 256 tile take.
-inline int splits_for(int na, int nb, long K, bool any) {
-  const int c = tile_choice(na, nb, any);
-  const long tiles = tiles_of(na, nb, tile_bm(c), tile_bn(c)), slots = c == 4 ? kComputeUnits : 2 * kComputeUnits;
+// any: register staging, which the large tile has no registers left for.
+// split: the caller can join split sums.
+//
+// A compute unit works through its tiles one after the other (two of the
+// smaller ones side by side), so the time goes with the number of rounds.
+// In units of a step of the 256 x 256 tile (1.64 us at 8192^3), a round of
+// that tile takes its steps and 5 for its ends; two 128 x 128 tiles side by
+// side take 0.6 a step and 3.  (8192^3: 840 us against 1000; 4096 x 5120 x
+// 5120, 320 large tiles on 256 units: 268 against 248.)  A split costs the
+// writing and reading of its tile in fp32: 12 and 4.
+inline Plan plan_for(int na, int nb, long K, bool any, bool split) {
   const long steps = (K + kStep - 1) / kStep;
-  const double extra = c == 4 ? 12 : 4;
-  int best = 1;
-  double least = double((tiles + slots - 1) / slots) * (steps + (K > 0 ? 0 : 1));
-  for (int s = 2; s <= 64 && s * 4 <= steps; ++s) {
-    const double cost = double((tiles * s + slots - 1) / slots) * ((steps + s - 1) / s + extra);
-    if (cost < least * 0.97) {
-      least = cost;
-      best = s;
+  const int first = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3, last = first < 3 || any ? first : 4;
+  Plan best = {first, 1};
+  double least = 1e300;
+  for (int c = last; c >= first; --c) {
+    const bool large = c == 4;
+    const long bm = large ? 256 : 128, bn = large ? 256 : 16l << c, slots = (large ? 1 : 2) * kComputeUnits;
+    const long tiles = ((na + bm - 1) / bm) * ((nb + bn - 1) / bn);
+    for (int s = 1; s <= 64 && (s == 1 || (split && s * 4 <= steps)); ++s) {
+      const double rounds = double((tiles * s + slots - 1) / slots);
+      const double steps_s = double((steps + s - 1) / s);
+      const double cost = rounds * (large ? steps_s + 5 + (s > 1 ? 12 : 0) : 0.6 * steps_s + 3 + (s > 1 ? 4 : 0));
+      if (cost < least * 0.97) {
+        least = cost;
+        best = {c, s};
+      }
     }
   }
   return best;
 }
 
-// MakeEpi<Shape>()(…) gives the epilogue for a tile shape (its statistics
-// depend on the shape).
-template <int LA0, int LA1, int LB, bool ANY, class MakeEpi>
-hipError_t launch_bf16(const Product<bf16_t>& g, const MakeEpi& make, int na, int nb, int splits, hipStream_t stream) {
+// make(shape) gives the epilogue for a tile shape (its statistics depend on
+// the shape).
+template <int LA0, int LA1, int LB, bool ANY, class Make>
+hipError_t launch_bf16(const Product<bf16_t>& g, const Make& make, int na, int nb, Plan plan, hipStream_t stream) {
+  const int s = plan.splits;
   if constexpr (ANY) {
-    switch (tile_choice(na, nb, ANY)) {
-      case 0: return launch_tile_bf16<Tile16Any, LA0, LA1, LB, true>(g, make(Tile16Any()), na, nb, splits, stream);
-      case 1: return launch_tile_bf16<Tile32Any, LA0, LA1, LB, true>(g, make(Tile32Any()), na, nb, splits, stream);
-      case 2: return launch_tile_bf16<Tile64Any, LA0, LA1, LB, true>(g, make(Tile64Any()), na, nb, splits, stream);
-      default: return launch_tile_bf16<Tile128, LA0, LA1, LB, true>(g, make(Tile128()), na, nb, splits, stream);
+    switch (plan.tile) {
+      case 0: return launch_tile_bf16<Tile16Any, LA0, LA1, LB, true>(g, make(Tile16Any()), na, nb, s, stream);
+      case 1: return launch_tile_bf16<Tile32Any, LA0, LA1, LB, true>(g, make(Tile32Any()), na, nb, s, stream);
+      case 2: return launch_tile_bf16<Tile64Any, LA0, LA1, LB, true>(g, make(Tile64Any()), na, nb, s, stream);
+      default: return launch_tile_bf16<Tile128, LA0, LA1, LB, true>(g, make(Tile128()), na, nb, s, stream);
     }
   } else {
-    switch (tile_choice(na, nb, ANY)) {
-      case 0: return launch_tile_bf16<Tile16, LA0, LA1, LB, false>(g, make(Tile16()), na, nb, splits, stream);
-      case 1: return launch_tile_bf16<Tile32, LA0, LA1, LB, false>(g, make(Tile32()), na, nb, splits, stream);
-      case 2: return launch_tile_bf16<Tile64, LA0, LA1, LB, false>(g, make(Tile64()), na, nb, splits, stream);
-      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, splits, stream);
-      default: return launch_tile256<LA0, LA1, LB>(g, make(Tile256()), na, nb, splits, stream);
+    switch (plan.tile) {
+      case 0: return launch_tile_bf16<Tile16, LA0, LA1, LB, false>(g, make(Tile16()), na, nb, s, stream);
+      case 1: return launch_tile_bf16<Tile32, LA0, LA1, LB, false>(g, make(Tile32()), na, nb, s, stream);
+      case 2: return launch_tile_bf16<Tile64, LA0, LA1, LB, false>(g, make(Tile64()), na, nb, s, stream);
+      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, s, stream);
+      default: return launch_tile256<LA0, LA1, LB>(g, make(Tile256()), na, nb, s, stream);
     }
   }
 }

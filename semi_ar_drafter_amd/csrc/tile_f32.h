@@ -93,7 +93,7 @@ __device__ __forceinline__ f32x4_t frag_f32(const float* lds, bool rows, int a, 
 template <class Sh, class Epi>
 __global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g, Epi epi, int na, int nb) {
   extern __shared__ __align__(128) float smem_f32[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_b = (nb + Sh::BN - 1) / Sh::BN;
   if (g.nb) nb = *g.nb;
   const int tile_a = blockIdx.x / tiles_b, tile_b = blockIdx.x % tiles_b;
