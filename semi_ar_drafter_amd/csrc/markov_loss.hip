@@ -71,37 +71,113 @@ struct RowData {
   float *lse, *g;
 };
 
-// X[i] = [h[row[i]] | 0 | W1[prev[row[i]]] | 0]; rows from count up to the
-// next multiple of 64 are zero.  rows.token[i] = prev[row[i]], clamped; label,
-// lse and g of the row.  One workgroup per row.
+constexpr int kCountRows = 8192;   // up to so many rows, prepare_kernel counts for itself
+constexpr int kFillBytes = 256 * 16 * 8;   // zeros per workgroup of prepare_kernel
+
 template <typename T>
-__global__ __launch_bounds__(256) void gather_kernel(int V, int d, int dp, int r, int rp, const int* __restrict__ count,
-                                                     const int* __restrict__ row, const int* __restrict__ prev,
-                                                     const T* __restrict__ h, const T* __restrict__ W1,
-                                                     T* __restrict__ X, RowData rows) {
-  const int i = blockIdx.x, n = *count;
-  if (i >= ((n + 63) & ~63)) return;
-  T* x = X + size_t(i) * (dp + rp);
-  const bool used = i < n;
-  const int src = used ? row[i] : 0;
+struct PrepareArgs {
+  int N, V, d, dp, r, rp;
+  int *count, *row, *place;
+  const int* prev;
+  const T *h, *W1;
+  T* X;
+  RowData rows;
+  T* dU;          // rows without a label get zeros (nullptr: no dU)
+  T* dz;          // rows from count to the next multiple of 64 get zeros (nullptr: none)
+  long width;     // of dz
+  T* dW1;         // cleared (nullptr: none)
+  size_t dW1_n;
+  bool counted;   // compact_kernel has filled count, row and place
+};
+
+__device__ __forceinline__ int labels_in(const int* label, int n, int V, int* sums) {
+  int c = 0;
+  for (int i = threadIdx.x; i < n; i += 256) c += unsigned(label[i]) < unsigned(V);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) c += __shfl_xor(c, m, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = c;
+  __syncthreads();
+  return sums[0] + sums[1] + sums[2] + sums[3];
+}
+
+// A workgroup's share of zeros from p on, n values: 16 bytes at a time where
+// they are aligned.
+template <typename T>
+__device__ __forceinline__ void fill_share(T* p, size_t n, int part, int parts) {
+  const size_t per = (n + parts - 1) / parts, at = ((per + 15) & ~size_t(15)) * part;
+  const size_t end = min(n, at + ((per + 15) & ~size_t(15)));
+  if (reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    constexpr int V = 16 / sizeof(T);
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    for (size_t i = at + size_t(threadIdx.x) * V; i + V <= end; i += 256 * V) *reinterpret_cast<u32x4_t*>(p + i) = zero;
+    for (size_t i = (end > at ? at + (end - at) / V * V : end) + threadIdx.x; i < end; i += 256) p[i] = from_f32<T>(0.f);
+  } else {
+    for (size_t i = at + threadIdx.x; i < end; i += 256) p[i] = from_f32<T>(0.f);
+  }
+}
+
+// All that comes before the products, in one launch.  Workgroup n < N: row n
+// takes its place i among the rows in use (their number before it) and writes
+// X[i] = [h[n] | 0 | W1[prev[n]] | 0] and the row's label, token, lse and g;
+// the next 64: rows of X from count up to the next multiple of 64 are zero;
+// the rest: zeros elsewhere.
+template <typename T>
+__global__ __launch_bounds__(256) void prepare_kernel(PrepareArgs<T> p) {
+  __shared__ int sums[4];
+  const int n = blockIdx.x, tid = threadIdx.x;
   const T zero = from_f32<T>(0.f);
-  if (used && threadIdx.x == 0) {
-    rows.label[i] = rows.label_in[src];
-    if (rows.lse_in) {
-      rows.lse[i] = rows.lse_in[src];
-      rows.g[i] = rows.g_in[src];
+  if (n < p.N) {
+    const int y = p.rows.label_in[n];
+    const bool used = unsigned(y) < unsigned(p.V);
+    int i;
+    if (p.counted) {
+      i = p.place[n];
+    } else {
+      i = labels_in(p.rows.label_in, n, p.V, sums);
+      if (tid == 0) {
+        p.place[n] = used ? i : -1;
+        if (used) p.row[i] = n;
+        if (n == p.N - 1) *p.count = i + used;
+      }
     }
+    if (!used) {
+      if (p.dU) {
+        T* u = p.dU + size_t(n) * p.V;
+        for (int v = tid; v < p.V; v += 256) u[v] = zero;
+      }
+      return;
+    }
+    if (tid == 0) {
+      p.rows.label[i] = y;
+      if (p.rows.lse_in) {
+        p.rows.lse[i] = p.rows.lse_in[n];
+        p.rows.g[i] = p.rows.g_in[n];
+      }
+    }
+    T* x = p.X + size_t(i) * (p.dp + p.rp);
+    const T* hr = p.h + size_t(n) * p.d;
+    for (int c = tid; c < p.dp; c += 256) x[c] = c < p.d ? hr[c] : zero;
+    if (p.rp) {
+      const int t = min(max(p.prev[n], 0), p.V - 1);
+      if (tid == 0) p.rows.token[i] = t;
+      const T* wr = p.W1 + size_t(t) * p.r;
+      for (int c = tid; c < p.rp; c += 256) x[p.dp + c] = c < p.r ? wr[c] : zero;
+    }
+    return;
   }
-  if (dp) {
-    const T* hr = h + size_t(src) * d;
-    for (int c = threadIdx.x; c < dp; c += 256) x[c] = used && c < d ? hr[c] : zero;
+  const int total = p.counted ? *p.count : labels_in(p.rows.label_in, p.N, p.V, sums);
+  const int end = (total + 63) & ~63;
+  if (n < p.N + 64) {
+    const int i = total + n - p.N;
+    if (i >= end) return;
+    T* x = p.X + size_t(i) * (p.dp + p.rp);
+    for (int c = tid; c < p.dp + p.rp; c += 256) x[c] = zero;
+    return;
   }
-  if (rp) {
-    const int t = used ? min(max(prev[src], 0), V - 1) : 0;
-    if (used && threadIdx.x == 0) rows.token[i] = t;
-    const T* wr = W1 + size_t(t) * r;
-    for (int c = threadIdx.x; c < rp; c += 256) x[dp + c] = used && c < r ? wr[c] : zero;
-  }
+  const int part = n - p.N - 64, parts = gridDim.x - p.N - 64;
+  if (p.dz) fill_share(p.dz + size_t(total) * p.width, size_t(end - total) * p.width, part, parts);
+  if (p.dW1) fill_share(p.dW1, p.dW1_n, part, parts);
 }
 
 // lse and nll of every row from the tiles' statistics, in a fixed order: LANES
@@ -146,35 +222,12 @@ __global__ __launch_bounds__(256) void join_kernel(int N, int tiles, const int* 
   }
 }
 
-// Rows of dU without a label are zero.
-template <typename T>
-__global__ __launch_bounds__(256) void zero_rows_kernel(int V, const int* __restrict__ place, T* __restrict__ dU) {
-  if (place[blockIdx.x] >= 0) return;
-  T* u = dU + size_t(blockIdx.x) * V;
-  for (int v = threadIdx.x; v < V; v += 256) u[v] = from_f32<T>(0.f);
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void zero_kernel(size_t n, T* __restrict__ p) {
-  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256) p[i] = from_f32<T>(0.f);
-}
-
-// Rows of dz from count up to the next multiple of 64 are zero: they end the
-// contraction over rows.  grid: (values / 2048, 64).
-template <typename T>
-__global__ __launch_bounds__(256) void zero_dz_kernel(const int* __restrict__ count, long width, T* __restrict__ dz) {
-  const int n = *count, row = n + blockIdx.y;
-  if (row >= ((n + 63) & ~63)) return;
-  const long end = min(width, long(blockIdx.x + 1) * 2048);
-  for (long v = long(blockIdx.x) * 2048 + threadIdx.x; v < end; v += 256) dz[size_t(row) * width + v] = from_f32<T>(0.f);
-}
-
 // dh[n] = the row's sum over splits, in order; zero for rows without a label.
 template <typename T>
-__global__ __launch_bounds__(256) void dh_kernel(int d, long ld, int splits, long split, const int* __restrict__ place,
-                                                 const float* __restrict__ dX, T* __restrict__ dh) {
-  const int n = blockIdx.x, i = place[n];
-  for (int c = threadIdx.x; c < d; c += 256) {
+__device__ __forceinline__ void dh_row(int n, int d, long ld, int splits, long split, const int* place,
+                                       const float* dX, T* dh) {
+  const int i = place[n];
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
     float v = 0.f;
     if (i >= 0) {
 #pragma unroll 8
@@ -184,10 +237,18 @@ __global__ __launch_bounds__(256) void dh_kernel(int d, long ld, int splits, lon
   }
 }
 
-// dE of every row in use: its splits, in order, into the first one's place.
-__global__ __launch_bounds__(256) void join_e_kernel(long ld, int splits, long split, const int* __restrict__ count,
-                                                     float* __restrict__ dE) {
-  const int i = blockIdx.x;
+// Workgroup n < N: dh[n] (if asked for); the others: dE of every row in use,
+// its splits, in order, into the first one's place.
+template <typename T>
+__global__ __launch_bounds__(256) void join_rows_kernel(int N, int d, long ld_h, int splits_h, long split_h,
+                                                        const int* __restrict__ place, const float* __restrict__ dX,
+                                                        T* __restrict__ dh, long ld, int splits, long split,
+                                                        const int* __restrict__ count, float* __restrict__ dE) {
+  if (int(blockIdx.x) < N) {
+    if (dh) dh_row(blockIdx.x, d, ld_h, splits_h, split_h, place, dX, dh);
+    return;
+  }
+  const int i = blockIdx.x - N;
   if (i >= *count) return;
   for (int c = threadIdx.x; c < ld; c += 256) {
     float v = 0.f;
@@ -201,12 +262,18 @@ __global__ __launch_bounds__(256) void join_e_kernel(long ld, int splits, long s
 // per row; the token's first row does the sum (the table was zeroed before).
 // Its rows are listed in LDS, kSegment rows at a time, and added in four
 // interleaved sums (a frequent token has hundreds of rows: their loads are
-// all independent), joined in order.
+// all independent), joined in order.  A second run of N workgroups does dh.
 constexpr int kSegment = 2048;
 template <typename T>
-__global__ __launch_bounds__(1024) void dw1_kernel(int r, long ld, const int* __restrict__ count,
+__global__ __launch_bounds__(1024) void dw1_kernel(int N, int r, long ld, const int* __restrict__ count,
                                                    const int* __restrict__ token, const float* __restrict__ dE,
-                                                   T* __restrict__ dW1) {
+                                                   T* __restrict__ dW1, int d, long ld_h, int splits_h, long split_h,
+                                                   const int* __restrict__ place, const float* __restrict__ dX,
+                                                   T* __restrict__ dh) {
+  if (int(blockIdx.x) >= N) {
+    dh_row(blockIdx.x - N, d, ld_h, splits_h, split_h, place, dX, dh);
+    return;
+  }
   __shared__ int list[kSegment];
   __shared__ int found, waves[16];
   __shared__ float sums[1024];
@@ -330,7 +397,7 @@ struct Parts {
 };
 
 template <typename T>
-hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t stream) {
+hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, PrepareArgs<T> pre, hipStream_t stream) {
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   p.L = L;
   p.count = reinterpret_cast<int*>(ws);
@@ -346,10 +413,27 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, hipStream_t st
   p.X = reinterpret_cast<T*>(ws + L.X);
   p.W2 = static_cast<const T*>(a.W2);
   p.kx = L.dp + L.rp;
-  hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
-  if (a.N)
-    hipLaunchKernelGGL((gather_kernel<T>), dim3(unsigned(up(a.N, 64))), dim3(256), 0, stream, a.V, a.d, L.dp, a.r,
-                       L.rp, p.count, p.row, a.prev, static_cast<const T*>(a.h), static_cast<const T*>(a.W1), p.X, p.rows);
+  const size_t fills = (pre.dW1 ? pre.dW1_n * sizeof(T) : 0) + (pre.dz ? size_t(64) * pre.width * sizeof(T) : 0);
+  size_t parts = (fills + kFillBytes - 1) / kFillBytes;
+  if (parts > 2048) parts = 2048;
+  pre.N = a.N;
+  pre.V = a.V;
+  pre.d = a.d;
+  pre.dp = L.dp;
+  pre.r = a.r;
+  pre.rp = L.rp;
+  pre.count = p.count;
+  pre.row = p.row;
+  pre.place = p.place;
+  pre.prev = a.prev;
+  pre.h = static_cast<const T*>(a.h);
+  pre.W1 = static_cast<const T*>(a.W1);
+  pre.X = p.X;
+  pre.rows = p.rows;
+  pre.counted = a.N > kCountRows || a.N == 0;
+  if (pre.counted)
+    hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
+  hipLaunchKernelGGL((prepare_kernel<T>), dim3(unsigned(a.N + 64 + parts)), dim3(256), 0, stream, pre);
   if (L.W2) {
     p.W2 = reinterpret_cast<T*>(ws + L.W2);
     hipLaunchKernelGGL(pad_w2_kernel, dim3(unsigned((L.w2_ld + 1023) / 1024), unsigned(a.r)), dim3(256), 0, stream,
@@ -401,7 +485,7 @@ template <typename T>
 hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
   const Layout L = layout(a.N, a.V, a.d, a.r, a.bf16, false);
   Parts<T> p;
-  hipError_t e = start(a, L, p, stream);
+  hipError_t e = start(a, L, p, PrepareArgs<T>{}, stream);
   if (e != hipSuccess) return e;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   float2* stat = reinterpret_cast<float2*>(ws + L.stat);
@@ -430,19 +514,23 @@ template <typename T>
 hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
   const Layout L = layout(a.N, a.V, a.d, a.r, a.bf16, true);
   Parts<T> p;
-  hipError_t e = start(a, L, p, stream);
-  if (e != hipSuccess) return e;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
   T* dz = reinterpret_cast<T*>(ws + L.dz);
   float *dXh = reinterpret_cast<float*>(ws + L.dXh), *dXe = reinterpret_cast<float*>(ws + L.dXe);
   const long split_h = long(L.rows) * L.dp, split_e = long(L.rows) * L.rp;
-  T *dU = static_cast<T*>(a.dU), *dWo = static_cast<T*>(a.dWo), *dW2 = static_cast<T*>(a.dW2);
+  T *dU = static_cast<T*>(a.dU), *dh = static_cast<T*>(a.dh), *dWo = static_cast<T*>(a.dWo);
+  T *dW1 = static_cast<T*>(a.dW1), *dW2 = static_cast<T*>(a.dW2);
   const bool any = a.d % 8 != 0;
-  if (dU && a.N)
-    hipLaunchKernelGGL((zero_rows_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.V, p.place, dU);
-  if (dWo || dW2)
-    hipLaunchKernelGGL((zero_dz_kernel<T>), dim3(unsigned(L.width + 2047) / 2048, 64), dim3(256), 0, stream, p.count,
-                       long(L.width), dz);
+  PrepareArgs<T> pre = {};
+  pre.dU = dU;
+  if (a.bf16 && (dWo || dW2)) {   // the bf16 products take whole steps of rows
+    pre.dz = dz;
+    pre.width = L.width;
+  }
+  pre.dW1 = dW1;
+  pre.dW1_n = size_t(a.V) * a.r;
+  hipError_t e = start(a, L, p, pre, stream);
+  if (e != hipSuccess) return e;
   for (int v0 = 0; v0 < a.V; v0 += L.width) {
     const int nv = a.V - v0 < L.width ? a.V - v0 : L.width;
     auto grad = [&](auto) {
@@ -451,7 +539,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
     if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N,
                                            plan_for(nv, a.N, a.d + a.r, any, false), stream)) != hipSuccess) return e;
     const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
-    if (a.dh) {
+    if (dh) {
       Product<T> g = {};
       g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, 1, a.d, a.d};
       g.B[0] = dz_rows;
@@ -460,7 +548,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       auto add = [&](auto) { return AddEpi{dXh, L.dp, a.d, v0 == 0, split_h}; };
       if ((e = multiply<kCols, kCols, kRows>(g, any, add, a.d, a.N, L.h, stream)) != hipSuccess) return e;
     }
-    if (a.dW1) {
+    if (dW1) {
       Product<T> g = {};
       g.A[0] = {p.W2 + v0, L.w2_ld, 1, a.r};
       g.B[0] = dz_rows;
@@ -490,19 +578,17 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
                                              plan_for(nv, a.r, a.N, false, false), stream)) != hipSuccess) return e;
     }
   }
-  if (a.dh && a.N)
-    hipLaunchKernelGGL((dh_kernel<T>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.d, long(L.dp), L.h.splits, split_h,
-                       p.place, dXh, static_cast<T*>(a.dh));
-  if (a.dW1) {
-    hipLaunchKernelGGL((zero_kernel<T>), dim3(2048), dim3(256), 0, stream, size_t(a.V) * a.r, static_cast<T*>(a.dW1));
-    if (a.N) {
-      if (L.e.splits > 1)
-        hipLaunchKernelGGL(join_e_kernel, dim3(unsigned(a.N)), dim3(256), 0, stream, long(L.rp), L.e.splits, split_e,
-                           p.count, dXe);
-      hipLaunchKernelGGL((dw1_kernel<T>), dim3(unsigned(a.N)), dim3(1024), 0, stream, a.r, long(L.rp), p.count,
-                         p.rows.token, dXe, static_cast<T*>(a.dW1));
-    }
-  }
+  if (a.N == 0) return hipSuccess;
+  const unsigned rows = unsigned(a.N);
+  const bool join_e = dW1 && L.e.splits > 1;
+  if (join_e || (dh && !dW1))
+    hipLaunchKernelGGL((join_rows_kernel<T>), dim3(join_e ? 2 * rows : rows), dim3(256), 0, stream, a.N, a.d,
+                       long(L.dp), L.h.splits, split_h, p.place, dXh, dh, long(L.rp), L.e.splits, split_e, p.count,
+                       dXe);
+  if (dW1)
+    hipLaunchKernelGGL((dw1_kernel<T>), dim3(dh && !join_e ? 2 * rows : rows), dim3(1024), 0, stream, a.N, a.r,
+                       long(L.rp), p.count, p.rows.token, dXe, dW1, a.d, long(L.dp), L.h.splits, split_h, p.place, dXh,
+                       dh);
   return hipGetLastError();
 }
 
