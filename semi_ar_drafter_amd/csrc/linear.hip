@@ -14,7 +14,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kDzRows = 32;   // rows per workgroup of dz_kernel
+constexpr int kDzRows = 16;   // rows per workgroup of dz_kernel where it sums, 4 where it does not
 
 // dz[m][n] = T(dy act'(pre)) into rows of ld values (columns N..ld and rows
 // M..rows zero), and part[chunk][n] = the chunk's sum of dz over its rows, in
@@ -23,9 +23,9 @@ constexpr int kDzRows = 32;   // rows per workgroup of dz_kernel
 template <typename T>
 __global__ __launch_bounds__(256) void dz_kernel(int M, int rows, int N, int act, const T* __restrict__ dy,
                                                  const float* __restrict__ pre, T* __restrict__ dz, long ld,
-                                                 float* __restrict__ part, bool vec) {
+                                                 float* __restrict__ part, bool vec, int per) {
   const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
-  const int m0 = blockIdx.y * kDzRows, m1 = min(rows, m0 + kDzRows);
+  const int m0 = blockIdx.y * per, m1 = min(rows, m0 + per);
   if (n >= ld) return;
   const int left = N - n;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
@@ -70,15 +70,6 @@ __global__ __launch_bounds__(256) void dbias_kernel(int N, int chunks, const flo
     for (int i = 1; i < 8; ++i) s += sums[i][c];
     dbias[n] = from_f32<T>(s);
   }
-}
-
-// dst[r][0..ld) = src[r][0..n), zeros behind: rows whose length is no multiple
-// of a step, copied for the bf16 kernels.  One workgroup per row.
-__global__ __launch_bounds__(256) void pad_rows_kernel(int n, long ld, const bf16_t* __restrict__ src,
-                                                       bf16_t* __restrict__ dst) {
-  const bf16_t* s = src + size_t(blockIdx.x) * n;
-  bf16_t* d = dst + size_t(blockIdx.x) * ld;
-  for (int i = threadIdx.x; i < ld; i += 256) d[i] = i < n ? s[i] : bf16_t(0);
 }
 
 // A few rows (M <= 16): the weights are read once, straight into the matrix
@@ -176,9 +167,9 @@ inline long dz_stride(int N) { return up64(N); }
 inline int dz_chunks(int M) { return int((up64(M) + kDzRows - 1) / kDzRows); }
 
 // Splits of a product's contraction into partial sums [split][rows][up64(na)].
-inline size_t split_bytes(int na, int nb, long K, bool bf16, bool any) {
+inline size_t split_bytes(int na, int nb, long K, bool bf16, bool any, bool cols) {
   if (na == 0 || nb == 0) return 0;
-  const int s = bf16 ? plan_for(na, nb, K, any, true).splits : f32_splits(na, nb, K);
+  const int s = bf16 ? plan_for(na, nb, K, any, cols, true).splits : f32_splits(na, nb, K);
   return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
 }
 
@@ -204,7 +195,7 @@ hipError_t product(const Product<T>& g, bool any, const LinearEpi<T>& epi, int n
                    hipStream_t stream) {
   if (na == 0 || nb == 0) return hipSuccess;
   constexpr bool bf16 = sizeof(T) == 2;
-  const Plan plan = bf16 ? plan_for(na, nb, g.K[0], any, true) : Plan{0, f32_splits(na, nb, g.K[0])};
+  const Plan plan = bf16 ? plan_for(na, nb, g.K[0], any, LA == kCols, true) : Plan{0, f32_splits(na, nb, g.K[0])};
   const int splits = plan.splits;
   auto run = [&](auto&& make) {
     if constexpr (bf16)
@@ -233,6 +224,14 @@ bool few_rows(int M, int N, int K) {
   return K % 8 == 0 ? M <= 4 || (M <= 16 && N <= 8192) : M <= 16 && N * M <= 32768;
 }
 
+// Whether a product's a operand of `rows` rows of K values is copied to
+// aligned rows: only for many b (77 x 1027 x 1001, split: 17.1 us without,
+// 19.8 with the copy).
+bool copies(int rows, int K, int nb) { return K % 8 != 0 && nb >= 256 && size_t(rows) * up64(K) * 2 <= kCopyBytes; }
+// Bytes of the copy, and whether the product still sees unaligned rows.
+size_t copy_bytes(int rows, int K, int nb) { return copies(rows, K, nb) ? up256(size_t(rows) * up64(K) * 2) : 0; }
+bool stays_any(int rows, int K, int nb) { return K % 8 != 0 && !copies(rows, K, nb); }
+
 hipError_t linear_bf16(const LinearArgs& a, hipStream_t stream) {
   if (few_rows(a.M, a.N, a.K)) {
     const bf16_t *x = static_cast<const bf16_t*>(a.x), *w = static_cast<const bf16_t*>(a.w);
@@ -251,14 +250,25 @@ hipError_t linear_bf16(const LinearArgs& a, hipStream_t stream) {
     ldx = up64(a.K);
     bf16_t* xp = reinterpret_cast<bf16_t*>(ws);
     ws += up256(size_t(a.M) * ldx * 2);
-    hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(a.M)), dim3(256), 0, stream, a.K, ldx, x, xp);
+    const hipError_t e = pad_rows(a.M, a.K, ldx, x, xp, stream);
+    if (e != hipSuccess) return e;
     x = xp;
   }
+  const bf16_t* w = static_cast<const bf16_t*>(a.w);
+  long ldw = a.K;
+  if (copies(a.N, a.K, a.M)) {
+    ldw = up64(a.K);
+    bf16_t* wp = reinterpret_cast<bf16_t*>(ws);
+    ws += up256(size_t(a.N) * ldw * 2);
+    const hipError_t e = pad_rows(a.N, a.K, ldw, w, wp, stream);
+    if (e != hipSuccess) return e;
+    w = wp;
+  }
   Product<bf16_t> g = {};
-  g.A[0] = {static_cast<const bf16_t*>(a.w), a.K, 1, a.N};
+  g.A[0] = {w, ldw, 1, a.N};
   g.B[0] = {x, ldx, 1, a.M};
   g.K[0] = a.K;
-  return product<kRows, kRows>(g, a.K % 8 != 0, linear_epi<bf16_t>(a), a.N, a.M, reinterpret_cast<float*>(ws), stream);
+  return product<kRows, kRows>(g, ldw % 8 != 0, linear_epi<bf16_t>(a), a.N, a.M, reinterpret_cast<float*>(ws), stream);
 }
 
 hipError_t linear_f32(const LinearArgs& a, hipStream_t stream) {
@@ -286,11 +296,13 @@ hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** 
     *dz = out;
   }
   if (a.N == 0) return hipSuccess;
+  // more rows per workgroup where the grid's second axis would not hold them
+  const int per = rows > 65535 * 4 ? kDzRows : a.dbias ? kDzRows : 4;
   if (rows > 0 && (copy || a.dbias))
-    hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 1023) / 1024), unsigned((rows + kDzRows - 1) / kDzRows)),
+    hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 1023) / 1024), unsigned((rows + per - 1) / per)),
                        dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, out, *ld,
                        a.dbias ? part : nullptr,
-                       a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0);
+                       a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0, per);
   if (a.dbias)
     hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 31) / 32)), dim3(256), 0, stream, a.N,
                        rows > 0 ? int((rows + kDzRows - 1) / kDzRows) : 0, part, static_cast<T*>(a.dbias));
@@ -322,21 +334,42 @@ hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
   const bool copy = a.act != 0 || (a.bf16 && (a.N % kStep != 0 || a.M % kStep != 0));
   hipError_t e = make_dz(a, copy, a.bf16 ? up64(a.M) : long(a.M), &dz, &ld, &ws, stream);
   if (e != hipSuccess) return e;
-  float* part = reinterpret_cast<float*>(ws);
-  const bool any = a.K % 8 != 0;
-  if (a.dx) {
+  // the a operand, its rows copied where they are not aligned
+  auto operand = [&](const void* p, int rows, int nb, const T** out, long* ld_out, float** part) {
+    *out = static_cast<const T*>(p);
+    *ld_out = a.K;
+    *part = reinterpret_cast<float*>(ws);
+    if constexpr (sizeof(T) == 2) {
+      if (copies(rows, a.K, nb)) {
+        bf16_t* copy = reinterpret_cast<bf16_t*>(ws);
+        *out = copy;
+        *ld_out = up64(a.K);
+        *part = reinterpret_cast<float*>(ws + copy_bytes(rows, a.K, nb));
+        return pad_rows(rows, a.K, *ld_out, static_cast<const bf16_t*>(p), copy, stream);
+      }
+    }
+    return hipSuccess;
+  };
+  const T* A;
+  long lda;
+  float* part;
+  if (a.dx && a.K > 0 && a.M > 0) {
+    if ((e = operand(a.w, a.N, a.M, &A, &lda, &part)) != hipSuccess) return e;
     Product<T> g = {};
-    g.A[0] = {static_cast<const T*>(a.w), 1, a.K, a.K};
+    g.A[0] = {A, 1, lda, a.K};
     g.B[0] = {dz, ld, 1, a.M};
     g.K[0] = a.N;
-    if ((e = product<kCols, kRows>(g, any, plain_epi<T>(a.dx, a.K), a.K, a.M, part, stream)) != hipSuccess) return e;
+    if ((e = product<kCols, kRows>(g, lda % 8 != 0, plain_epi<T>(a.dx, a.K), a.K, a.M, part, stream)) != hipSuccess)
+      return e;
   }
-  if (a.dw) {
+  if (a.dw && a.K > 0 && a.N > 0) {
+    if ((e = operand(a.x, a.M, a.N, &A, &lda, &part)) != hipSuccess) return e;
     Product<T> g = {};
-    g.A[0] = {static_cast<const T*>(a.x), 1, a.K, a.K};
+    g.A[0] = {A, 1, lda, a.K};
     g.B[0] = {dz, 1, ld, a.N};
     g.K[0] = a.M;
-    if ((e = product<kCols, kCols>(g, any, plain_epi<T>(a.dw, a.K), a.K, a.N, part, stream)) != hipSuccess) return e;
+    if ((e = product<kCols, kCols>(g, lda % 8 != 0, plain_epi<T>(a.dw, a.K), a.K, a.N, part, stream)) != hipSuccess)
+      return e;
   }
   return hipSuccess;
 }
@@ -345,12 +378,16 @@ hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
 
 size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
   if (bf16 && few_rows(M, N, K)) return 0;
-  return (bf16 && K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + split_bytes(N, M, K, bf16, K % 8 != 0);
+  if (!bf16) return split_bytes(N, M, K, false, false, false);
+  return (K % kStep ? up256(size_t(M) * up64(K) * 2) : 0) + copy_bytes(N, K, M) +
+         split_bytes(N, M, K, true, stays_any(N, K, M), false);
 }
 
 size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16) {
   const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4));
-  const size_t dx = split_bytes(K, M, N, bf16, K % 8 != 0), dw = split_bytes(K, N, M, bf16, K % 8 != 0);
+  // dx reads w, dw reads x, one after the other
+  const size_t dx = (bf16 ? copy_bytes(N, K, M) : 0) + split_bytes(K, M, N, bf16, stays_any(N, K, M), true);
+  const size_t dw = (bf16 ? copy_bytes(M, K, N) : 0) + split_bytes(K, N, M, bf16, stays_any(M, K, N), true);
   return dz + (dx > dw ? dx : dw);
 }
 

@@ -227,7 +227,8 @@ template <typename T>
 __device__ __forceinline__ void dh_row(int n, int d, long ld, int splits, long split, const int* place,
                                        const float* dX, T* dh) {
   const int i = place[n];
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+  // the grid's second axis takes turns at the columns
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < d; c += blockDim.x * gridDim.y) {
     float v = 0.f;
     if (i >= 0) {
 #pragma unroll 8
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(256) void join_rows_kernel(int N, int d, long ld_h,
   }
   const int i = blockIdx.x - N;
   if (i >= *count) return;
-  for (int c = threadIdx.x; c < ld; c += 256) {
+  for (int c = blockIdx.y * 256 + threadIdx.x; c < ld; c += 256 * gridDim.y) {
     float v = 0.f;
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) v += dE[size_t(s) * split + size_t(i) * ld + c];
@@ -321,20 +322,12 @@ __global__ __launch_bounds__(1024) void dw1_kernel(int N, int r, long ld, const 
   }
 }
 
-// W2 with rows padded to a multiple of 64 tokens (zeros), for vocabularies
-// whose rows are not 16-byte aligned.  grid: (tokens / 1024, r).
-__global__ __launch_bounds__(256) void pad_w2_kernel(int V, long ld, const bf16_t* __restrict__ W2,
-                                                     bf16_t* __restrict__ out) {
-  const long v0 = long(blockIdx.x) * 1024;
-  for (long v = v0 + threadIdx.x; v < v0 + 1024 && v < ld; v += 256)
-    out[size_t(blockIdx.y) * ld + v] = v < V ? W2[size_t(blockIdx.y) * V + v] : bf16_t(0);
-}
-
 // What the forward and the backward call carve out of the workspace.
 struct Layout {
-  size_t row, place, token, label, lse, g, X, W2, stat, zlab, dz, dXh, dXe, total;
+  size_t row, place, token, label, lse, g, X, W2, Wo, stat, zlab, dz, dXh, dXe, total;
   int dp, rp, rows, width;   // padded parts of X, padded rows, width of a piece
-  long w2_ld;                // row length of W2 as the products read it
+  long w2_ld, wo_ld;         // row lengths of W2 and Wo as the products read them
+  bool any;                  // rows of Wo are not 16-byte aligned
   Plan h, e;                 // of the contractions over a piece's tokens
 };
 
@@ -364,6 +357,12 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     L.w2_ld = long(up(V, 64));
     L.W2 = take(size_t(r) * L.w2_ld * 2);
   }
+  L.wo_ld = d;
+  if (bf16 && d % 8 && d >= 512 && size_t(V) * L.dp * 2 <= kCopyBytes) {
+    L.wo_ld = L.dp;
+    L.Wo = take(size_t(V) * L.dp * 2);
+  }
+  L.any = bf16 && L.wo_ld % 8 != 0;
   if (!backward) {
     L.stat = take((size_t(V) + kLeastTile - 1) / kLeastTile * N * sizeof(float2));
     L.zlab = take(size_t(N) * 4);
@@ -372,12 +371,12 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     const size_t most = kPieceBytes / (size_t(L.rows) * elem);
     const size_t pieces = most >= full ? 1 : (full + (most ? most : 1) - 1) / (most ? most : 1);
     L.width = int(up((full + pieces - 1) / pieces, kPieceAlign));
-    auto plan = [&](int na, bool any) {
+    auto plan = [&](int na, bool any, bool cols) {
       if (!na || !N) return Plan{0, 1};
-      return bf16 ? plan_for(na, N, L.width, any, true) : Plan{0, f32_splits(na, N, L.width)};
+      return bf16 ? plan_for(na, N, L.width, any, cols, true) : Plan{0, f32_splits(na, N, L.width)};
     };
-    L.h = plan(d, d % 8 != 0);
-    L.e = plan(r, false);
+    L.h = plan(d, L.any, true);
+    L.e = plan(r, false, false);
     L.dz = take(size_t(L.rows) * L.width * elem);
     L.dXh = take(size_t(L.h.splits) * L.rows * L.dp * 4);
     L.dXe = take(size_t(L.e.splits) * L.rows * L.rp * 4);
@@ -392,7 +391,7 @@ struct Parts {
   int *count, *row, *place;
   RowData rows;
   T* X;
-  const T* W2;
+  const T *W2, *Wo;
   int kx;
 };
 
@@ -434,12 +433,21 @@ hipError_t start(const LossArgs& a, const Layout& L, Parts<T>& p, PrepareArgs<T>
   if (pre.counted)
     hipLaunchKernelGGL(compact_kernel, dim3(1), dim3(1024), 0, stream, a.N, a.V, a.label, p.count, p.row, p.place);
   hipLaunchKernelGGL((prepare_kernel<T>), dim3(unsigned(a.N + 64 + parts)), dim3(256), 0, stream, pre);
-  if (L.W2) {
-    p.W2 = reinterpret_cast<T*>(ws + L.W2);
-    hipLaunchKernelGGL(pad_w2_kernel, dim3(unsigned((L.w2_ld + 1023) / 1024), unsigned(a.r)), dim3(256), 0, stream,
-                       a.V, L.w2_ld, static_cast<const bf16_t*>(a.W2), reinterpret_cast<bf16_t*>(ws + L.W2));
+  p.Wo = static_cast<const T*>(a.Wo);
+  hipError_t e = hipGetLastError();
+  if constexpr (sizeof(T) == 2) {
+    if (e == hipSuccess && L.W2) {
+      bf16_t* copy = reinterpret_cast<bf16_t*>(ws + L.W2);
+      p.W2 = copy;
+      e = pad_rows(a.r, a.V, L.w2_ld, static_cast<const bf16_t*>(a.W2), copy, stream);
+    }
+    if (e == hipSuccess && L.Wo) {
+      bf16_t* copy = reinterpret_cast<bf16_t*>(ws + L.Wo);
+      p.Wo = copy;
+      e = pad_rows(a.V, a.d, L.wo_ld, static_cast<const bf16_t*>(a.Wo), copy, stream);
+    }
   }
-  return hipGetLastError();
+  return e;
 }
 
 // The logits of tokens [v0, v0 + nv) as a product.
@@ -448,7 +456,7 @@ Product<T> logits(const LossArgs& a, const Parts<T>& p, int v0, int nv) {
   Product<T> g = {};
   g.B[0] = g.B[1] = {p.X, p.kx, 1, p.L.rows};
   if (a.d) {
-    g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, a.d, 1, nv};
+    g.A[0] = {p.Wo + size_t(v0) * p.L.wo_ld, p.L.wo_ld, 1, nv};
     g.K[0] = a.d;
   }
   if (a.r) {
@@ -495,8 +503,8 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
     bm = shape.BM;
     return StatsEpi<T, shape.WA, shape.BN>{base_logits(a, p, 0, a.V, nullptr), p.rows.label, stat, a.N, zlab};
   };
-  if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), a.d % 8 != 0, make, a.V, a.N,
-                                         plan_for(a.V, a.N, a.d + a.r, a.d % 8 != 0, false), stream)) != hipSuccess)
+  if ((e = multiply<kRows, kCols, kRows>(logits(a, p, 0, a.V), L.any, make, a.V, a.N,
+                                         plan_for(a.V, a.N, a.d + a.r, L.any, a.d == 0, false), stream)) != hipSuccess)
     return e;
   // few rows: all threads of a workgroup on one row's tiles; many: neighbours
   // in a wave read neighbouring rows
@@ -520,7 +528,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
   const long split_h = long(L.rows) * L.dp, split_e = long(L.rows) * L.rp;
   T *dU = static_cast<T*>(a.dU), *dh = static_cast<T*>(a.dh), *dWo = static_cast<T*>(a.dWo);
   T *dW1 = static_cast<T*>(a.dW1), *dW2 = static_cast<T*>(a.dW2);
-  const bool any = a.d % 8 != 0;
+  const bool any = L.any;
   PrepareArgs<T> pre = {};
   pre.dU = dU;
   if (a.bf16 && (dWo || dW2)) {   // the bf16 products take whole steps of rows
@@ -537,11 +545,11 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       return GradEpi<T>{base_logits(a, p, v0, nv, dU), p.rows.label, p.rows.lse, p.rows.g, dz, L.width, dU};
     };
     if ((e = multiply<kRows, kCols, kRows>(logits(a, p, v0, nv), any, grad, nv, a.N,
-                                           plan_for(nv, a.N, a.d + a.r, any, false), stream)) != hipSuccess) return e;
+                                           plan_for(nv, a.N, a.d + a.r, any, a.d == 0, false), stream)) != hipSuccess) return e;
     const Operand<T> dz_rows = {dz, L.width, 1, L.rows}, dz_tokens = {dz, 1, L.width, nv};
     if (dh) {
       Product<T> g = {};
-      g.A[0] = {static_cast<const T*>(a.Wo) + size_t(v0) * a.d, 1, a.d, a.d};
+      g.A[0] = {p.Wo + size_t(v0) * L.wo_ld, 1, L.wo_ld, a.d};
       g.B[0] = dz_rows;
       g.K[0] = nv;
       g.nb = p.count;
@@ -565,7 +573,7 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       const bool vec = a.d % 4 == 0 && reinterpret_cast<uintptr_t>(dWo) % (4 * sizeof(T)) == 0;
       auto store = [&](auto) { return StoreEpi<T>{dWo + size_t(v0) * a.d, a.d, a.d, vec}; };
       if ((e = multiply<kCols, kCols, kCols>(g, false, store, a.d, nv,
-                                             plan_for(a.d, nv, a.N, false, false), stream)) != hipSuccess) return e;
+                                             plan_for(a.d, nv, a.N, false, true, false), stream)) != hipSuccess) return e;
     }
     if (dW2) {
       Product<T> g = {};
@@ -575,18 +583,20 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
       const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(dW2) % (4 * sizeof(T)) == 0;
       auto store = [&](auto) { return StoreEpi<T>{dW2 + v0, a.V, nv, vec}; };
       if ((e = multiply<kCols, kCols, kCols>(g, false, store, nv, a.r,
-                                             plan_for(nv, a.r, a.N, false, false), stream)) != hipSuccess) return e;
+                                             plan_for(nv, a.r, a.N, false, true, false), stream)) != hipSuccess) return e;
     }
   }
   if (a.N == 0) return hipSuccess;
   const unsigned rows = unsigned(a.N);
-  const bool join_e = dW1 && L.e.splits > 1;
-  if (join_e || (dh && !dW1))
-    hipLaunchKernelGGL((join_rows_kernel<T>), dim3(join_e ? 2 * rows : rows), dim3(256), 0, stream, a.N, a.d,
+  // split sums are many values for few rows: a launch of their own, spread over the columns
+  const bool join_e = dW1 && L.e.splits > 1, join_h = dh && (!dW1 || join_e || L.h.splits > 1);
+  const unsigned wide = unsigned(((a.d > a.r ? a.d : a.r) + 255) / 256);
+  if (join_e || join_h)
+    hipLaunchKernelGGL((join_rows_kernel<T>), dim3(join_e ? 2 * rows : rows, rows >= 1024 ? 1 : wide), dim3(256), 0, stream, a.N, a.d,
                        long(L.dp), L.h.splits, split_h, p.place, dXh, dh, long(L.rp), L.e.splits, split_e, p.count,
                        dXe);
   if (dW1)
-    hipLaunchKernelGGL((dw1_kernel<T>), dim3(dh && !join_e ? 2 * rows : rows), dim3(1024), 0, stream, a.N, a.r,
+    hipLaunchKernelGGL((dw1_kernel<T>), dim3(dh && !join_h ? 2 * rows : rows), dim3(1024), 0, stream, a.N, a.r,
                        long(L.rp), p.count, p.rows.token, dXe, dW1, a.d, long(L.dp), L.h.splits, split_h, p.place, dXh,
                        dh);
   return hipGetLastError();

@@ -64,10 +64,9 @@ __device__ __forceinline__ void store4(float* p, f32x4_t v, int n, bool vec) {
 }
 __device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n, bool vec) {
   if (vec && n >= 4) {
-    u32x2_t u;
-    u[0] = uint32_t(f32_to_bf16(v[0])) | (uint32_t(f32_to_bf16(v[1])) << 16);
-    u[1] = uint32_t(f32_to_bf16(v[2])) | (uint32_t(f32_to_bf16(v[3])) << 16);
-    *reinterpret_cast<u32x2_t*>(p) = u;
+    typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+    const bf16x4_t h = __builtin_convertvector(v, bf16x4_t);   // two packed conversions, nearest even
+    *reinterpret_cast<bf16x4_t*>(p) = h;
     return;
   }
 #pragma unroll
@@ -94,7 +93,9 @@ template <> struct Raw4<bf16_t> {
 // relative, far below the half step 2^-8 that dz is rounded by.
 template <typename T> __device__ __forceinline__ float exp_of(float x);
 template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
-template <> __device__ __forceinline__ float exp_of<bf16_t>(float x) { return __expf(x); }
+template <> __device__ __forceinline__ float exp_of<bf16_t>(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+}
 
 // One operand: element (a, k) at p[a * sa + k * sk], one of the strides 1;
 // a in [0, n).
@@ -393,30 +394,49 @@ struct StatsEpi {
     const float ninf = -__builtin_huge_valf();
     int labels[FN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) labels[j] = label[min(t.b0 + 16 * j + (lane & 15), t.nb - 1)];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int b = t.b0 + 16 * j + (lane & 15);
-      const int y = b < t.nb ? labels[j] - base.v0 : -1;
-      float m = ninf;
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int a = t.a0 + 16 * i + 4 * (lane >> 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (a + e >= base.na) acc[i][j][e] = ninf;
-          if (a + e == y) zlab[b] = acc[i][j][e];
-          m = fmaxf(m, acc[i][j][e]);
-        }
-      }
-      m = fmaxf(m, __shfl_xor(m, 16, 64));
-      m = fmaxf(m, __shfl_xor(m, 32, 64));
-      const float ref = m == ninf ? 0.f : m;
-      float s = 0.f;
+    for (int j = 0; j < FN; ++j) labels[j] = label[min(t.b0 + 16 * j + (lane & 15), t.nb - 1)] - base.v0;
+    if (t.a0 + 16 * FM > base.na) {   // tokens behind the vocabulary's end
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += exp_of<T>(acc[i][j][e] - ref);
+        for (int e = 0; e < 4; ++e)
+          if (t.a0 + 16 * i + 4 * (lane >> 4) + e >= base.na) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j][e] = ninf;
+          }
+    }
+    // few waves hold the label of any of their rows
+    bool mine = false;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) mine |= unsigned(labels[j] - t.a0) < unsigned(16 * FM);
+    if (__any(mine)) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15), y = b < t.nb ? labels[j] : -1;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (t.a0 + 16 * i + 4 * (lane >> 4) + e == y) zlab[b] = acc[i][j][e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      float m = ninf;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      const float ref = m == ninf ? 0.f : m;
+      // four sums: the additions do not wait for one another
+      f32x4_t part4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part4[e] += exp_of<T>(acc[i][j][e] - ref);
+      float s = (part4[0] + part4[1]) + (part4[2] + part4[3]);
       s += __shfl_xor(s, 16, 64);
       s += __shfl_xor(s, 32, 64);
       if (lane < 16) part[t.wave_a * BN + t.wave_b * 16 * FN + 16 * j + lane] = make_float2(m, s);
@@ -467,23 +487,30 @@ struct GradEpi {
       lses[j] = lse[b];
       gs[j] = g[b];
     }
+    const bool edge = t.a0 + 16 * FM > base.na;
+    bool mine = edge;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) mine |= unsigned(labels[j] - t.a0) < unsigned(16 * FM);
+    mine = __any(mine);   // few waves hold the label of any of their rows, or the vocabulary's end
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const int b = t.b0 + 16 * j + (lane & 15);
       if (b >= t.nb) continue;
-      const int y = labels[j];
       T* u = dU ? dU + size_t(base.row[b]) * base.V + base.v0 : nullptr;
+      T* out = dz + size_t(b) * dz_ld;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int a = t.a0 + 16 * i + 4 * (lane >> 4);
         f32x4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = exp_of<T>(acc[i][j][e] - lses[j]);
-          v[e] = a + e < base.na ? gs[j] * (p - (a + e == y ? 1.f : 0.f)) : 0.f;
+        for (int e = 0; e < 4; ++e) v[e] = exp_of<T>(acc[i][j][e] - lses[j]);
+        if (mine) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = a + e >= base.na ? 0.f : a + e == labels[j] ? v[e] - 1.f : v[e];
         }
+        v *= gs[j];
         // the piece's width dz_ld is a multiple of the tile: every a of the tile is inside it
-        store4(dz + size_t(b) * dz_ld + a, v, 4, true);
+        store4(out + a, v, 4, true);
         if (dU && a < base.na) store4(u + a, v, base.na - a, base.vec);
       }
     }

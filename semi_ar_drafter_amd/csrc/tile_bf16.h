@@ -556,11 +556,36 @@ using Tile16 = TileShape<128, 16, 4, 1, 64, 4>;
 using Tile32 = TileShape<128, 32, 4, 1, 64, 3>;
 using Tile64 = TileShape<128, 64, 2, 2, 64, 3>;
 using Tile128 = TileShape<128, 128, 2, 2, 64, 2>;
+using Tile128Deep = TileShape<128, 128, 2, 2, 64, 4>;   // one workgroup per compute unit: two steps more in flight
 using Tile16Any = TileShape<128, 16, 4, 1, 64, 2>;
 using Tile32Any = TileShape<128, 32, 4, 1, 64, 2>;
 using Tile64Any = TileShape<128, 64, 2, 2, 64, 2>;
 
 constexpr int kComputeUnits = 256;
+
+// dst[r][0..ld) = src[r][0..n), zeros behind: rows that are not 16-byte
+// aligned, or no whole number of steps, copied.  Eight values per thread.
+static __global__ __launch_bounds__(256) void pad_rows_kernel(long rows, long n, long ld, const bf16_t* __restrict__ src,
+                                                              bf16_t* __restrict__ dst) {
+  const uint32_t per = uint32_t(ld / 8);   // ld is a multiple of 8
+  const long at = long(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= rows * per) return;
+  const long r = at / per, c = (at - r * per) * 8;
+  const bf16_t* s = src + r * n;
+  const u32x4_t v = load_any(s + c, s + (c < n ? n : c));
+  *reinterpret_cast<u32x4_t*>(dst + at * 8) = v;
+}
+inline hipError_t pad_rows(long rows, long n, long ld, const bf16_t* src, bf16_t* dst, hipStream_t stream) {
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned((rows * (ld / 8) + 255) / 256)), dim3(256), 0, stream, rows, n, ld,
+                     src, dst);
+  return hipGetLastError();
+}
+// Weights whose rows are not 16-byte aligned are copied up to this size, where
+// their product is long: the copy takes a few microseconds, and direct loads
+// then take less than half of a step by register staging (24 rows, 1088 x
+// 3535: 52 us for the logits before, 20 with the copy), or allow the large
+// tile.
+constexpr size_t kCopyBytes = size_t(64) << 20;
 
 // Which tile a product takes (0 .. 4: Tile16 .. Tile256) and into how many
 // fp32 sums its contraction is split.
@@ -575,10 +600,11 @@ struct Plan {
 // smaller ones side by side), so the time goes with the number of rounds.
 // In units of a step of the 256 x 256 tile (1.64 us at 8192^3), a round of
 // that tile takes its steps and 5 for its ends; two 128 x 128 tiles side by
-// side take 0.6 a step and 3.  (8192^3: 840 us against 1000; 4096 x 5120 x
-// 5120, 320 large tiles on 256 units: 268 against 248.)  A split costs the
-// writing and reading of its tile in fp32: 12 and 4.
-inline Plan plan_for(int na, int nb, long K, bool any, bool split) {
+// side take 3 and, a step, 0.6 or (cols: the a operand is kCols) 0.72.
+// (8192^3: 840 us against 1000 and 1230; 4096 x 5120 x 5120, 320 large tiles
+// on 256 units: 267 against 248 and 285.)  A split costs the writing and
+// reading of its tile in fp32: 12 and 4.
+inline Plan plan_for(int na, int nb, long K, bool any, bool cols, bool split) {
   const long steps = (K + kStep - 1) / kStep;
   const int first = nb <= 16 ? 0 : nb <= 32 ? 1 : nb <= 64 ? 2 : 3, last = first < 3 || any ? first : 4;
   Plan best = {first, 1};
@@ -590,7 +616,7 @@ inline Plan plan_for(int na, int nb, long K, bool any, bool split) {
     for (int s = 1; s <= 64 && (s == 1 || (split && s * 4 <= steps)); ++s) {
       const double rounds = double((tiles * s + slots - 1) / slots);
       const double steps_s = double((steps + s - 1) / s);
-      const double cost = rounds * (large ? steps_s + 5 + (s > 1 ? 12 : 0) : 0.6 * steps_s + 3 + (s > 1 ? 4 : 0));
+      const double cost = rounds * (large ? steps_s + 5 + (s > 1 ? 12 : 0) : (cols ? 0.72 : 0.6) * steps_s + 3 + (s > 1 ? 4 : 0));
       if (cost < least * 0.97) {
         least = cost;
         best = {c, s};
@@ -617,7 +643,10 @@ hipError_t launch_bf16(const Product<bf16_t>& g, const Make& make, int na, int n
       case 0: return launch_tile_bf16<Tile16, LA0, LA1, LB, false>(g, make(Tile16()), na, nb, s, stream);
       case 1: return launch_tile_bf16<Tile32, LA0, LA1, LB, false>(g, make(Tile32()), na, nb, s, stream);
       case 2: return launch_tile_bf16<Tile64, LA0, LA1, LB, false>(g, make(Tile64()), na, nb, s, stream);
-      case 3: return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, s, stream);
+      case 3:
+        if (long((na + 127) / 128) * ((nb + 127) / 128) * s <= kComputeUnits)
+          return launch_tile_bf16<Tile128Deep, LA0, LA1, LB, false>(g, make(Tile128Deep()), na, nb, s, stream);
+        return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, s, stream);
       default: return launch_tile256<LA0, LA1, LB>(g, make(Tile256()), na, nb, s, stream);
     }
   }
