@@ -469,24 +469,41 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   }
   epi.init(acc, at);
   if (t_begin < t_end) {
-    wait_vm<0>();
+    // the first step has landed: 8 of the loads sent off, in order
+    if (t_end - t_begin == 1)
+      wait_vm<0>();
+    else if (lead || t_end - t_begin == 2)
+      wait_vm<8>();
+    else
+      wait_vm<12>();
     meet();
     if (!lead) meet();   // phase 0 of the second half
     for (int t = t_begin; t < t_end; ++t) {
       const unsigned char* sa = smem + ((t & 1) * 2 + at.wave_a) * Sh::a_half;
       const unsigned char* sb = smem + 4 * Sh::a_half + (t % 3) * Sh::b_step;
+      // read addresses are made again each step: held over the loop, they
+      // would spill what the MFMAs need
+      int vlane = lane;
+      asm volatile("" : "+v"(vlane));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        read_frags<LB, 256, kStep>(fb[half], sb, at.wave_b * 64, half, lane);
+        read_frags<LB, 256, kStep>(fb[half], sb, at.wave_b * 64, half, vlane);
         if (two && t >= T0)
-          read_frags<LA1, 128, kStep>(fa[half], sa, 0, half, lane);
+          read_frags<LA1, 128, kStep>(fa[half], sa, 0, half, vlane);
         else
-          read_frags<LA0, 128, kStep>(fa[half], sa, 0, half, lane);
+          read_frags<LA0, 128, kStep>(fa[half], sa, 0, half, vlane);
       }
       const int next_a = t + 2, next_b = lead ? t + 2 : t + 3;
       if (next_a < t_end) prepare_a(next_a, false);
       if (next_b < t_end) prepare_b(next_b);
       lds_wait();
+      // the second half's share of the second step's b, which the lead reads next
+      if (!lead && t == t_begin) {
+        if (t_end - t_begin > 2)
+          wait_vm<4>();
+        else
+          wait_vm<0>();
+      }
       meet();
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
