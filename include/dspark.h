@@ -552,8 +552,8 @@ dspark_launch dspark_get_draft_launch(void);
  *   workspace     >= dspark_linear_workspace_bytes(M, N, K, dtype) bytes
  *                 (NULL if that is 0), 256-byte aligned, any contents.  Calls
  *                 that can overlap need separate ones.
- * Outputs overlap no input but y the residual.  Results do not depend on
- * execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
+ * An output that overlaps another array is refused (DSPARK_ERR_INVALID_ARG),
+ * but for y == residual.  Results do not depend on execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
  */
 dspark_status dspark_linear(
     int M, int N, int K, dspark_dtype dtype, const void* x, const void* w, const void* bias,
@@ -578,6 +578,7 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
  *                 With M == 0, dw and dbias are zero; with N == 0, dx is.
  *   workspace     >= dspark_linear_backward_workspace_bytes(M, N, K, dtype)
  *                 bytes, 256-byte aligned, any contents.
+ * Outputs that overlap another array are refused.
  */
 dspark_status dspark_linear_backward(
     int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x, const void* w,
@@ -605,7 +606,8 @@ size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype 
  *   N, V, d, r    rows (0: no-op), vocabulary, hidden size, Markov rank
  *   dtype         storage of U, h, Wo, W1, W2
  *   label int32 [N]
- *   U     [N][V] or NULL     base logits; -inf masks a token
+ *   U     [N][V] or NULL     base logits; -inf masks a token (a row that is
+ *                            not ignored keeps at least one finite logit)
  *   h     [N][d], Wo [V][d]  hidden states and output projection (d > 0), 16-byte aligned
  *   prev  int32 [N]          x_{k-1}, clamped to the vocabulary (r > 0)
  *   W1    [V][r], W2 [r][V]  (r > 0), 16-byte aligned
@@ -640,7 +642,8 @@ size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dty
  *                 storage type; each may be NULL: not computed
  *   workspace     >= dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype)
  *                 bytes, 256-byte aligned, any contents
- * N == 0 leaves dWo, dW1 and dW2 zero.
+ * N == 0 leaves dWo, dW1 and dW2 zero.  Outputs that overlap another array are
+ * refused.
  */
 dspark_status dspark_markov_loss_backward(
     int N, int V, int d, int r, dspark_dtype dtype, const float* g, const float* lse,

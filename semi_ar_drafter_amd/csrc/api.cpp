@@ -420,7 +420,28 @@ namespace {
 bool known_dtype(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
 bool misaligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
-// Checks shared by the linear layer's two directions; nullptr or the complaint.
+// Whether [p, p + n) and [q, q + m) share a byte.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  if (!p || !q || n == 0 || m == 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+struct Span {
+  const void* p;
+  size_t n;
+};
+// Whether any output shares memory with an input or with another output.
+bool any_overlap(const Span* out, int n_out, const Span* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+// Checks shared by the linear layer's two directions.
 dspark_status linear_sizes(int M, int N, int K, dspark_dtype dtype, dspark_activation act) {
   if (M < 0 || N < 0 || K < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
   if (!known_dtype(dtype)) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype");
@@ -461,6 +482,13 @@ dspark_status dspark_linear(int M, int N, int K, dspark_dtype dtype, const void*
   st = check_workspace(workspace, workspace_bytes, dspark_linear_workspace_bytes(M, N, K, dtype),
                        "dspark_linear_workspace_bytes");
   if (st != DSPARK_OK) return st;
+  {
+    const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+    const Span out[] = {{y, m * n * elem}, {pre, m * n * 4}};
+    const Span in[] = {
+        {x, m * k * elem}, {w, n * k * elem}, {bias, n * elem}, {residual == y ? nullptr : residual, m * n * elem}};
+    if (any_overlap(out, 2, in, 4)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
+  }
   dspark::LinearArgs a;
   a.M = M;
   a.N = N;
@@ -502,6 +530,12 @@ dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, co
   st = check_workspace(workspace, workspace_bytes, dspark_linear_backward_workspace_bytes(M, N, K, dtype),
                        "dspark_linear_backward_workspace_bytes");
   if (st != DSPARK_OK) return st;
+  {
+    const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+    const Span out[] = {{dx, m * k * elem}, {dw, n * k * elem}, {dbias, n * elem}};
+    const Span in[] = {{dy, m * n * elem}, {x, m * k * elem}, {w, n * k * elem}, {pre, m * n * 4}};
+    if (any_overlap(out, 3, in, 4)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
+  }
   dspark::LinearBackwardArgs a;
   a.M = M;
   a.N = N;
@@ -590,6 +624,8 @@ dspark_status dspark_markov_loss(int N, int V, int d, int r, dspark_dtype dtype,
   st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_workspace_bytes(N, V, d, r, dtype),
                        "dspark_markov_loss_workspace_bytes");
   if (st != DSPARK_OK) return st;
+  if (overlap(nll, size_t(N) * 4, lse, size_t(N) * 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
   a.nll = nll;
   a.lse = lse;
   hipError_t e = dspark::launch_markov_loss(a, stream);
@@ -621,6 +657,12 @@ dspark_status dspark_markov_loss_backward(int N, int V, int d, int r, dspark_dty
   st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype),
                        "dspark_markov_loss_backward_workspace_bytes");
   if (st != DSPARK_OK) return st;
+  {
+    const size_t n = size_t(N) * elem, v = size_t(V) * elem, R = size_t(r), D = size_t(d);
+    const Span out[] = {{dU, n * V}, {dh, n * D}, {dWo, v * D}, {dW1, v * R}, {dW2, v * R}};
+    const Span in[] = {{U, n * V}, {h, n * D}, {Wo, v * D}, {W1, v * R}, {W2, v * R}};
+    if (any_overlap(out, 5, in, 5)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
+  }
   a.lse_in = lse;
   a.g = g;
   a.dU = dU;

@@ -296,8 +296,8 @@ hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** 
     *dz = out;
   }
   if (a.N == 0) return hipSuccess;
-  // more rows per workgroup where the grid's second axis would not hold them
-  const int per = rows > 65535 * 4 ? kDzRows : a.dbias ? kDzRows : 4;
+  // the grid's second axis holds 65535 chunks
+  const int per = rows > 65535l * kDzRows ? 2 * kDzRows : a.dbias || rows > 65535l * 4 ? kDzRows : 4;
   if (rows > 0 && (copy || a.dbias))
     hipLaunchKernelGGL((dz_kernel<T>), dim3(unsigned((*ld + 1023) / 1024), unsigned((rows + per - 1) / per)),
                        dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, out, *ld,
@@ -305,7 +305,7 @@ hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** 
                        a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0, per);
   if (a.dbias)
     hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 31) / 32)), dim3(256), 0, stream, a.N,
-                       rows > 0 ? int((rows + kDzRows - 1) / kDzRows) : 0, part, static_cast<T*>(a.dbias));
+                       rows > 0 ? int((rows + per - 1) / per) : 0, part, static_cast<T*>(a.dbias));
   return hipGetLastError();
 }
 

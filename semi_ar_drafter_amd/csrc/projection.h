@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "device_util.h"
 
 namespace dspark {
@@ -95,6 +97,19 @@ template <typename T> __device__ __forceinline__ float exp_of(float x);
 template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
 template <> __device__ __forceinline__ float exp_of<bf16_t>(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+}
+
+// Lets a kernel use `bytes` of LDS on the current device: once per kernel and
+// device (the attribute belongs to both).
+inline hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& devices) {
+  int d = 0;
+  hipError_t e = hipGetDevice(&d);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = d < 64 ? uint64_t(1) << d : 0;
+  if (bit && (devices.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // One operand: element (a, k) at p[a * sa + k * sk], one of the strides 1;

@@ -540,10 +540,10 @@ template <int LA0, int LA1, int LB, class Epi>
 hipError_t launch_tile256(const Product<bf16_t>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
   if (na <= 0 || nb <= 0) return hipSuccess;
   const unsigned tiles = unsigned((na + 255) / 256) * unsigned((nb + 255) / 256);
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&tile256_kernel<LA0, LA1, LB, Epi>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, Tile256::lds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e =
+      allow_lds(reinterpret_cast<const void*>(&tile256_kernel<LA0, LA1, LB, Epi>), Tile256::lds, allowed);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((tile256_kernel<LA0, LA1, LB, Epi>), dim3(tiles, unsigned(splits)), dim3(512), Tile256::lds,
                      stream, g, epi, na, nb);
   return hipGetLastError();
@@ -554,10 +554,10 @@ hipError_t launch_tile_bf16(const Product<bf16_t>& g, const Epi& epi, int na, in
   static_assert(!ANY || Sh::S == 2, "register staging is double buffered");
   if (na <= 0 || nb <= 0) return hipSuccess;
   const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
-  auto* kernel = &tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, Sh::lds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e =
+      allow_lds(reinterpret_cast<const void*>(&tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>), Sh::lds, allowed);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads),
                      Sh::lds, stream, g, epi, na, nb);
   return hipGetLastError();

@@ -176,9 +176,9 @@ inline int f32_splits(int na, int nb, long K) {
 template <class Sh, class Epi>
 hipError_t launch_tile_f32(const Product<float>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
   const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&tile_f32_kernel<Sh, Epi>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, Sh::lds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&tile_f32_kernel<Sh, Epi>), Sh::lds, allowed);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((tile_f32_kernel<Sh, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads), Sh::lds, stream, g,
                      epi, na, nb);
   return hipGetLastError();

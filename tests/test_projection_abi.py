@@ -160,3 +160,31 @@ def test_hidden_draft_validation(lib):
     assert call(ws=ctypes.c_void_p(0x10040)) == WORKSPACE
     assert call(B=0, anchor=NULL, U=NULL, ws=NULL, n=0) == OK
     assert lib.dspark_hidden_draft_workspace_bytes(0, 4, 1024, 32, 16, 1) == 0
+
+
+def test_overlapping_outputs_are_refused(lib):
+    """Every array at an address of its own is past this check; each output
+    moved onto (or into) an input, or onto another output, is not.  Only
+    calls that fail are made."""
+    at = lambda i, off=0: ctypes.c_void_p(0x100000 * (i + 1) + off)  # noqa: E731
+    lin = dict(x=at(0), w=at(1), bias=at(2), res=at(3), y=at(4), pre=at(5), ws=at(6))
+    for out in ("y", "pre"):
+        for other in ("x", "w", "bias"):
+            assert linear(lib, **{**lin, out: lin[other]}) == INVALID, (out, other)
+    assert linear(lib, **{**lin, "y": lin["pre"]}) == INVALID
+    assert linear(lib, **{**lin, "y": at(0, 16)}) == INVALID             # inside x
+    assert linear(lib, **{**lin, "y": at(3, 2)}) == INVALID              # the residual, shifted
+    back = dict(dy=at(0), x=at(1), w=at(2), pre=at(3), dx=at(4), dw=at(5), db=at(6), ws=at(7))
+    for out in ("dx", "dw", "db"):
+        for other in ("dy", "x", "w", "pre"):
+            assert linear_backward(lib, **{**back, "act": 2, out: back[other]}) == INVALID, (out, other)
+    assert linear_backward(lib, **{**back, "dx": back["dw"]}) == INVALID
+    ins = {k: at(i) for i, k in enumerate(("label", "U", "h", "Wo", "prev", "W1", "W2"))}
+    assert loss(lib, **ins, nll=at(8), lse=at(8), ws=at(9)) == INVALID
+    outs = {k: at(10 + i) for i, k in enumerate(("dU", "dh", "dWo", "dW1", "dW2"))}
+    rest = dict(g=at(20), lse=at(21), ws=at(22))
+    for out in outs:
+        for other in ("U", "h", "Wo", "W1", "W2"):
+            assert loss_backward(lib, **{**ins, **outs, **rest, out: ins[other]}) == INVALID, (out, other)
+    assert loss_backward(lib, **{**ins, **outs, **rest, "dW1": outs["dWo"]}) == INVALID
+    assert "overlaps" in lib.dspark_last_error().decode()

@@ -475,6 +475,74 @@ def test_loss_gradients_against_differences():
         assert abs((vals[0] - vals[1]) / (2 * t) - float((grad.double() * v.double()).sum())) < 0.004, k
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_workspace_of_the_stated_size_is_enough(dtype):
+    """A workspace of exactly the stated size, in the middle of a larger
+    buffer that keeps what it holds around it."""
+    lib = binding.load()
+    storage = 1 if dtype is torch.bfloat16 else 0
+
+    def inside(nbytes):
+        room = torch.full((nbytes + 1024,), 91, dtype=torch.uint8, device=DEV)
+        off = 512 + (-(room.data_ptr() + 512)) % 256
+        return room, room[off:off + nbytes], off
+
+    def untouched(room, off, nbytes):
+        return bool((room[:off] == 91).all()) and bool((room[off + nbytes:] == 91).all())
+
+    for M, N, K in ((1, 40, 24), (5, 4100, 129), (70, 130, 1000), (300, 200, 4096), (333, 515, 333), (64, 64, 64)):
+        x, w, bias, res, dy = linear_inputs(M, N, K, dtype, "gelu")
+        pre = torch.empty(M, N, device=DEV)
+        n = lib.dspark_linear_workspace_bytes(M, N, K, storage)
+        room, ws, off = inside(n)
+        y = linear(x, w, bias=bias, act="gelu", residual=res, pre=pre, workspace=ws if n else None)
+        check_linear(x, w, bias, "gelu", res, y, pre)
+        assert untouched(room, off, n)
+        n = lib.dspark_linear_backward_workspace_bytes(M, N, K, storage)
+        room, ws, off = inside(n)
+        got = linear_backward(dy, x, w, act="gelu", pre=pre, workspace=ws)
+        assert untouched(room, off, n)
+        assert all(torch.equal(a, b) for a, b in zip(got, linear_backward(dy, x, w, act="gelu", pre=pre)))
+    for N, V, d, r in ((1, 9, 5, 3), (20, 1001, 600, 17), (70, 3000, 129, 64), (300, 700, 64, 33)):
+        s, label, g = loss_inputs(N, V, d, r, True, N // 5, dtype)
+        nll, lse, grads = check_loss(s, label, g, dtype)
+        n = lib.dspark_markov_loss_workspace_bytes(N, V, d, r, storage)
+        room, ws, off = inside(n)
+        again = markov_loss(label, workspace=ws, **s)
+        assert torch.equal(again[0], nll) and torch.equal(again[1], lse) and untouched(room, off, n)
+        n = lib.dspark_markov_loss_backward_workspace_bytes(N, V, d, r, storage)
+        room, ws, off = inside(n)
+        more = markov_loss_backward(g, lse, label, workspace=ws, **s)
+        assert untouched(room, off, n) and all(torch.equal(more[k], grads[k]) for k in grads)
+
+
+@pytest.mark.parametrize("M,N,K", [(4000, 4090, 1096), (1000, 4090, 4080)])
+def test_linear_large_tiles(M, N, K):
+    """Sizes that fill the compute units with the largest tile, ragged along
+    every axis (the contraction too), in all three products."""
+    x, w, bias, res, dy = linear_inputs(M, N, K, torch.bfloat16, "silu")
+    y = linear(x, w, bias=bias, act="silu", residual=res)
+    check_linear(x, w, bias, "silu", res, y)
+    dx, dw, _ = linear_backward(dy, x, w)
+    h = HALF[torch.bfloat16]
+    for got, a, b, n, what in ((dx, dy.double(), w.double(), N, "dx"), (dw, dy.double().t(), x.double(), M, "dw")):
+        want, tol = a @ b, 2 * (n + 8) * U32 * (a.abs() @ b.abs())
+        within(got, want, tol + h * (want.abs() + tol) + 1e-38, what)
+
+
+def test_loss_large_tiles():
+    for base, d in ((False, 456), (True, 0)):
+        s, label, g = loss_inputs(2040, 8190, d, 72, base, 100, torch.bfloat16)
+        check_loss(s, label, g, torch.bfloat16)
+
+
+def test_loss_of_many_rows():
+    """More rows than one workgroup counts for itself, most of them ignored."""
+    N = 9000
+    s, label, g = loss_inputs(N, 300, 24, 16, False, 7000, torch.bfloat16, tokens=40)
+    check_loss(s, label, g, torch.bfloat16)
+
+
 def test_same_inputs_same_bits():
     s, label, g = loss_inputs(300, 5003, 104, 56, False, 20, torch.bfloat16)
     first = markov_loss(label, **s)
