@@ -600,7 +600,7 @@ inline hipError_t pad_rows(long rows, long n, long ld, const bf16_t* src, bf16_t
 // Weights whose rows are not 16-byte aligned are copied up to this size, where
 // their product is long: the copy takes a few microseconds, and direct loads
 // then take less than half of a step by register staging (24 rows, 1088 x
-// 3535: 52 us for the logits before, 20 with the copy), or allow the large
+// 3535: 52 us for the logits before, 27 with the copy), or allow the large
 // tile.
 constexpr size_t kCopyBytes = size_t(64) << 20;
 
