@@ -583,7 +583,8 @@ def _is(t, name, dtype, shape, device):
 
 def _storage(t, name):
     torch = _torch()
-    _need(t, name)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+        _need(t, name)
     if t.dtype is torch.bfloat16:
         return DSPARK_BF16
     if t.dtype is not torch.float32:
@@ -679,7 +680,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     _optional(out, "out", x.dtype, (M, N), dev)
     a = _act(act)
     with _on(dev):
-        y = out if out is not None else torch.empty((M, N), dtype=x.dtype, device=dev)
+        y = out if out is not None else x.new_empty((M, N))
         ws, n = _scratch(_bytes("linear", M, N, K, dt), dev, "linear", workspace)
         _check(lib.dspark_linear(M, N, K, dt, _at(x), _at(w), _at(bias), a, _at(residual), _at(y), _at(pre),
                                  ws, n, _raw_stream(dev)))
@@ -705,7 +706,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     if set(need) - {"dx", "dw", "dbias"}:
         raise ValueError("need names dx, dw and dbias")
     with _on(dev):
-        new = lambda name, *sh: torch.empty(sh, dtype=x.dtype, device=dev) if name in need else None  # noqa: E731
+        new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
         dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
         ws, n = _scratch(_bytes("linear_backward", M, N, K, dt), dev, "linear_backward",
                          workspace)
@@ -715,7 +716,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
 
 
 def _loss_inputs(label, U, h, Wo, prev, W1, W2):
-    """Checks the loss's inputs; returns (N, V, d, r, dtype, device, storage)."""
+    """Checks the loss's inputs; returns (N, V, d, r, storage, device)."""
     torch = _torch()
     if (h is None) != (Wo is None) or (W1 is None) != (W2 is None) or (prev is None) != (W1 is None):
         raise ValueError("h goes with Wo, and prev with W1 and W2")
@@ -736,7 +737,7 @@ def _loss_inputs(label, U, h, Wo, prev, W1, W2):
     _optional(prev, "prev", torch.int32, (N,), dev)
     _optional(W1, "W1", first.dtype, (V, r), dev)
     _optional(W2, "W2", first.dtype, (r, V), dev)
-    return N, V, d, r, dt, dev, first.dtype
+    return N, V, d, r, dt, dev
 
 
 def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out=None, workspace=None):
@@ -748,7 +749,7 @@ def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out
     each of the three parts may be left out, not all."""
     torch = _torch()
     lib = load()
-    N, V, d, r, dt, dev, _ = _loss_inputs(label, U, h, Wo, prev, W1, W2)
+    N, V, d, r, dt, dev = _loss_inputs(label, U, h, Wo, prev, W1, W2)
     with _on(dev):
         if out is None:
             out = (torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev))
@@ -769,7 +770,7 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
     position weights; lse is what markov_loss() returned."""
     torch = _torch()
     lib = load()
-    N, V, d, r, dt, dev, dtype = _loss_inputs(label, U, h, Wo, prev, W1, W2)
+    N, V, d, r, dt, dev = _loss_inputs(label, U, h, Wo, prev, W1, W2)
     _is(g, "g", torch.float32, (N,), dev)
     _is(lse, "lse", torch.float32, (N,), dev)
     shapes = {}
@@ -784,7 +785,8 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
         if k not in shapes:
             raise ValueError(f"no input for the gradient {k}")
     with _on(dev):
-        grads = {k: torch.empty(shapes[k], dtype=dtype, device=dev) for k in need}
+        like = U if U is not None else Wo if Wo is not None else W2
+        grads = {k: like.new_empty(shapes[k]) for k in need}
         ws, n = _scratch(_bytes("markov_loss_backward", N, V, d, r, dt), dev,
                          "markov_loss_backward", workspace)
         _check(lib.dspark_markov_loss_backward(

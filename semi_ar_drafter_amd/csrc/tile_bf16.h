@@ -616,10 +616,11 @@ struct Plan {
 // A compute unit works through its tiles one after the other (two of the
 // smaller ones side by side), so the time goes with the number of rounds.
 // In units of a step of the 256 x 256 tile (1.64 us at 8192^3), a round of
-// that tile takes its steps and 5 for its ends; two 128 x 128 tiles side by
+// that tile takes its steps and 7 for its ends; two 128 x 128 tiles side by
 // side take 3 and, a step, 0.6 or (cols: the a operand is kCols) 0.72.
 // (8192^3: 840 us against 1000 and 1230; 4096 x 5120 x 5120, 320 large tiles
-// on 256 units: 267 against 248 and 285.)  A split costs the writing and
+// on 256 units: 267 against 248 and 285; 1000 x 50021 outputs of five steps:
+// 76 against 70.)  A split costs the writing and
 // reading of its tile in fp32: 12 and 4.
 inline Plan plan_for(int na, int nb, long K, bool any, bool cols, bool split) {
   const long steps = (K + kStep - 1) / kStep;
@@ -633,7 +634,7 @@ inline Plan plan_for(int na, int nb, long K, bool any, bool cols, bool split) {
     for (int s = 1; s <= 64 && (s == 1 || (split && s * 4 <= steps)); ++s) {
       const double rounds = double((tiles * s + slots - 1) / slots);
       const double steps_s = double((steps + s - 1) / s);
-      const double cost = rounds * (large ? steps_s + 5 + (s > 1 ? 12 : 0) : (cols ? 0.72 : 0.6) * steps_s + 3 + (s > 1 ? 4 : 0));
+      const double cost = rounds * (large ? steps_s + 7 + (s > 1 ? 12 : 0) : (cols ? 0.72 : 0.6) * steps_s + 3 + (s > 1 ? 4 : 0));
       if (cost < least * 0.97) {
         least = cost;
         best = {c, s};
