@@ -24,8 +24,7 @@
 // = 256: four products of 5.1 to 5.4 ms, 1.2 PFLOP/s), reading Wo and W2 with
 // few (8 rows, d = 2560: 145 us, 5.9 TB/s), the tiles' ends where the
 // contraction is short (rank 256 alone: 800 us for the statistics of 4096 rows,
-// of which four steps' MFMAs are 150).  A piece's dz stays within the 256 MB
-// of the last-level cache, from which the next products read it.
+// of which four steps' MFMAs are 150).
 #include "launch.h"
 #include "projection.h"
 #include "tile_bf16.h"
@@ -37,8 +36,11 @@ namespace {
 
 inline size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
-// Largest width of a piece's dz array, in bytes.
-constexpr size_t kPieceBytes = size_t(256) << 20;
+// Most bytes of a piece's dz array.  Larger pieces mean fewer, fuller rounds of
+// tiles and fewer passes over dX (4096 rows, V = 151936, rank 256 alone / with d
+// = 5120: 128 MB 3.57 / 22.6 ms, 256 MB 3.28 / 22.2, 512 MB 3.14 / 21.8); the
+// logits themselves would be 1.2 GB in bf16.
+constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kPieceAlign = 256;
 constexpr int kLeastTile = 64;   // along the vocabulary
 
