@@ -644,6 +644,9 @@ def _captured(nbytes, device, zero=False):
 
 
 _HERE_ALREADY = contextlib.nullcontext()
+# Held while a call's launches are enqueued: two threads on one stream share
+# its workspace, so their calls must not be enqueued into each other.
+_launching = threading.Lock()
 
 
 def _on(device):
@@ -679,7 +682,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     _optional(pre, "pre", torch.float32, (M, N), dev)
     _optional(out, "out", x.dtype, (M, N), dev)
     a = _act(act)
-    with _on(dev):
+    with _on(dev), _launching:
         y = out if out is not None else x.new_empty((M, N))
         ws, n = _scratch(_bytes("linear", M, N, K, dt), dev, "linear", workspace)
         _check(lib.dspark_linear(M, N, K, dt, _at(x), _at(w), _at(bias), a, _at(residual), _at(y), _at(pre),
@@ -705,7 +708,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     _optional(pre, "pre", torch.float32, (M, N), dev)
     if set(need) - {"dx", "dw", "dbias"}:
         raise ValueError("need names dx, dw and dbias")
-    with _on(dev):
+    with _on(dev), _launching:
         new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
         dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
         ws, n = _scratch(_bytes("linear_backward", M, N, K, dt), dev, "linear_backward",
@@ -750,7 +753,7 @@ def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out
     torch = _torch()
     lib = load()
     N, V, d, r, dt, dev = _loss_inputs(label, U, h, Wo, prev, W1, W2)
-    with _on(dev):
+    with _on(dev), _launching:
         if out is None:
             out = (torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev))
         nll, lse = out
@@ -784,7 +787,7 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
     for k in need:
         if k not in shapes:
             raise ValueError(f"no input for the gradient {k}")
-    with _on(dev):
+    with _on(dev), _launching:
         like = U if U is not None else Wo if Wo is not None else W2
         grads = {k: like.new_empty(shapes[k]) for k in need}
         ws, n = _scratch(_bytes("markov_loss_backward", N, V, d, r, dt), dev,
@@ -815,7 +818,7 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
     _need(conf_w, "conf_w", torch.float32, (d + r,), dev)
     _need(sts_T, "sts_T", torch.float32, (gamma,), dev)
     _optional(U, "U", h.dtype, (B, gamma, V), dev)
-    with _on(dev):
+    with _on(dev), _launching:
         if U is None:
             U = torch.empty((B, gamma, V), dtype=h.dtype, device=dev)
         if out is None:

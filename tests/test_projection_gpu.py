@@ -578,6 +578,31 @@ def test_two_streams_at_once():
             assert torch.equal(n1, n2) and torch.equal(l1, l2) and all(torch.equal(g1[k], g2[k]) for k in g1)
 
 
+def test_threads_on_one_stream():
+    """Calls of several launches from threads that share a stream, and so its
+    workspace, are not enqueued into each other."""
+    import threading
+    sets = [loss_inputs(60 + 40 * i, 1500 + 300 * i, 64, 24, False, 5, torch.bfloat16, seed=i) for i in range(4)]
+    want = [check_loss(*c, torch.bfloat16) for c in sets]
+    wrong = []
+
+    def work(i):
+        s, label, g = sets[i]
+        for _ in range(20):
+            nll, lse = markov_loss(label, **s)
+            grads = markov_loss_backward(g, lse, label, **s)
+            torch.cuda.synchronize()
+            if not (torch.equal(nll, want[i][0]) and all(torch.equal(grads[k], want[i][2][k]) for k in grads)):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_captured_and_replayed():
     """Two graphs, captured one after the other, replayed with new inputs in
     place, with eager calls between the replays."""
