@@ -1,13 +1,13 @@
 // Matrix product of bf16 operands on v_mfma_f32_16x16x32_bf16, tiles staged
 // through LDS by direct-to-LDS loads.
 //
-// A step covers K = 64 or 32 of the contraction.  Each operand is stored with
-// either the contraction contiguous (kRows: one row per a) or the a axis
-// contiguous (kCols: one row per k), and is staged as it is stored:
-//   kRows  LDS [a][K]; a fragment is one ds_read_b128.  16-byte chunk c of row
-//          a lies at place c ^ (a & 7) (K = 64) or c ^ (a / 4 & 3) (K = 32), so
-//          that any 16 rows of one chunk fall on all 64 banks.
-//   kCols  LDS [K][a]; a fragment is two ds_read_b64_tr_b16, which transpose
+// A step covers 64 of the contraction.  Each operand is stored with either the
+// contraction contiguous (kRows: one row per a) or the a axis contiguous
+// (kCols: one row per k), and is staged as it is stored:
+//   kRows  LDS [a][64 k], 128 bytes a row; a fragment is one ds_read_b128.
+//          16-byte chunk c of row a lies at place c ^ (a & 7), so that any 16
+//          rows of one chunk fall on all 64 banks.
+//   kCols  LDS [64 k][a]; a fragment is two ds_read_b64_tr_b16, which transpose
 //          4 k x 16 a on the way out.  32-byte pair p of row k lies at p ^
 //          pair_turn(k), so that the eight rows that half a wave reads (k to
 //          k + 3 and k + 8 to k + 11) fall on all banks.
@@ -26,7 +26,7 @@
 namespace dspark {
 
 enum Layout2 { kRows = 0, kCols = 1 };
-constexpr int kStep = 64;   // both operands' padding along the contraction
+constexpr int kStep = 64;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -47,14 +47,13 @@ template <int N> __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Tile shape: BM along a, BN along b, WA x WB waves, steps of K, S of them in
-// LDS.
-template <int BM_, int BN_, int WA_, int WB_, int K_, int S_>
+// Tile shape: BM along a, BN along b, WA x WB waves, S steps in LDS.
+template <int BM_, int BN_, int WA_, int WB_, int S_>
 struct TileShape {
-  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_, K = K_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WA = WA_, WB = WB_, S = S_;
   static constexpr int waves = WA * WB, threads = 64 * waves;
-  static constexpr int FM = BM / WA / 16, FN = BN / WB / 16, FK = K / 32;
-  static constexpr int a_bytes = BM * K * 2, b_bytes = BN * K * 2;
+  static constexpr int FM = BM / WA / 16, FN = BN / WB / 16;
+  static constexpr int a_bytes = BM * kStep * 2, b_bytes = BN * kStep * 2;
   static constexpr int stage = a_bytes + b_bytes, lds = S * stage;
   static constexpr int la = a_bytes / 1024, lb = b_bytes / 1024;   // 1 KiB wave loads per step
 };
@@ -67,7 +66,7 @@ __device__ __forceinline__ constexpr int pair_turn(int rows, int k) {
          : rows == 32 ? k >> 3 & 1 : 0;
 }
 // Turn of the chunks of row a of a kRows tile.
-__device__ __forceinline__ constexpr int chunk_turn(int K, int a) { return K == 64 ? a & 7 : a >> 2 & 3; }
+__device__ __forceinline__ constexpr int chunk_turn(int a) { return a & 7; }
 
 // Number of wave loads of `n` that wave w of `waves` issues: a fixed count per
 // wave, so that waits can count them (surplus waves repeat the last one).
@@ -75,16 +74,16 @@ constexpr int loads_per_wave(int n, int waves) { return (n + waves - 1) / waves;
 
 // One operand's staging by one wave: per-lane byte offsets from the tile's
 // base, fixed over the steps.
-template <int LAYOUT, int ROWS, int K, int LOADS>
+template <int LAYOUT, int ROWS, int LOADS>
 struct Stager {
-  static constexpr int units = ROWS * K / 512;   // 1 KiB each
-  static constexpr int chunks = LAYOUT == kRows ? K / 8 : ROWS / 8;   // in a row of LDS
+  static constexpr int units = ROWS * kStep / 512;   // 1 KiB each
+  static constexpr int chunks = LAYOUT == kRows ? kStep / 8 : ROWS / 8;   // in a row of LDS
   uint32_t off[LOADS];
 
   __device__ __forceinline__ static int unit_of(int w, int i) { return min(w * LOADS + i, units - 1); }
   // the chunk of its row that a lane loads in any unit (kRows)
   __device__ __forceinline__ static int chunk_of(int lane) {
-    return (lane % chunks) ^ chunk_turn(K, lane / chunks);
+    return (lane % chunks) ^ chunk_turn(lane / chunks);
   }
 
   // first: the tile's first row along the operand's axis; n: its size; ld: row
@@ -104,7 +103,7 @@ struct Stager {
     }
   }
 
-  // The last step when K is no divisor of the contraction: chunks (kRows) or
+  // The last step of a contraction that ends inside it: chunks (kRows) or
   // rows (kCols) behind its end repeat the last one.  left: what is left of it.
   __device__ __forceinline__ uint32_t tail(int i, int w, int lane, long ld, int left) const {
     if (LAYOUT == kRows) {
@@ -140,15 +139,15 @@ __device__ __forceinline__ u32x4_t load_any(const bf16_t* p, const bf16_t* end) 
   return v;
 }
 
-// Fragments of 32 of a step's K, from `half` * 32 on.
-template <int LAYOUT, int ROWS, int K, int F>
+// Fragments of 32 of a step's 64, from `half` * 32 on.
+template <int LAYOUT, int ROWS, int F>
 __device__ __forceinline__ void read_frags(bf16x8_t (&f)[F], const unsigned char* lds, int first, int half, int lane) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int q = lane >> 4, l = lane & 15;
   if (LAYOUT == kRows) {
-    const unsigned char* p = lds + (first + l) * (K * 2) + (((half * 4 + q) ^ chunk_turn(K, l)) * 16);
+    const unsigned char* p = lds + (first + l) * (kStep * 2) + (((half * 4 + q) ^ chunk_turn(l)) * 16);
 #pragma unroll
-    for (int i = 0; i < F; ++i) f[i] = *reinterpret_cast<const bf16x8_t*>(p + i * 32 * K);
+    for (int i = 0; i < F; ++i) f[i] = *reinterpret_cast<const bf16x8_t*>(p + i * 32 * kStep);
   } else {
     const int k = half * 32 + q * 8 + (l >> 2);   // and k + 4, which turns the same way
     const unsigned char* row = lds + k * (ROWS * 2) + (l & 3) * 8;
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   if (g.nb) nb = *g.nb;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
   const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
-  const int T0 = (K0 + Sh::K - 1) / Sh::K, T = T0 + (K1 + Sh::K - 1) / Sh::K;
+  const int T0 = (K0 + kStep - 1) / kStep, T = T0 + (K1 + kStep - 1) / kStep;
   const int t_begin = int(long(T) * blockIdx.y / gridDim.y), t_end = int(long(T) * (blockIdx.y + 1) / gridDim.y);
 
   TileAt at;
@@ -204,9 +203,9 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   at.nb = nb;
   at.tile_a = tile_a;
 
-  Stager<LA0, Sh::BM, Sh::K, NA> sa0;
-  Stager<LA1, Sh::BM, Sh::K, NA> sa1;
-  Stager<LB, Sh::BN, Sh::K, NB> sb;
+  Stager<LA0, Sh::BM, NA> sa0;
+  Stager<LA1, Sh::BM, NA> sa1;
+  Stager<LB, Sh::BN, NB> sb;
   const long lda0 = LA0 == kRows ? g.A[0].sa : g.A[0].sk, lda1 = LA1 == kRows ? g.A[1].sa : g.A[1].sk;
   const long ldb0 = LB == kRows ? g.B[0].sa : g.B[0].sk;
   sa0.init(a_first, g.A[0].n, lda0, wave, lane);
@@ -222,7 +221,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   auto issue = [&](int t) {
     unsigned char* st = smem + (t % Sh::S) * Sh::stage;
     const bool second = t >= T0;
-    const int k = (second ? t - T0 : t) * Sh::K;
+    const int k = (second ? t - T0 : t) * kStep;
     {
       const rsrc_t rb = make_rsrc((second ? b1 : b0) + (LB == kRows ? long(k) : long(k) * ldb0));
 #pragma unroll
@@ -236,9 +235,9 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
         const bf16_t* end = g.A[0].p + (LA0 == kRows ? long(g.A[0].n - 1) * lda0 + K0 : long(K0 - 1) * lda0 + g.A[0].n);
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
-          const uint32_t o = left < Sh::K ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
+          const uint32_t o = left < kStep ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
           held[i] = load_any(reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(p) + o), end);
-          if (LA0 == kRows && left < Sh::K) {   // values behind K belong to the next row
+          if (LA0 == kRows && left < kStep) {   // values behind K belong to the next row
             const int keep = left - min(sa0.chunk_of(lane), (left - 1) / 8) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -250,7 +249,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
     }
     if (!two || !second) {
       const rsrc_t ra = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * (second ? lda1 : lda0)));
-      if (left < Sh::K) {
+      if (left < kStep) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
           buffer_to_lds16(ra, st + sa0.unit_of(wave, i) * 1024,
@@ -262,7 +261,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
       }
     } else {
       const rsrc_t ra = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
-      if (left < Sh::K) {
+      if (left < kStep) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
           buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.tail(i, wave, lane, lda1, left));
@@ -283,22 +282,22 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   };
 
   const int wa = at.wave_a * (Sh::BM / Sh::WA), wb = at.wave_b * (Sh::BN / Sh::WB);
-  bf16x8_t fa[Sh::FK][Sh::FM], fb[Sh::FK][Sh::FN];   // a step's fragments
+  bf16x8_t fa[2][Sh::FM], fb[2][Sh::FN];   // a step's fragments
   f32x4_t acc[Sh::FM][Sh::FN];
   auto read = [&](int t) {
     const unsigned char* st = smem + (t % Sh::S) * Sh::stage;
 #pragma unroll
-    for (int half = 0; half < Sh::FK; ++half) {
-      read_frags<LB, Sh::BN, Sh::K>(fb[half], st + Sh::a_bytes, wb, half, lane);
+    for (int half = 0; half < 2; ++half) {
+      read_frags<LB, Sh::BN>(fb[half], st + Sh::a_bytes, wb, half, lane);
       if (two && t >= T0)
-        read_frags<LA1, Sh::BM, Sh::K>(fa[half], st, wa, half, lane);
+        read_frags<LA1, Sh::BM>(fa[half], st, wa, half, lane);
       else
-        read_frags<LA0, Sh::BM, Sh::K>(fa[half], st, wa, half, lane);
+        read_frags<LA0, Sh::BM>(fa[half], st, wa, half, lane);
     }
   };
   auto multiply = [&]() {
 #pragma unroll
-    for (int half = 0; half < Sh::FK; ++half)
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < Sh::FM; ++i)
 #pragma unroll
@@ -306,7 +305,8 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[half][i], fb[half][j], acc[i][j], 0, 0, 0);
   };
   // A ring of S stages, one barrier a step; other workgroups of the compute
-  // unit multiply while this one waits.
+  // unit multiply while this one waits.  Loads go before the fragment reads
+  // (after them: 800 us against 780 for a 5120 x 5120 layer's training pass).
   constexpr int per_step = NA + NB;
 #pragma unroll
   for (int s = 0; s < Sh::S - 1; ++s)
@@ -365,7 +365,7 @@ template <int LAYOUT, int ROWS>
 __device__ __forceinline__ uint32_t unit_offset(int unit, int lane, uint32_t ld2, int last_row, int last_chunk) {
   constexpr int chunks = LAYOUT == kRows ? kStep / 8 : ROWS / 8;
   const int at = unit * 64 + lane, row = at / chunks;
-  const int c = (at % chunks) ^ (LAYOUT == kRows ? chunk_turn(kStep, row) : pair_turn(ROWS, row) << 1);
+  const int c = (at % chunks) ^ (LAYOUT == kRows ? chunk_turn(row) : pair_turn(ROWS, row) << 1);
   return uint32_t(min(row, last_row)) * ld2 + uint32_t(min(c, last_chunk)) * 16;
 }
 
@@ -487,11 +487,11 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
       asm volatile("" : "+v"(vlane));
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        read_frags<LB, 256, kStep>(fb[half], sb, at.wave_b * 64, half, vlane);
+        read_frags<LB, 256>(fb[half], sb, at.wave_b * 64, half, vlane);
         if (two && t >= T0)
-          read_frags<LA1, 128, kStep>(fa[half], sa, 0, half, vlane);
+          read_frags<LA1, 128>(fa[half], sa, 0, half, vlane);
         else
-          read_frags<LA0, 128, kStep>(fa[half], sa, 0, half, vlane);
+          read_frags<LA0, 128>(fa[half], sa, 0, half, vlane);
       }
       const int next_a = t + 2, next_b = lead ? t + 2 : t + 3;
       if (next_a < t_end) prepare_a(next_a, false);
@@ -569,14 +569,14 @@ hipError_t launch_tile_bf16(const Product<bf16_t>& g, const Epi& epi, int na, in
 // Few rows: bound by reading the a operand once, so narrow tiles with a deep
 // ring, several workgroups per compute unit.  Many rows: 256 x 256, where one
 // step's 128 MFMAs per SIMD cover the loads of the next.
-using Tile16 = TileShape<128, 16, 4, 1, 64, 4>;
-using Tile32 = TileShape<128, 32, 4, 1, 64, 3>;
-using Tile64 = TileShape<128, 64, 2, 2, 64, 3>;
-using Tile128 = TileShape<128, 128, 2, 2, 64, 2>;
-using Tile128Deep = TileShape<128, 128, 2, 2, 64, 4>;   // one workgroup per compute unit: two steps more in flight
-using Tile16Any = TileShape<128, 16, 4, 1, 64, 2>;
-using Tile32Any = TileShape<128, 32, 4, 1, 64, 2>;
-using Tile64Any = TileShape<128, 64, 2, 2, 64, 2>;
+using Tile16 = TileShape<128, 16, 4, 1, 4>;
+using Tile32 = TileShape<128, 32, 4, 1, 3>;
+using Tile64 = TileShape<128, 64, 2, 2, 3>;
+using Tile128 = TileShape<128, 128, 2, 2, 2>;
+using Tile128Deep = TileShape<128, 128, 2, 2, 4>;   // one workgroup per compute unit: two steps more in flight
+using Tile16Any = TileShape<128, 16, 4, 1, 2>;
+using Tile32Any = TileShape<128, 32, 4, 1, 2>;
+using Tile64Any = TileShape<128, 64, 2, 2, 2>;
 
 constexpr int kComputeUnits = 256;
 
