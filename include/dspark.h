@@ -56,7 +56,7 @@ typedef enum {
 /* Activation of dspark_linear. */
 typedef enum {
   DSPARK_ACT_NONE = 0,  /* z                                            */
-  DSPARK_ACT_RELU = 1,  /* max(z, 0)                                    */
+  DSPARK_ACT_RELU = 1,  /* max(z, 0); NaN stays NaN                     */
   DSPARK_ACT_GELU = 2,  /* z Phi(z), Phi the standard normal's integral */
   DSPARK_ACT_SILU = 3   /* z / (1 + exp(-z))                            */
 } dspark_activation;
@@ -569,7 +569,7 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
  *   dz = dy act'(z)   (rounded to the storage type for the two products)
  *   dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz
  * each summed in fp32 and rounded once; the residual's gradient is dy itself.
- * relu's slope at 0 is 0.
+ * relu's slope at 0 is 0, at NaN it is NaN.
  *
  * Arguments: sizes, types and layouts as dspark_linear, and
  *   dy   [M][N]      16-byte aligned

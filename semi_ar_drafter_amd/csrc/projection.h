@@ -174,15 +174,15 @@ template <> __device__ __forceinline__ float sigmoid<bf16_t>(float z) {
 template <typename T>
 __device__ __forceinline__ float act_value(int act, float z) {
   float e;
-  if (act == 1) return z > 0.f ? z : 0.f;
+  if (act == 1) return z < 0.f ? 0.f : z;   // NaN stays NaN
   if (act == 2) return z * normal_cdf<T>(z, &e);
   if (act == 3) return z * sigmoid<T>(z);
   return z;
 }
-// d act / dz
+// d act / dz (relu: 0 at 0, NaN at NaN)
 template <typename T>
 __device__ __forceinline__ float act_slope(int act, float z) {
-  if (act == 1) return z > 0.f ? 1.f : 0.f;
+  if (act == 1) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
   if (act == 2) {
     float e;
     const float c = normal_cdf<T>(z, &e);
