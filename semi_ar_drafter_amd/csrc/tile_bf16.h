@@ -14,6 +14,9 @@
 // The exchange is made on the global side (each lane picks which chunk it
 // loads), because a direct-to-LDS load always writes lane after lane.
 //
+// Byte offsets inside a step are 32 bits: of a row length up to 2^24 values,
+// 127 rows fit.
+//
 // Requirements, all met by the callers: bases 16-byte aligned; the b operand
 // rows of a multiple of 8 values, zero from K to the next multiple of 64
 // (kRows: the columns, kCols: the rows), so that whatever finite values the a
@@ -402,8 +405,10 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   const int f0 = min(at.a0, LA0 == kRows ? n0 - 1 : (n0 - 1) & ~7), f1 = min(at.a0, LA1 == kRows ? n1 - 1 : (n1 - 1) & ~7);
   const bf16_t* a0 = g.A[0].p + (LA0 == kRows ? long(f0) * lda0 : long(f0));
   const bf16_t* a1 = g.A[1].p + (LA1 == kRows ? long(f1) * lda1 : long(f1));
-  const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(b_first) * ldb : long(b_first));
-  const bf16_t* b1 = g.B[1].p + (LB == kRows ? long(b_first) * ldb : long(b_first));
+  // kRows: from the wave's own 32 rows on, since 256 rows can be longer than a 32-bit offset reaches
+  const int bf = LB == kRows ? min(b_first + wave * 32, nbo - 1) : b_first;
+  const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(bf) * ldb : long(bf));
+  const bf16_t* b1 = g.B[1].p + (LB == kRows ? long(bf) * ldb : long(bf));
 
   // What a step's loads need besides the lane offsets: made while fragments
   // are on their way, so that little but the loads stands between the MFMAs.
@@ -413,7 +418,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     off_b[i] = LB == kRows
-        ? unit_offset<LB, 256>(wave * 4 + i, lane, uint32_t(ldb * 2), nbo - 1 - b_first, kStep / 8 - 1)
+        ? unit_offset<LB, 256>(i, lane, uint32_t(ldb * 2), nbo - 1 - bf, kStep / 8 - 1)
         : unit_offset<LB, 256>(wave * 4 + i, lane, uint32_t(ldb * 2), kStep - 1, (nbo - 1 - b_first) / 8);
   auto prepare_a = [&](int t, bool fresh) {   // this wave's four of its half's 16 units
     const bool second = t >= T0;

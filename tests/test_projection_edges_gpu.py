@@ -50,3 +50,21 @@ def test_nan_passes_every_activation(act, dtype):
         dx, dw, db = linear_backward(dy, x, w, act=act, pre=pre)
         assert torch.isnan(dx[1]).all() and torch.isfinite(dx[rest]).all()
         assert torch.isnan(dw).all() and torch.isnan(db).all()
+
+
+# ---------------------------------------------------------------------------
+# the largest sizes
+# ---------------------------------------------------------------------------
+def test_row_gradient_of_very_many_features():
+    """Rows of dy so long that 256 of them take more than 2^32 bytes: every row
+    of dx is its own row's product.  Row m of dy is 1 + m % 7 in the last 64
+    features and zero elsewhere, w is 1 there: dx is 64 (1 + m % 7), exact."""
+    M, N, K = 256, 8421504 + 64, 1024
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    dy, w = torch.zeros(M, N, dtype=torch.bfloat16, device=DEV), torch.zeros(N, K, dtype=torch.bfloat16, device=DEV)
+    row = 1 + torch.arange(M, device=DEV) % 7
+    dy[:, -64:] = row[:, None].to(torch.bfloat16)
+    w[-64:] = 1
+    dx, _, _ = linear_backward(dy, torch.empty(M, K, dtype=torch.bfloat16, device=DEV), w, need=("dx",))
+    assert torch.equal(dx.float(), (64.0 * row)[:, None].expand(M, K))
