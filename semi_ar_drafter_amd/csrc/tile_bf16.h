@@ -19,10 +19,11 @@
 //
 // Requirements, all met by the callers: bases 16-byte aligned; the b operand
 // rows of a multiple of 8 values, zero from K to the next multiple of 64
-// (kRows: the columns, kCols: the rows), so that whatever finite values the a
-// operand repeats there do not count.  The a operand either has rows of a
-// multiple of 8 values (direct loads), or any row length (ANY: loads to
-// registers at element alignment, then LDS).
+// (kRows: the columns, kCols: the rows); the a operand, whatever its memory
+// holds there, is loaded as zeros behind K, so that no infinity meets a zero.
+// Its rows either have a multiple of 8 values (direct loads; up to 7 values
+// behind K, in the row's own padding, have to be finite), or any number (ANY:
+// loads to registers at element alignment, then LDS).
 #pragma once
 #include "projection.h"
 
@@ -35,10 +36,14 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) unsigned char lds_u8_t;
 
+// A load from kNowhere on, where the buffer ends, gives zeros.  It lies behind
+// every offset of a step (127 rows of 2^25 bytes and a chunk: below 0xFE000100).
+constexpr uint32_t kNowhere = 0xFF000000u;
+
 #if defined(__HIP_DEVICE_COMPILE__)
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kNowhere), 0x00020000);
 }
 // lane j: 16 bytes from base + off (per lane) to lds + 16 j
 __device__ __forceinline__ void buffer_to_lds16(rsrc_t r, unsigned char* lds, uint32_t off) {
@@ -106,15 +111,14 @@ struct Stager {
     }
   }
 
-  // The last step of a contraction that ends inside it: chunks (kRows) or
-  // rows (kCols) behind its end repeat the last one.  left: what is left of it.
-  __device__ __forceinline__ uint32_t tail(int i, int w, int lane, long ld, int left) const {
-    if (LAYOUT == kRows) {
-      const int c = chunk_of(lane), last = (left - 1) / 8;
-      return c > last ? off[i] - uint32_t(c - last) * 16 : off[i];
-    }
-    const int k = (unit_of(w, i) * 64 + lane) / chunks;
-    return k >= left ? off[i] - uint32_t(k - (left - 1)) * uint32_t(ld * 2) : off[i];
+  // The last step of a contraction that ends inside it: whether the chunk
+  // (kRows) or row (kCols) of a load lies behind its end.  left: what is left of it.
+  __device__ __forceinline__ static bool behind(int i, int w, int lane, int left) {
+    return LAYOUT == kRows ? chunk_of(lane) * 8 >= left : (unit_of(w, i) * 64 + lane) / chunks >= left;
+  }
+  // Offset of a direct load of that step: zeros behind the end.
+  __device__ __forceinline__ uint32_t tail(int i, int w, int lane, int left) const {
+    return behind(i, w, lane, left) ? kNowhere : off[i];
   }
 };
 
@@ -238,10 +242,13 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
         const bf16_t* end = g.A[0].p + (LA0 == kRows ? long(g.A[0].n - 1) * lda0 + K0 : long(K0 - 1) * lda0 + g.A[0].n);
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
-          const uint32_t o = left < kStep ? sa0.tail(i, wave, lane, lda0, left) : sa0.off[i];
-          held[i] = load_any(reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(p) + o), end);
+          if (left < kStep && sa0.behind(i, wave, lane, left)) {
+            held[i] = u32x4_t{0u, 0u, 0u, 0u};
+            continue;
+          }
+          held[i] = load_any(reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(p) + sa0.off[i]), end);
           if (LA0 == kRows && left < kStep) {   // values behind K belong to the next row
-            const int keep = left - min(sa0.chunk_of(lane), (left - 1) / 8) * 8;
+            const int keep = left - sa0.chunk_of(lane) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (e >= keep) held[i][e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
@@ -256,7 +263,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
 #pragma unroll
         for (int i = 0; i < NA; ++i)
           buffer_to_lds16(ra, st + sa0.unit_of(wave, i) * 1024,
-                          second ? sa1.tail(i, wave, lane, lda1, left) : sa0.tail(i, wave, lane, lda0, left));
+                          second ? sa1.tail(i, wave, lane, left) : sa0.tail(i, wave, lane, left));
       } else {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
@@ -267,7 +274,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
       if (left < kStep) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-          buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.tail(i, wave, lane, lda1, left));
+          buffer_to_lds16(ra, st + sa1.unit_of(wave, i) * 1024, sa1.tail(i, wave, lane, left));
       } else {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
@@ -361,15 +368,27 @@ struct Tile256 {
 };
 
 // Byte offset of what `lane` loads in unit `unit` (1 KiB) of a tile of ROWS
-// rows (of a, or values of one k), not held in registers.  last_row, last_chunk:
-// kRows: last row of the operand, from the tile's first, and (as the step's
-// end needs it) last chunk; kCols: the same with the roles exchanged.
+// rows (of a, or values of one k), not held in registers.  n: the operand's
+// size along its axis, from the tile's first on; what lies behind repeats the
+// last.  left: what is left of the contraction; zeros behind it.
 template <int LAYOUT, int ROWS>
-__device__ __forceinline__ uint32_t unit_offset(int unit, int lane, uint32_t ld2, int last_row, int last_chunk) {
+__device__ __forceinline__ uint32_t unit_offset(int unit, int lane, uint32_t ld2, int n, int left) {
   constexpr int chunks = LAYOUT == kRows ? kStep / 8 : ROWS / 8;
   const int at = unit * 64 + lane, row = at / chunks;
   const int c = (at % chunks) ^ (LAYOUT == kRows ? chunk_turn(row) : pair_turn(ROWS, row) << 1);
-  return uint32_t(min(row, last_row)) * ld2 + uint32_t(min(c, last_chunk)) * 16;
+  const bool behind = LAYOUT == kRows ? c * 8 >= left : row >= left;
+  const uint32_t off = LAYOUT == kRows ? uint32_t(min(row, n - 1)) * ld2 + uint32_t(c) * 16
+                                       : uint32_t(row) * ld2 + uint32_t(min(c, (n - 1) / 8)) * 16;
+  return behind ? kNowhere : off;
+}
+
+// x, so that what is made from it is made here: held over the loop, read
+// addresses and the last steps' offsets would spill what the MFMAs need.
+__device__ __forceinline__ int here(int x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(x));
+#endif
+  return x;
 }
 
 template <int LA0, int LA1, int LB, class Epi>
@@ -417,9 +436,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   unsigned char *lds_a, *lds_b;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    off_b[i] = LB == kRows
-        ? unit_offset<LB, 256>(i, lane, uint32_t(ldb * 2), nbo - 1 - bf, kStep / 8 - 1)
-        : unit_offset<LB, 256>(wave * 4 + i, lane, uint32_t(ldb * 2), kStep - 1, (nbo - 1 - b_first) / 8);
+    off_b[i] = unit_offset<LB, 256>(LB == kRows ? i : wave * 4 + i, lane, uint32_t(ldb * 2), nbo - bf, kStep);
   auto prepare_a = [&](int t, bool fresh) {   // this wave's four of its half's 16 units
     const bool second = t >= T0;
     const int k = (second ? t - T0 : t) * kStep, left = (second ? K1 : K0) - k;
@@ -428,21 +445,18 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
       const long ld = second ? lda1 : lda0;
       rsrc_a = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * ld));
       if (fresh || t == T0 || left < kStep) {
-        const int n = second ? n1 - f1 : n0 - f0;
+        const int n = second ? n1 - f1 : n0 - f0, vlane = here(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          off_a[i] = LA0 == kRows
-              ? unit_offset<LA0, 128>(w4 * 4 + i, lane, uint32_t(ld * 2), n - 1, (min(left, kStep) - 1) / 8)
-              : unit_offset<LA0, 128>(w4 * 4 + i, lane, uint32_t(ld * 2), left - 1, (n - 1) / 8);
+          off_a[i] = unit_offset<LA0, 128>(w4 * 4 + i, vlane, uint32_t(ld * 2), n, left);
       }
     } else {
       rsrc_a = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
       if (fresh || t == T0 || left < kStep) {
+        const int vlane = here(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          off_a[i] = LA1 == kRows
-              ? unit_offset<LA1, 128>(w4 * 4 + i, lane, uint32_t(lda1 * 2), n1 - f1 - 1, (min(left, kStep) - 1) / 8)
-              : unit_offset<LA1, 128>(w4 * 4 + i, lane, uint32_t(lda1 * 2), left - 1, (n1 - f1 - 1) / 8);
+          off_a[i] = unit_offset<LA1, 128>(w4 * 4 + i, vlane, uint32_t(lda1 * 2), n1 - f1, left);
       }
     }
   };
@@ -486,10 +500,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
     for (int t = t_begin; t < t_end; ++t) {
       const unsigned char* sa = smem + ((t & 1) * 2 + at.wave_a) * Sh::a_half;
       const unsigned char* sb = smem + 4 * Sh::a_half + (t % 3) * Sh::b_step;
-      // read addresses are made again each step: held over the loop, they
-      // would spill what the MFMAs need
-      int vlane = lane;
-      asm volatile("" : "+v"(vlane));
+      const int vlane = here(lane);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         read_frags<LB, 256>(fb[half], sb, at.wave_b * 64, half, vlane);

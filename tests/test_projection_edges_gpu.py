@@ -52,6 +52,38 @@ def test_nan_passes_every_activation(act, dtype):
         assert torch.isnan(dw).all() and torch.isnan(db).all()
 
 
+# Contractions whose last step is not whole, through every tile of the products: few and many rows, rows that are
+# 16-byte aligned, copied, and staged as they are.
+TAILS = [(2, 40, 72), (20, 300, 72), (40, 300, 200), (100, 300, 136), (300, 520, 200), (20, 300, 77), (40, 300, 201),
+         (100, 300, 141), (300, 520, 333), (2000, 4090, 1096)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", TAILS)
+def test_infinities_keep_their_sign(M, N, K, dtype):
+    """One infinite factor in a sum of finite terms: the sum is infinite, with
+    the sign of the other factor, also where it is the last of the contraction
+    and what lies behind it is padding.  The other sums do not see it."""
+    if dtype is torch.float32 and M > 1000:
+        pytest.skip("the size is for the bf16 tiles")
+    x, w, dy = rand(5, M, K, dtype=dtype), rand(6, N, K, sd=0.1, dtype=dtype), rand(7, M, N, dtype=dtype)
+    y0, (dx0, dw0, _) = linear(x, w), linear_backward(dy, x, w)
+    for k in (K - 1, (K - 1) // 64 * 64):
+        v = w.clone()
+        v[N - 1, k], v[0, k] = math.inf, -math.inf
+        y = linear(x, v)
+        assert torch.equal(y[:, N - 1].float(), torch.sign(x[:, k].float()) * math.inf)
+        assert torch.equal(y[:, 0].float(), torch.sign(x[:, k].float()) * -math.inf)
+        assert torch.equal(y[:, 1:N - 1], y0[:, 1:N - 1])
+    # dx sums over the features, dw over the rows
+    v, z = w.clone(), x.clone()
+    v[N - 1, K - 1], z[M - 1, K - 1] = math.inf, -math.inf
+    dx, dw, _ = linear_backward(dy, z, v)
+    assert torch.equal(dx[:, K - 1].float(), torch.sign(dy[:, N - 1].float()) * math.inf)
+    assert torch.equal(dw[:, K - 1].float(), torch.sign(dy[M - 1].float()) * -math.inf)
+    assert torch.equal(dx[:, :K - 1], dx0[:, :K - 1]) and torch.equal(dw[:, :K - 1], dw0[:, :K - 1])
+
+
 # ---------------------------------------------------------------------------
 # the largest sizes
 # ---------------------------------------------------------------------------
