@@ -229,10 +229,12 @@ bool few_rows(int M, int N, int K) {
   return K % 8 == 0 ? M <= 4 || (M <= 16 && N <= 8192) : M <= 16 && N * M <= 32768;
 }
 
-// Whether a product's a operand of `rows` rows of K values is copied to
-// aligned rows: only for many b (77 x 1027 x 1001, split: 17.1 us without,
-// 19.8 with the copy).
-bool copies(int rows, int K, int nb) { return K % 8 != 0 && nb >= 256 && size_t(rows) * up64(K) * 2 <= kCopyBytes; }
+// Whether a product's a operand of `rows` rows (none: nothing to copy) of K
+// values is copied to aligned rows: only for many b (77 x 1027 x 1001, split:
+// 17.1 us without, 19.8 with the copy).
+bool copies(int rows, int K, int nb) {
+  return rows > 0 && K % 8 != 0 && nb >= 256 && size_t(rows) * up64(K) * 2 <= kCopyBytes;
+}
 // Bytes of the copy, and whether the product still sees unaligned rows.
 size_t copy_bytes(int rows, int K, int nb) { return copies(rows, K, nb) ? up256(size_t(rows) * up64(K) * 2) : 0; }
 bool stays_any(int rows, int K, int nb) { return K % 8 != 0 && !copies(rows, K, nb); }

@@ -85,6 +85,22 @@ def test_infinities_keep_their_sign(M, N, K, dtype):
 
 
 # ---------------------------------------------------------------------------
+# empty batches
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("K", [8, 9, 72, 333])
+def test_gradients_of_nothing_are_zero(K, dtype):
+    """No rows: dw and dbias are zero; no features: dx is.  The other axis on
+    both sides of the size from which unaligned rows are copied."""
+    for n in (5, 256, 1030):
+        empty = lambda *sh: torch.empty(sh, dtype=dtype, device=DEV)  # noqa: E731
+        dx, dw, db = linear_backward(empty(0, n), empty(0, K), rand(1, n, K, dtype=dtype))
+        assert dx.shape == (0, K) and dw.shape == (n, K) and not dw.any() and not db.any()
+        dx, dw, db = linear_backward(empty(n, 0), rand(2, n, K, dtype=dtype), empty(0, K))
+        assert dx.shape == (n, K) and not dx.any() and dw.shape == (0, K) and db.shape == (0,)
+
+
+# ---------------------------------------------------------------------------
 # the largest sizes
 # ---------------------------------------------------------------------------
 def test_row_gradient_of_very_many_features():
