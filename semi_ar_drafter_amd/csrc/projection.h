@@ -144,24 +144,28 @@ struct TileAt {
 // Activations
 // ---------------------------------------------------------------------------
 // The normal distribution's integral P(z) and density times sqrt(2 pi),
-// exp(-z^2 / 2).  fp32 storage takes the library's error function.  For bf16
-// storage Abramowitz and Stegun 7.1.26, within 1e-7 of P: erfc(x) = (t (a1 +
-// t (a2 + ..))) exp(-x^2), t = 1 / (1 + p x), x = |z| / sqrt 2, which shares
-// its exponential with the density (about 15 instructions instead of 60).
+// exp(-z^2 / 2).  P by way of erfc(-z / sqrt 2), which keeps its relative
+// accuracy for negative z, where 1 + erf loses it (10 % at z = -5 in fp32).
+// fp32 storage takes the library's function.  For bf16 storage erfc(x) =
+// t q(t) exp(-x^2), t = 1 / (1 + p x), x = |z| / sqrt 2, whose exponential is
+// the density's: q of degree 6, p and q fitted to exp(x^2) erfc(x) on [0, 9.6]
+// for the least relative error, 6e-7 (about 17 instructions instead of 60).
 template <typename T> __device__ __forceinline__ float normal_cdf(float z, float* e);
 template <> __device__ __forceinline__ float normal_cdf<float>(float z, float* e) {
   *e = expf(-0.5f * z * z);
-  return 0.5f * (1.f + erff(z * 0.70710678118654752f));
+  return 0.5f * erfcf(z * -0.70710678118654752f);
 }
 template <> __device__ __forceinline__ float normal_cdf<bf16_t>(float z, float* e) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3725f * x);
   *e = __expf(-x * x);
-  float q = 1.061405429f;
-  q = q * t - 1.453152027f;
-  q = q * t + 1.421413741f;
-  q = q * t - 0.284496736f;
-  q = q * t + 0.254829592f;
+  float q = -0.1394701151540878f;
+  q = q * t + 0.41369502739896746f;
+  q = q * t - 0.16042987722460397f;
+  q = q * t + 0.3019267804465362f;
+  q = q * t + 0.15901532659798573f;
+  q = q * t + 0.21541323049746136f;
+  q = q * t + 0.20984971869445848f;
   const float tail = 0.5f * q * t * *e;   // P(-|z|)
   return z < 0.f ? tail : 1.f - tail;
 }

@@ -12,6 +12,8 @@ torch = pytest.importorskip("torch")
 from semi_ar_drafter_amd import binding, linear, linear_backward  # noqa: E402
 
 DEV = "cuda:0"
+U32 = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}   # half a step of the type
 TYPES = [torch.bfloat16, torch.float32]
 IDS = ["bf16", "f32"]
 
@@ -98,6 +100,37 @@ def test_gradients_of_nothing_are_zero(K, dtype):
         assert dx.shape == (0, K) and dw.shape == (n, K) and not dw.any() and not db.any()
         dx, dw, db = linear_backward(empty(n, 0), rand(2, n, K, dtype=dtype), empty(0, K))
         assert dx.shape == (n, K) and not dx.any() and dw.shape == (0, K) and db.shape == (0,)
+
+
+# ---------------------------------------------------------------------------
+# the activations' tails
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_activations_to_their_own_scale(dtype):
+    """gelu and silu keep the type's precision where they are small: z runs
+    over [-13, 13] (gelu(-13) is 1e-37), as the product of 1 and w.  z is exact.
+    Beside the half step of the result, 64 u z^2 + 64 u: exp(-z^2 / 2) is off
+    by the rounding of its argument (z^2 u, and twice that for its scaling to
+    base 2), silu's exp(-z) by less, and polynomial and quotient by a few u
+    each; gelu's slope Phi + z phi loses a factor of 4 by cancellation at most
+    outside [-1.2, -0.3], and there an absolute 4 u; so does silu's."""
+    N = 6000
+    w = torch.linspace(-13, 13, N, device=DEV).to(dtype)[:, None].contiguous()
+    z = w[:, 0].double()
+    x = torch.ones(1, 1, dtype=dtype, device=DEV)
+    phi, Phi = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi), 0.5 * torch.erfc(-z / math.sqrt(2))
+    sig = torch.sigmoid(z)
+    rel = 64 * U32 * (z * z + 1)
+    for act, value, slope in (("gelu", z * Phi, Phi + z * phi), ("silu", z * sig, sig + z * sig * (1 - sig))):
+        pre = torch.empty(1, N, device=DEV)
+        y = linear(x, w, act=act, pre=pre)
+        assert torch.equal(pre[0].double(), z)
+        off = (y[0].double() - value).abs()
+        assert (off <= (HALF[dtype] + rel) * value.abs() + 1e-38).all(), act
+        _, _, db = linear_backward(torch.ones(1, N, dtype=dtype, device=DEV), x, w, act=act, pre=pre)
+        off = (db.double() - slope).abs()
+        near = 16 * U32 * ((z > -3) & (z < 0)).double()
+        assert (off <= (HALF[dtype] + 4 * rel) * slope.abs() + near + 1e-38).all(), act + " slope"
 
 
 # ---------------------------------------------------------------------------
