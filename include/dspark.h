@@ -552,8 +552,9 @@ dspark_launch dspark_get_draft_launch(void);
  *   workspace     >= dspark_linear_workspace_bytes(M, N, K, dtype) bytes
  *                 (NULL if that is 0), 256-byte aligned, any contents.  Calls
  *                 that can overlap need separate ones.
- * An output that overlaps another array is refused (DSPARK_ERR_INVALID_ARG),
- * but for y == residual.  Results do not depend on execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
+ * An output, or the workspace's stated bytes, that overlap another array are
+ * refused (DSPARK_ERR_INVALID_ARG), but for y == residual.  Results do not
+ * depend on execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
  */
 dspark_status dspark_linear(
     int M, int N, int K, dspark_dtype dtype, const void* x, const void* w, const void* bias,
@@ -578,7 +579,7 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
  *                 With M == 0, dw and dbias are zero; with N == 0, dx is.
  *   workspace     >= dspark_linear_backward_workspace_bytes(M, N, K, dtype)
  *                 bytes, 256-byte aligned, any contents.
- * Outputs that overlap another array are refused.
+ * Outputs or a workspace that overlap another array are refused.
  */
 dspark_status dspark_linear_backward(
     int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x, const void* w,
@@ -615,6 +616,7 @@ size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype 
  *   workspace     >= dspark_markov_loss_workspace_bytes(N, V, d, r, dtype)
  *                 bytes, 256-byte aligned, any contents.  Calls that can
  *                 overlap need separate ones.
+ * Outputs or a workspace that overlap another array are refused.
  * Limits: N <= 2^20, V <= 2^24, d, r <= 65536.  Nothing depends on execution
  * order: the same inputs give the same bits.
  */
@@ -642,8 +644,8 @@ size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dty
  *                 storage type; each may be NULL: not computed
  *   workspace     >= dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype)
  *                 bytes, 256-byte aligned, any contents
- * N == 0 leaves dWo, dW1 and dW2 zero.  Outputs that overlap another array are
- * refused.
+ * N == 0 leaves dWo, dW1 and dW2 zero.  Outputs or a workspace that overlap
+ * another array (g, lse, label and prev among them) are refused.
  */
 dspark_status dspark_markov_loss_backward(
     int N, int V, int d, int r, dspark_dtype dtype, const float* g, const float* lse,
@@ -664,6 +666,7 @@ size_t dspark_markov_loss_backward_workspace_bytes(int N, int V, int d, int r, d
  *   workspace  >= dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dtype)
  *              bytes, 256-byte aligned: the drafting workspace, with its
  *              zero-fill rule, then the projection's.
+ * Outputs (U among them) or a workspace that overlap another array are refused.
  * Limits: those of both, and B * gamma <= 2^20.
  */
 dspark_status dspark_hidden_draft(

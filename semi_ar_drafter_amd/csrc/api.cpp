@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/dspark.h"
 #include "launch.h"
@@ -430,16 +431,18 @@ struct Span {
   const void* p;
   size_t n;
 };
-// Whether any output shares memory with an input or with another output.
-bool any_overlap(const Span* out, int n_out, const Span* in, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+// Whether any output (the workspace is one) shares memory with an input or
+// with another output.
+bool any_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (const Span* o = out.begin(); o != out.end(); ++o) {
+    for (const Span& i : in)
+      if (overlap(o->p, o->n, i.p, i.n)) return true;
+    for (const Span* q = out.begin(); q != o; ++q)
+      if (overlap(o->p, o->n, q->p, q->n)) return true;
   }
   return false;
 }
+dspark_status overlap_refused() { return fail(DSPARK_ERR_INVALID_ARG, "an output or the workspace overlaps another array"); }
 
 // Checks shared by the linear layer's two directions.
 dspark_status linear_sizes(int M, int N, int K, dspark_dtype dtype, dspark_activation act) {
@@ -479,16 +482,16 @@ dspark_status dspark_linear(int M, int N, int K, dspark_dtype dtype, const void*
   if (misaligned(x, 16) || misaligned(w, 16)) return fail(DSPARK_ERR_INVALID_ARG, "x and w need 16-byte alignment");
   if (misaligned(bias, elem) || misaligned(residual, elem) || misaligned(y, elem) || misaligned(pre, 4))
     return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
-  st = check_workspace(workspace, workspace_bytes, dspark_linear_workspace_bytes(M, N, K, dtype),
-                       "dspark_linear_workspace_bytes");
+  const size_t need = dspark_linear_workspace_bytes(M, N, K, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_linear_workspace_bytes");
   if (st != DSPARK_OK) return st;
-  {
-    const size_t m = size_t(M), n = size_t(N), k = size_t(K);
-    const Span out[] = {{y, m * n * elem}, {pre, m * n * 4}};
-    const Span in[] = {
-        {x, m * k * elem}, {w, n * k * elem}, {bias, n * elem}, {residual == y ? nullptr : residual, m * n * elem}};
-    if (any_overlap(out, 2, in, 4)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
-  }
+  const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+  if (any_overlap({{y, m * n * elem}, {pre, m * n * 4}, {workspace, need}},
+                  {{x, m * k * elem},
+                   {w, n * k * elem},
+                   {bias, n * elem},
+                   {residual == y ? nullptr : residual, m * n * elem}}))
+    return overlap_refused();
   dspark::LinearArgs a;
   a.M = M;
   a.N = N;
@@ -527,15 +530,13 @@ dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, co
     return fail(DSPARK_ERR_INVALID_ARG, "x, w and dy need 16-byte alignment");
   if (misaligned(dx, elem) || misaligned(dw, elem) || misaligned(dbias, elem) || misaligned(pre, 4))
     return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
-  st = check_workspace(workspace, workspace_bytes, dspark_linear_backward_workspace_bytes(M, N, K, dtype),
-                       "dspark_linear_backward_workspace_bytes");
+  const size_t need = dspark_linear_backward_workspace_bytes(M, N, K, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_linear_backward_workspace_bytes");
   if (st != DSPARK_OK) return st;
-  {
-    const size_t m = size_t(M), n = size_t(N), k = size_t(K);
-    const Span out[] = {{dx, m * k * elem}, {dw, n * k * elem}, {dbias, n * elem}};
-    const Span in[] = {{dy, m * n * elem}, {x, m * k * elem}, {w, n * k * elem}, {pre, m * n * 4}};
-    if (any_overlap(out, 3, in, 4)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
-  }
+  const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+  if (any_overlap({{dx, m * k * elem}, {dw, n * k * elem}, {dbias, n * elem}, {workspace, need}},
+                  {{dy, m * n * elem}, {x, m * k * elem}, {w, n * k * elem}, {pre, m * n * 4}}))
+    return overlap_refused();
   dspark::LinearBackwardArgs a;
   a.M = M;
   a.N = N;
@@ -603,6 +604,18 @@ dspark::LossArgs loss_args(int N, int V, int d, int r, dspark_dtype dtype, const
   return a;
 }
 
+// any_overlap() with the inputs that the loss and its gradient share.
+bool overlaps_loss(std::initializer_list<Span> out, const dspark::LossArgs& a) {
+  const size_t elem = a.bf16 ? 2 : 4, n = size_t(a.N), v = size_t(a.V), d = size_t(a.d), r = size_t(a.r);
+  return any_overlap(out, {{a.label, n * 4},
+                           {a.prev, n * 4},
+                           {a.U, n * v * elem},
+                           {a.h, n * d * elem},
+                           {a.Wo, v * d * elem},
+                           {a.W1, v * r * elem},
+                           {a.W2, r * v * elem}});
+}
+
 }  // namespace
 
 size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dtype dtype) {
@@ -621,11 +634,11 @@ dspark_status dspark_markov_loss(int N, int V, int d, int r, dspark_dtype dtype,
   if (N == 0) return DSPARK_OK;
   if (!nll || !lse) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
   if (misaligned(nll, 4) || misaligned(lse, 4)) return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
-  st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_workspace_bytes(N, V, d, r, dtype),
-                       "dspark_markov_loss_workspace_bytes");
+  const size_t need = dspark_markov_loss_workspace_bytes(N, V, d, r, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_markov_loss_workspace_bytes");
   if (st != DSPARK_OK) return st;
-  if (overlap(nll, size_t(N) * 4, lse, size_t(N) * 4))
-    return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
+  const size_t rows = size_t(N) * 4;
+  if (overlaps_loss({{nll, rows}, {lse, rows}, {workspace, need}}, a)) return overlap_refused();
   a.nll = nll;
   a.lse = lse;
   hipError_t e = dspark::launch_markov_loss(a, stream);
@@ -654,15 +667,13 @@ dspark_status dspark_markov_loss_backward(int N, int V, int d, int r, dspark_dty
   if (misaligned(g, 4) || misaligned(lse, 4) || misaligned(dU, elem) || misaligned(dh, elem) ||
       misaligned(dWo, elem) || misaligned(dW1, elem) || misaligned(dW2, elem))
     return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
-  st = check_workspace(workspace, workspace_bytes, dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype),
-                       "dspark_markov_loss_backward_workspace_bytes");
+  const size_t need = dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_markov_loss_backward_workspace_bytes");
   if (st != DSPARK_OK) return st;
-  {
-    const size_t n = size_t(N) * elem, v = size_t(V) * elem, R = size_t(r), D = size_t(d);
-    const Span out[] = {{dU, n * V}, {dh, n * D}, {dWo, v * D}, {dW1, v * R}, {dW2, v * R}};
-    const Span in[] = {{U, n * V}, {h, n * D}, {Wo, v * D}, {W1, v * R}, {W2, v * R}};
-    if (any_overlap(out, 5, in, 5)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps another array");
-  }
+  const size_t n = size_t(N) * elem, v = size_t(V) * elem, rows = size_t(N) * 4;
+  const std::initializer_list<Span> out = {
+      {dU, n * V}, {dh, n * d}, {dWo, v * d}, {dW1, v * r}, {dW2, v * r}, {workspace, need}};
+  if (overlaps_loss(out, a) || any_overlap(out, {{g, rows}, {lse, rows}})) return overlap_refused();
   a.lse_in = lse;
   a.g = g;
   a.dU = dU;
@@ -693,10 +704,30 @@ dspark_status dspark_hidden_draft(int B, int gamma, int V, int r, int d, dspark_
   dspark_status st = draft_impl(B, gamma, V, r, d, dtype, anchor, U, h, W1, W2, nullptr, false, conf_w, conf_b, sts_T,
                                 mode, seed, tokens, logit, conf, surv, workspace, workspace_bytes, stream, false,
                                 nullptr, nullptr, /*check_only=*/true);
-  if (st != DSPARK_OK || B == 0 || gamma == 0) return st;
+  // (they ask the device last: what is wrong with the arrays is said where there is none, too)
+  if ((st != DSPARK_OK && st != DSPARK_ERR_HIP) || B == 0 || gamma == 0) return st;
   const size_t draft = dspark_draft_workspace_bytes(B, gamma, V, r);
   if (workspace_bytes < dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dtype))
     return fail(DSPARK_ERR_WORKSPACE, "workspace smaller than dspark_hidden_draft_workspace_bytes()");
+  {
+    const size_t elem = dtype == DSPARK_BF16 ? 2 : 4, n = size_t(B) * gamma, v = size_t(V);
+    if (any_overlap({{U, n * v * elem},
+                     {tokens, n * 4},
+                     {logit, n * 4},
+                     {conf, n * 4},
+                     {surv, n * 4},
+                     {workspace, dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dtype)}},
+                    {{anchor, size_t(B) * 4},
+                     {h, n * d * elem},
+                     {Wo, v * d * elem},
+                     {bias, v * elem},
+                     {W1, v * r * elem},
+                     {W2, v * r * elem},
+                     {conf_w, (size_t(d) + r) * 4},
+                     {sts_T, size_t(gamma) * 4}}))
+      return overlap_refused();
+  }
+  if (st != DSPARK_OK) return st;
   st = dspark_linear(B * gamma, V, d, dtype, h, Wo, bias, DSPARK_ACT_NONE, nullptr, U, nullptr,
                      static_cast<unsigned char*>(workspace) + draft, workspace_bytes - draft, stream);
   if (st != DSPARK_OK) return st;
