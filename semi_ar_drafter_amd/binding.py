@@ -806,6 +806,8 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
     arguments and the result as markov_draft."""
     torch = _torch()
     lib = load()
+    if mode not in ("greedy", "gumbel"):
+        raise ValueError('mode must be "greedy" or "gumbel"')
     dt = _storage(h, "h")
     B, gamma, d = h.shape
     V, r = W1.shape
@@ -827,9 +829,14 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
                    torch.empty((B, gamma), dtype=torch.float32, device=dev),
                    torch.empty((B, gamma), dtype=torch.float32, device=dev))
         tokens, logit, conf, surv = out
+        _need(tokens, "tokens", torch.int32, (B, gamma), dev)
+        for t, name in ((logit, "logit"), (conf, "conf"), (surv, "surv")):
+            _need(t, name, torch.float32, (B, gamma), dev)
         nbytes = int(lib.dspark_hidden_draft_workspace_bytes(B, gamma, V, r, d, dt))
         ws = workspace
-        if ws is None:
+        if ws is not None:
+            _need(ws, "workspace", torch.uint8, None, dev)
+        else:
             ws = _captured(nbytes, dev, zero=True) or _workspace(nbytes, dev, "hidden_draft", (B, gamma))
         _check(lib.dspark_hidden_draft(
             B, gamma, V, r, d, dt, _ptr(anchor), _ptr(h), _ptr(Wo), _ptr(bias), _ptr(W1), _ptr(W2), _ptr(conf_w),

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from semi_ar_drafter_amd import binding, linear, linear_backward  # noqa: E402
+from semi_ar_drafter_amd import binding, hidden_draft, linear, linear_backward  # noqa: E402
 
 DEV = "cuda:0"
 U32 = 2.0 ** -24
@@ -149,3 +149,69 @@ def test_row_gradient_of_very_many_features():
     w[-64:] = 1
     dx, _, _ = linear_backward(dy, torch.empty(M, K, dtype=torch.bfloat16, device=DEV), w, need=("dx",))
     assert torch.equal(dx.float(), (64.0 * row)[:, None].expand(M, K))
+
+
+# ---------------------------------------------------------------------------
+# drafting from hidden states
+# ---------------------------------------------------------------------------
+def hidden_inputs(B, gamma, V, d, r, dtype, seed=0):
+    return (torch.randint(0, V, (B,), generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV,
+                          dtype=torch.int32),
+            rand(seed + 1, B, gamma, d, dtype=dtype), rand(seed + 2, V, d, sd=(2 / d) ** 0.5, dtype=dtype),
+            rand(seed + 3, V, r, sd=r ** -0.25, dtype=dtype), rand(seed + 4, r, V, sd=r ** -0.25, dtype=dtype),
+            rand(seed + 5, d + r, sd=0.05), 1.0, torch.ones(gamma, device=DEV))
+
+
+def test_hidden_draft_refusals():
+    """What is not a device tensor of the right type and shape gets no further
+    than the binding; neither does a workspace that is too small."""
+    B, gamma, V, d, r = 3, 4, 500, 16, 32
+    args = hidden_inputs(B, gamma, V, d, r, torch.bfloat16)
+    good = [torch.empty(B, gamma, dtype=t, device=DEV) for t in (torch.int32,) + (torch.float32,) * 3]
+    hidden_draft(*args, out=good)
+    for i in range(4):
+        for wrong, error in ((good[i].cpu(), ValueError), (good[i][:, :3].contiguous(), ValueError),
+                             (good[i].half(), TypeError), (good[i].t().contiguous().t(), ValueError), (None, TypeError)):
+            with pytest.raises(error):
+                hidden_draft(*args, out=good[:i] + [wrong] + good[i + 1:])
+    for wrong, error in ((torch.zeros(1 << 20, dtype=torch.uint8), ValueError),
+                         (torch.zeros(1 << 20, device=DEV), TypeError),
+                         (torch.zeros(64, dtype=torch.uint8, device=DEV), binding.DSparkError)):
+        with pytest.raises(error):
+            hidden_draft(*args, workspace=wrong)
+    for mode in ("argmax", "Greedy", None):
+        with pytest.raises(ValueError):
+            hidden_draft(*args, mode=mode)
+
+
+@pytest.mark.parametrize("B,gamma", [(2, 8), (40, 3)])
+def test_hidden_draft_captured_and_replayed(B, gamma):
+    """Two graphs, captured one after the other and replayed with new inputs in
+    place, with eager calls between the replays."""
+    V, d, r = 2000, 48, 32
+    sets = [hidden_inputs(B, gamma, V, d, r, torch.bfloat16, seed=10 * i) for i in range(3)]
+
+    def work(args):
+        U = torch.empty(B, gamma, V, dtype=torch.bfloat16, device=DEV)
+        return [U, *hidden_draft(*args, U=U)]
+
+    want = [[t.clone() for t in work(a)] for a in sets]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        held = [t.clone() if isinstance(t, torch.Tensor) else t for t in sets[0]]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = work(held)
+        graphs.append((graph, held, outs))
+    for i in (1, 2, 0, 1):
+        for j, (graph, held, _) in enumerate(graphs):
+            for dst, src in zip(held, sets[(i + j) % 3]):
+                if isinstance(dst, torch.Tensor):
+                    dst.copy_(src)
+            graph.replay()
+        eager = work(sets[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, want[i]))
+        for j, (_, _, outs) in enumerate(graphs):
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[(i + j) % 3]))
