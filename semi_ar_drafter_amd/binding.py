@@ -603,6 +603,17 @@ def _optional(t, name, dtype, shape, device):
         _is(t, name, dtype, shape, device)
 
 
+def _no_graph(name, *tensors):
+    """The operators record nothing for autograd: a tensor whose gradient it
+    would be asked for is refused rather than cut off silently."""
+    if _torch().is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{name}() records no graph for autograd: call it under torch.no_grad() (or on "
+                                   "detached tensors); gradients come from linear_backward() and "
+                                   "markov_loss_backward()")
+
+
 @functools.lru_cache(maxsize=4096)
 def _bytes(name, *sizes):
     """dspark_<name>_workspace_bytes of these sizes."""
@@ -669,7 +680,9 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     x [M, K], w [N, K], bias [N] and residual [M, N] are all float32 or all
     bfloat16 device tensors; act is "none", "relu", "gelu" (with the error
     function) or "silu".  `pre`, a float32 [M, N] tensor, receives
-    x @ w.T + bias for linear_backward.  `out` takes y; it may be `residual`."""
+    x @ w.T + bias for linear_backward.  `out` takes y; it may be `residual`.
+    Nothing is recorded for autograd: inputs that require a gradient are
+    refused while torch's gradient mode is on."""
     torch = _torch()
     lib = load()
     dt = _storage(x, "x")
@@ -682,6 +695,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     _optional(pre, "pre", torch.float32, (M, N), dev)
     _optional(out, "out", x.dtype, (M, N), dev)
     a = _act(act)
+    _no_graph("linear", x, w, bias, residual)
     with _on(dev), _launching:
         y = out if out is not None else x.new_empty((M, N))
         ws, n = _scratch(_bytes("linear", M, N, K, dt), dev, "linear", workspace)
@@ -708,6 +722,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     _optional(pre, "pre", torch.float32, (M, N), dev)
     if set(need) - {"dx", "dw", "dbias"}:
         raise ValueError("need names dx, dw and dbias")
+    _no_graph("linear_backward", dy, x, w, pre)
     with _on(dev), _launching:
         new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
         dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
@@ -749,10 +764,12 @@ def markov_loss(label, U=None, h=None, Wo=None, prev=None, W1=None, W2=None, out
 
     label int32 [N] (outside [0, V): the row is ignored, its nll and lse are
     0), U [N, V], h [N, d], Wo [V, d], prev int32 [N], W1 [V, r], W2 [r, V];
-    each of the three parts may be left out, not all."""
+    each of the three parts may be left out, not all.  Nothing is recorded for
+    autograd, as for linear()."""
     torch = _torch()
     lib = load()
     N, V, d, r, dt, dev = _loss_inputs(label, U, h, Wo, prev, W1, W2)
+    _no_graph("markov_loss", U, h, Wo, W1, W2)
     with _on(dev), _launching:
         if out is None:
             out = (torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev))
@@ -776,6 +793,7 @@ def markov_loss_backward(g, lse, label, U=None, h=None, Wo=None, prev=None, W1=N
     N, V, d, r, dt, dev = _loss_inputs(label, U, h, Wo, prev, W1, W2)
     _is(g, "g", torch.float32, (N,), dev)
     _is(lse, "lse", torch.float32, (N,), dev)
+    _no_graph("markov_loss_backward", g, lse, U, h, Wo, W1, W2)
     shapes = {}
     if U is not None:
         shapes["dU"] = (N, V)

@@ -9,7 +9,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from semi_ar_drafter_amd import binding, hidden_draft, linear, linear_backward  # noqa: E402
+from semi_ar_drafter_amd import (binding, hidden_draft, linear, linear_backward, markov_loss,  # noqa: E402
+                                 markov_loss_backward)
 
 DEV = "cuda:0"
 U32 = 2.0 ** -24
@@ -149,6 +150,32 @@ def test_row_gradient_of_very_many_features():
     w[-64:] = 1
     dx, _, _ = linear_backward(dy, torch.empty(M, K, dtype=torch.bfloat16, device=DEV), w, need=("dx",))
     assert torch.equal(dx.float(), (64.0 * row)[:, None].expand(M, K))
+
+
+# ---------------------------------------------------------------------------
+# autograd
+# ---------------------------------------------------------------------------
+def test_inputs_that_require_a_gradient_are_refused():
+    """The operators record no graph, so they do not take a tensor whose
+    gradient autograd would be asked for; without gradient mode they do."""
+    x, w, b, res = rand(1, 8, 16), rand(2, 24, 16), rand(3, 24), rand(4, 8, 24)
+    label = torch.zeros(8, dtype=torch.int32, device=DEV)
+    s = dict(U=rand(5, 8, 90), h=rand(6, 8, 16), Wo=rand(7, 90, 16), prev=label, W1=rand(8, 90, 8), W2=rand(9, 8, 90))
+    g = torch.ones(8, device=DEV)
+    _, lse = markov_loss(label, **s)
+    calls = [(lambda: linear(x, w, bias=b, residual=res), (x, w, b, res)),
+             (lambda: linear_backward(res, x, w), (res, x, w)),
+             (lambda: markov_loss(label, **s), [s[k] for k in s if k != "prev"]),
+             (lambda: markov_loss_backward(g, lse, label, **s), [g] + [s[k] for k in s if k != "prev"])]
+    for call, tensors in calls:
+        call()
+        for t in tensors:
+            t.requires_grad_(True)
+            with pytest.raises(RuntimeError, match="no graph"):
+                call()
+            with torch.no_grad():
+                call()
+            t.requires_grad_(False)
 
 
 # ---------------------------------------------------------------------------
