@@ -577,8 +577,8 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
  *   pre  fp32 [M][N] z as dspark_linear wrote it (NULL without activation)
  *   dx [M][K], dw [N][K], dbias [N] out; each may be NULL: not computed.
  *                 With M == 0, dw and dbias are zero; with N == 0, dx is.
- *   workspace     >= dspark_linear_backward_workspace_bytes(M, N, K, dtype)
- *                 bytes, 256-byte aligned, any contents.
+ *   workspace     >= dspark_linear_backward_act_workspace_bytes(M, N, K, dtype,
+ *                 act) bytes, 256-byte aligned, any contents.
  * Outputs or a workspace that overlap another array are refused.
  */
 dspark_status dspark_linear_backward(
@@ -586,6 +586,10 @@ dspark_status dspark_linear_backward(
     dspark_activation act, const float* pre, void* dx, void* dw, void* dbias,
     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Bytes of workspace dspark_linear_backward needs with this activation, and
+ * with any of them: an activation's dz is an array of its own (M * N values),
+ * without one it is dy itself where the sizes allow. */
+size_t dspark_linear_backward_act_workspace_bytes(int M, int N, int K, dspark_dtype dtype, dspark_activation act);
 size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
 
 /*

@@ -97,7 +97,7 @@ def _declare(lib):
     lib.dspark_hidden_draft.argtypes = ([c_int] * 6 + [c_vp] * 7 + [c_f, c_vp, c_int, c_u64] + [c_vp] * 6 +
                                         [c_size, c_vp])
     lib.dspark_hidden_draft.restype = c_int
-    for name, n in (("linear", 4), ("linear_backward", 4), ("markov_loss", 5), ("markov_loss_backward", 5),
+    for name, n in (("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5), ("markov_loss_backward", 5),
                     ("hidden_draft", 6)):
         f = getattr(lib, f"dspark_{name}_workspace_bytes")
         f.argtypes, f.restype = [c_int] * n, c_size
@@ -726,8 +726,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     with _on(dev), _launching:
         new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
         dx, dw, db = new("dx", M, K), new("dw", N, K), new("dbias", N)
-        ws, n = _scratch(_bytes("linear_backward", M, N, K, dt), dev, "linear_backward",
-                         workspace)
+        ws, n = _scratch(_bytes("linear_backward_act", M, N, K, dt, a), dev, "linear_backward", workspace)
         _check(lib.dspark_linear_backward(M, N, K, dt, _at(dy), _at(x), _at(w), a, _at(pre), _at(dx), _at(dw),
                                           _at(db), ws, n, _raw_stream(dev)))
     return dx, dw, db

@@ -510,9 +510,13 @@ dspark_status dspark_linear(int M, int N, int K, dspark_dtype dtype, const void*
   return DSPARK_OK;
 }
 
-size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+size_t dspark_linear_backward_act_workspace_bytes(int M, int N, int K, dspark_dtype dtype, dspark_activation act) {
   if (M < 0 || N <= 0 || K < 0 || M > dspark::kMaxRows || N > kMaxV || K > kMaxD || !known_dtype(dtype)) return 0;
-  return dspark::linear_backward_workspace_bytes(M, N, K, dtype == DSPARK_BF16);
+  return dspark::linear_backward_workspace_bytes(M, N, K, dtype == DSPARK_BF16, act != DSPARK_ACT_NONE);
+}
+
+size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+  return dspark_linear_backward_act_workspace_bytes(M, N, K, dtype, DSPARK_ACT_RELU);
 }
 
 dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x,
@@ -530,8 +534,8 @@ dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, co
     return fail(DSPARK_ERR_INVALID_ARG, "x, w and dy need 16-byte alignment");
   if (misaligned(dx, elem) || misaligned(dw, elem) || misaligned(dbias, elem) || misaligned(pre, 4))
     return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
-  const size_t need = dspark_linear_backward_workspace_bytes(M, N, K, dtype);
-  st = check_workspace(workspace, workspace_bytes, need, "dspark_linear_backward_workspace_bytes");
+  const size_t need = dspark_linear_backward_act_workspace_bytes(M, N, K, dtype, act);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_linear_backward_act_workspace_bytes");
   if (st != DSPARK_OK) return st;
   const size_t m = size_t(M), n = size_t(N), k = size_t(K);
   if (any_overlap({{dx, m * k * elem}, {dw, n * k * elem}, {dbias, n * elem}, {workspace, need}},

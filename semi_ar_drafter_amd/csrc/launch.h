@@ -143,7 +143,7 @@ struct LinearBackwardArgs {
 };
 constexpr int kMaxRows = 1 << 20;   // rows of the linear layer and of the loss
 size_t linear_workspace_bytes(int M, int N, int K, bool bf16);
-size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16);
+size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16, bool act);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t stream);
 

@@ -332,14 +332,16 @@ LinearEpi<T> plain_epi(void* out, int na) {
   return epi;
 }
 
+// Whether dz is an array of its own: with an activation, or as bf16 b operand,
+// which ends in zeros along both axes.  Otherwise it is dy itself.
+bool copies_dz(int M, int N, bool act, bool bf16) { return act || (bf16 && (N % kStep != 0 || M % kStep != 0)); }
+
 template <typename T>
 hipError_t linear_backward_t(const LinearBackwardArgs& a, hipStream_t stream) {
   const T* dz;
   long ld;
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  // as bf16 b operand dz ends in zeros along both axes
-  const bool copy = a.act != 0 || (a.bf16 && (a.N % kStep != 0 || a.M % kStep != 0));
-  hipError_t e = make_dz(a, copy, a.bf16 ? up64(a.M) : long(a.M), &dz, &ld, &ws, stream);
+  hipError_t e = make_dz(a, copies_dz(a.M, a.N, a.act != 0, a.bf16), a.bf16 ? up64(a.M) : long(a.M), &dz, &ld, &ws, stream);
   if (e != hipSuccess) return e;
   // the a operand, its rows copied where they are not aligned
   auto operand = [&](const void* p, int rows, int nb, const T** out, long* ld_out, float** part) {
@@ -390,8 +392,9 @@ size_t linear_workspace_bytes(int M, int N, int K, bool bf16) {
          split_bytes(N, M, K, true, stays_any(N, K, M), false);
 }
 
-size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16) {
-  const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) + up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4));
+size_t linear_backward_workspace_bytes(int M, int N, int K, bool bf16, bool act) {
+  const size_t dz = up256(size_t(dz_chunks(M)) * N * 4) +
+                    (copies_dz(M, N, act, bf16) ? up256(size_t(up64(M)) * dz_stride(N) * (bf16 ? 2 : 4)) : 0);
   // dx reads w, dw reads x, one after the other
   const size_t dx = (bf16 ? copy_bytes(N, K, M) : 0) + split_bytes(K, M, N, bf16, stays_any(N, K, M), true);
   const size_t dw = (bf16 ? copy_bytes(M, K, N) : 0) + split_bytes(K, N, M, bf16, stays_any(M, K, N), true);

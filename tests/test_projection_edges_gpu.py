@@ -153,6 +153,26 @@ def test_row_gradient_of_very_many_features():
 
 
 # ---------------------------------------------------------------------------
+# workspaces
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_gradient_workspace_of_the_stated_size_is_enough(dtype):
+    """Without an activation, with and without a copy of dy: a workspace of
+    exactly the stated size, in the middle of a larger buffer that keeps what
+    it holds around it, and the same gradients as with a larger one."""
+    size = binding.load().dspark_linear_backward_act_workspace_bytes
+    for M, N, K in ((64, 128, 64), (64, 128, 2050), (300, 512, 256), (2048, 64, 320), (77, 131, 1001), (5, 4100, 129)):
+        x, w, dy = rand(1, M, K, dtype=dtype), rand(2, N, K, sd=0.1, dtype=dtype), rand(3, M, N, dtype=dtype)
+        n = size(M, N, K, 1 if dtype is torch.bfloat16 else 0, 0)
+        room = torch.full((n + 1024,), 91, dtype=torch.uint8, device=DEV)
+        off = 512 + (-(room.data_ptr() + 512)) % 256
+        got = linear_backward(dy, x, w, workspace=room[off:off + n])
+        assert (room[:off] == 91).all() and (room[off + n:] == 91).all()
+        more = torch.empty(n + (64 << 20), dtype=torch.uint8, device=DEV)
+        assert all(torch.equal(a, b) for a, b in zip(got, linear_backward(dy, x, w, workspace=more)))
+
+
+# ---------------------------------------------------------------------------
 # autograd
 # ---------------------------------------------------------------------------
 def test_inputs_that_require_a_gradient_are_refused():

@@ -82,3 +82,24 @@ def test_every_output_that_overlaps_is_refused(lib, entry):
     assert 256 < need <= BIG
     for other in entry.arrays[:-1]:
         refused(lib, entry, INVALID, "overlaps", **{other: entry.values["ws"] + (need - 16) // 256 * 256})
+
+
+def test_workspace_of_a_gradient_without_activation(lib):
+    """dz = dy takes no memory of its own where dy can be read as it is: the
+    output projection's gradient asks for little more than its bias sums."""
+    act = lib.dspark_linear_backward_act_workspace_bytes
+    for dt, elem in ((F32, 4), (BF16, 2)):
+        M, N, K = 4096, 151936, 2560
+        copy = M * N * elem
+        assert act(M, N, K, dt, 0) < copy // 2
+        for a in (1, 2, 3):
+            assert act(M, N, K, dt, a) == act(M, N, K, dt, 0) + copy
+        for size in ((M, N, K), (77, 1027, 1001), (1, 1, 1), (64, 128, 0), (0, 300, 9)):
+            assert lib.dspark_linear_backward_workspace_bytes(*size, dt) == act(*size, dt, 1) >= act(*size, dt, 0)
+    # sizes that are no whole steps are copied for bf16, not for fp32
+    assert act(77, 1027, 1001, BF16, 0) == act(77, 1027, 1001, BF16, 2)
+    assert act(77, 1027, 1001, F32, 0) < act(77, 1027, 1001, F32, 2)
+    assert act(4, 8, 16, 7, 0) == act(-1, 8, 16, BF16, 0) == 0
+    need = act(64, 128, 64, BF16, 0)
+    refused(lib, LINEAR_BACKWARD, WORKSPACE, "smaller", M=64, N=128, K=64, act=0, n=need - 1)
+    refused(lib, LINEAR_BACKWARD, WORKSPACE, "smaller", M=64, N=128, K=64, act=2, n=need)
