@@ -103,3 +103,91 @@ def test_workspace_of_a_gradient_without_activation(lib):
     need = act(64, 128, 64, BF16, 0)
     refused(lib, LINEAR_BACKWARD, WORKSPACE, "smaller", M=64, N=128, K=64, act=0, n=need - 1)
     refused(lib, LINEAR_BACKWARD, WORKSPACE, "smaller", M=64, N=128, K=64, act=2, n=need)
+
+
+SIZES = {"linear": "M N K", "linear_backward": "M N K", "markov_loss": "N V d r", "markov_loss_backward": "N V d r",
+         "hidden_draft": "B gamma V r d"}
+# limits that are one too many
+LIMITS = {"linear": dict(M=1 << 20, N=1 << 24, K=1 << 16), "linear_backward": dict(M=1 << 20, N=1 << 24, K=1 << 16),
+          "markov_loss": dict(N=1 << 20, V=1 << 24, d=1 << 16, r=1 << 16),
+          "markov_loss_backward": dict(N=1 << 20, V=1 << 24, d=1 << 16, r=1 << 16),
+          "hidden_draft": dict(gamma=64, V=1 << 24, d=1 << 16)}
+
+
+@pytest.mark.parametrize("entry", ENTRIES, ids=lambda e: e.name)
+def test_sizes_types_and_limits(lib, entry):
+    for k in SIZES[entry.name].split():
+        refused(lib, entry, INVALID, "negative size", **{k: -1})
+    for dt in (-1, 2, 99):
+        refused(lib, entry, INVALID, "unknown dtype", dt=dt)
+    if "act" in entry.values:
+        for act in (-1, 4):
+            refused(lib, entry, INVALID, "unknown activation", act=act)
+    for k, most in LIMITS[entry.name].items():
+        refused(lib, entry, UNSUPPORTED, f"{k} >" if k not in "dr" or entry is HIDDEN_DRAFT else "d or r >", **{k: most + 1})
+    if entry is HIDDEN_DRAFT:
+        refused(lib, entry, INVALID, "sampling mode", mode=2)
+        refused(lib, entry, INVALID, "positive", V=0)
+        refused(lib, entry, UNSUPPORTED, "B * gamma", B=1 << 15, gamma=64)
+        refused(lib, entry, UNSUPPORTED, "supports r", r=48)
+    elif "V" in entry.values:
+        refused(lib, entry, INVALID, "V must be positive", V=0)
+
+
+# arrays that may be left out
+OPTIONAL = {"linear": "bias res pre", "linear_backward": "dx dw db", "markov_loss": "U",
+            "markov_loss_backward": "dU dh dWo dW1 dW2", "hidden_draft": "bias"}
+
+
+@pytest.mark.parametrize("entry", ENTRIES, ids=lambda e: e.name)
+def test_arrays_that_are_missing(lib, entry):
+    for k in entry.arrays:
+        if k in OPTIONAL[entry.name].split():
+            continue
+        if k == "ws":
+            refused(lib, entry, WORKSPACE, "workspace missing", ws=0)
+        elif k in ("Wo", "W2") and entry in (LOSS, LOSS_BACKWARD):
+            refused(lib, entry, INVALID, "go with d > 0", **{k: 0})
+        elif k == "U" and entry is LOSS_BACKWARD:
+            refused(lib, entry, INVALID, "gradient of an input that is not there", U=0)
+        elif k == "Wo" and entry is HIDDEN_DRAFT:
+            continue        # looked at after the draft's own checks, which end at the device
+        else:
+            refused(lib, entry, INVALID, "null pointer", **{k: 0})
+    if entry in (LOSS, LOSS_BACKWARD):
+        refused(lib, entry, INVALID, "go with d > 0", d=0)
+        refused(lib, entry, INVALID, "go with d > 0", r=0)
+        refused(lib, entry, INVALID, "no logits", U=0, d=0, h=0, Wo=0, r=0, prev=0, W1=0, W2=0)
+    if entry is LOSS_BACKWARD:
+        refused(lib, entry, INVALID, "gradient of an input", d=0, h=0, Wo=0)
+        refused(lib, entry, INVALID, "gradient of an input", r=0, prev=0, W1=0, W2=0)
+
+
+@pytest.mark.parametrize("entry", ENTRIES, ids=lambda e: e.name)
+def test_arrays_that_are_not_aligned(lib, entry):
+    """Operands of the products to 16 bytes, everything else to its element,
+    the workspace to 256 bytes."""
+    wide = {"linear": "x w", "linear_backward": "dy x w", "markov_loss": "h Wo W1 W2",
+            "markov_loss_backward": "h Wo W1 W2", "hidden_draft": "W1"}[entry.name].split()
+    narrow = {"linear": "bias res y pre", "linear_backward": "pre dx dw db", "markov_loss": "label prev U nll lse",
+              "markov_loss_backward": "label prev U g lse dU dh dWo dW1 dW2", "hidden_draft": "U"}[entry.name].split()
+    for k in wide:
+        refused(lib, entry, INVALID, "16-byte", **{k: entry.values[k] + 8})
+    for dt in (BF16, F32):
+        fp32 = dict(r=16) if entry is HIDDEN_DRAFT else {}
+        for k in narrow:
+            refused(lib, entry, INVALID, "misaligned", dt=dt, **fp32, **{k: entry.values[k] + 1})
+    for k in narrow:
+        if k in ("U", "bias", "res", "y", "dx", "dw", "db", "dU", "dh", "dWo", "dW1", "dW2"):
+            refused(lib, entry, INVALID, "misaligned", dt=F32, **(dict(r=16) if entry is HIDDEN_DRAFT else {}),
+                    **{k: entry.values[k] + 2})
+    refused(lib, entry, WORKSPACE, "256-byte", ws=entry.values["ws"] + 64)
+
+
+@pytest.mark.parametrize("entry", ENTRIES, ids=lambda e: e.name)
+def test_a_workspace_that_is_short(lib, entry):
+    size = [entry.values[k] for k in ("B gamma V r d dt" if entry is HIDDEN_DRAFT else "M N K dt" if "M" in entry.values
+                                      else "N V d r dt").split()]
+    need = getattr(lib, f"dspark_{entry.name}_workspace_bytes")(*size)
+    for n in (0, 255, need - 1):
+        refused(lib, entry, WORKSPACE, "smaller than", n=n)
