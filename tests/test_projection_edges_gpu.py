@@ -262,3 +262,106 @@ def test_hidden_draft_captured_and_replayed(B, gamma):
         assert all(torch.equal(a, b) for a, b in zip(eager, want[i]))
         for j, (_, _, outs) in enumerate(graphs):
             assert all(torch.equal(a, b) for a, b in zip(outs, want[(i + j) % 3]))
+
+
+def test_linear_of_the_most_rows_and_of_the_most_features():
+    """2^20 rows, and 2^24 features: values are small whole numbers, so every
+    sum is exact in both types, and every row and feature is looked at."""
+    for dtype in TYPES:
+        for M, N, K in ((1 << 20, 40, 24), (3, 1 << 24, 8), (70, 1 << 24, 8)):
+            x = (torch.arange(M * K, device=DEV) % 5 - 2).view(M, K)
+            w = (torch.arange(N * K, device=DEV) % 3 - 1).view(N, K)
+            dy = (torch.arange(M * N, device=DEV) % 7 == 0).view(M, N).to(dtype)
+            xt, wt = x.to(dtype), w.to(dtype)
+            y = linear(xt, wt)                       # |y| <= 48: exact in bf16
+            assert torch.equal(y, (xt.float() @ wt.float().t()).to(dtype)), (M, N, K)
+            del y
+            # sums of up to 2^20 whole numbers below 2^22: exact in fp32, rounded once
+            dx, dw, db = linear_backward(dy, xt, wt)
+            dyf = dy.float()
+            assert torch.equal(dx, (dyf @ wt.float()).to(dtype)), (M, N, K)
+            assert torch.equal(dw, (dyf.t().contiguous() @ xt.float()).to(dtype)), (M, N, K)
+            assert torch.equal(db, dyf.sum(0).to(dtype)), (M, N, K)
+            del x, w, dy, xt, wt, dx, dw, db, dyf
+            torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_loss_of_the_most_rows(dtype):
+    """2^20 rows, a third of them ignored, over a tiny vocabulary whose tokens
+    all occur often, against the definition in 64 bits.  With |z| < 8 and 16
+    tokens lse and nll are sums of few terms: 64 u of values below 16.  dz is
+    off by h and 64 u relative to g, dW1 sums about N / 16 rows of |dE| <= |g|
+    |W2| 16 in fp32 in four interleaved sums, 2 (N / 64 + 64) u in all; dW2 and
+    dWo sum N terms in fp32, 2 (N + 64) u of the sum of their sizes."""
+    N, V, d, r = 1 << 20, 16, 8, 8
+    h_, u = HALF[dtype], U32
+    label = torch.randint(-8, V, (N,), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV, dtype=torch.int32)
+    prev = torch.randint(0, V, (N,), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV, dtype=torch.int32)
+    s = dict(h=rand(3, N, d, sd=0.5, dtype=dtype).clamp(-1, 1), Wo=rand(4, V, d, sd=0.5, dtype=dtype).clamp(-1, 1) / 2,
+             prev=prev, W1=rand(5, V, r, sd=0.5, dtype=dtype).clamp(-1, 1) / 2,
+             W2=rand(6, r, V, sd=0.5, dtype=dtype).clamp(-1, 1))
+    g = torch.rand(N, generator=torch.Generator(device=DEV).manual_seed(7), device=DEV)
+    nll, lse = markov_loss(label, **s)
+    grads = markov_loss_backward(g, lse, label, **s)
+    torch.cuda.synchronize()
+    used = label >= 0
+    hd, Wo, W1, W2 = (s[k].double() for k in ("h", "Wo", "W1", "W2"))
+    E = W1[prev.long()]
+    z = hd @ Wo.t() + E @ W2
+    lse64 = torch.logsumexp(z, 1)
+    y = label.long().clamp(min=0)[:, None]
+    gu = torch.where(used, g.double(), 0.0)[:, None]
+    dz = gu * (torch.softmax(z, 1) - torch.zeros_like(z).scatter_(1, y, 1.0))
+    zero = torch.zeros_like(lse64)
+    assert ((lse.double() - torch.where(used, lse64, zero)).abs() <= 64 * u * 16).all()
+    assert ((nll.double() - torch.where(used, lse64 - z.gather(1, y)[:, 0], zero)).abs() <= 64 * u * 16).all()
+    er = h_ * dz.abs() + 64 * u * gu
+    E0 = torch.where(used[:, None], E, 0.0)
+    put = lambda t: torch.zeros(V, r, dtype=torch.float64, device=DEV).index_add_(0, prev.long(), t)  # noqa: E731
+    terms = 2 * (N + 64) * u
+    for k, want, size, err, t in (
+            ("dh", dz @ Wo, dz.abs() @ Wo.abs(), er @ Wo.abs(), 2 * (V + 8) * u),
+            ("dWo", dz.t() @ hd, dz.abs().t() @ hd.abs(), er.t() @ hd.abs(), terms),
+            ("dW2", E0.t() @ dz, E0.abs().t() @ dz.abs(), E0.abs().t() @ er, terms),
+            ("dW1", put(dz @ W2.t()), put(dz.abs() @ W2.abs().t()), put(er @ W2.abs().t()), terms)):
+        tol = err + t * size
+        off = (grads[k].double() - want).abs()
+        assert (off <= tol + h_ * (want.abs() + tol)).all(), k
+
+
+def test_loss_of_the_largest_vocabulary():
+    """2^24 tokens: logits that are small whole numbers, so lse is known in
+    closed form, and each row's label and gradient at both ends of the
+    vocabulary."""
+    N, V, r = 5, 1 << 24, 8
+    W1 = torch.zeros(V, r, dtype=torch.bfloat16, device=DEV)
+    W2 = torch.zeros(r, V, dtype=torch.bfloat16, device=DEV)
+    prev = torch.tensor([0, 1, V - 1, V - 2, 77], dtype=torch.int32, device=DEV)
+    label = torch.tensor([0, V - 1, V - 1, 5, V // 2], dtype=torch.int32, device=DEV)
+    W1[prev.long(), 0] = torch.arange(1, 6, dtype=torch.bfloat16, device=DEV)
+    W2[0, label.long()] = 4
+    nll, lse = markov_loss(label, prev=prev, W1=W1, W2=W2)
+    z = 4.0 * torch.arange(1, 6, dtype=torch.float64, device=DEV)
+    hot = torch.unique(label).numel()                       # tokens whose logit is z, the others' is 0
+    want = torch.log(hot * torch.exp(z) + (V - hot))
+    # V equal terms summed in fp32 over lanes, tiles and threads: below 600 additions deep
+    assert ((lse.double() - want).abs() <= 700 * U32 + 2 * U32 * want).all()
+    assert ((nll.double() - (want - z)).abs() <= 700 * U32 + 4 * U32 * want).all()
+    g = torch.ones(N, device=DEV)
+    grads = markov_loss_backward(g, lse, label, prev=prev, W1=W1, W2=W2)
+    p = torch.exp(z - want)
+    # dW2[0, v] = sum_n W1[prev_n, 0] dz_n(v)
+    e = torch.arange(1, 6, dtype=torch.float64, device=DEV)
+    for n in range(N):
+        v = int(label[n])
+        ref = float((e * (p - (label == v).double())).sum())
+        assert abs(float(grads["dW2"][0, v]) - ref) <= 3 * 2.0 ** -8 * float((e * (p + 1)).sum())
+    cold = float((e * torch.exp(-want)).sum())
+    assert abs(float(grads["dW2"][0, 3]) - cold) <= 3 * 2.0 ** -8 * cold
+    # dW1[prev_n, 0] = 4 (sum over the hot tokens of p - 1); no other token has a gradient
+    for n in range(N):
+        ref = 4 * float(hot * p[n] - 1)
+        assert abs(float(grads["dW1"][int(prev[n]), 0]) - ref) <= 3 * 2.0 ** -8 * 4 * float(hot * p[n] + 1)
+    grads["dW1"][prev.long()] = 0
+    assert not grads["dW1"].any() and not grads["dW2"][1:].any()
