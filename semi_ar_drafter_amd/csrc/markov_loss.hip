@@ -367,7 +367,13 @@ Layout layout(int N, int V, int d, int r, bool bf16, bool backward) {
     L.W2 = take(size_t(r) * L.w2_ld * 2);
   }
   L.wo_ld = d;
-  if (bf16 && d % 8 && d >= 512 && size_t(V) * L.dp * 2 <= kCopyBytes) {
+  // The copy reads and writes what the product reads once more: worth it where
+  // that product has few tiles, each with many steps, or many rows (forward /
+  // with all gradients, us, copied against not: 24 rows, V = 1088, d = 3535 40
+  // against 60 / 72 against 90; 1024 rows, V = 50021, d = 601 126 against 133 /
+  // 424 against 444; but 24 rows, V = 50021, d = 601 45 against 29 / 134 against
+  // 124, and 333 rows 72 against 66 / 244 against 234).
+  if (bf16 && d % 8 && d >= 256 && (V <= 8192 || N > 512) && size_t(V) * L.dp * 2 <= kCopyBytes) {
     L.wo_ld = L.dp;
     L.Wo = take(size_t(V) * L.dp * 2);
   }
