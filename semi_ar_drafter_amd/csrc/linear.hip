@@ -243,7 +243,10 @@ hipError_t linear_bf16(const LinearArgs& a, hipStream_t stream) {
   if (few_rows(a.M, a.N, a.K)) {
     const bf16_t *x = static_cast<const bf16_t*>(a.x), *w = static_cast<const bf16_t*>(a.w);
     const dim3 grid(unsigned((a.N + 15) / 16));
-    // more waves share the contraction where there are too few workgroups to fill the compute units
+    // more waves share the contraction where there are too few workgroups to
+    // fill the compute units (one row, 8 waves against 4, us: 4096 x 4096 7.4
+    // against 8.0, 8192 x 4096 13.2 against 14.5, 16384 x 4096 23.2 both,
+    // 151936 x 512 26.0 against 24.4)
     if (a.N <= 16 * 2 * kComputeUnits)
       hipLaunchKernelGGL((few_rows_kernel<8>), grid, dim3(512), 0, stream, a.M, a.N, a.K, x, w, linear_epi<bf16_t>(a));
     else

@@ -522,7 +522,8 @@ hipError_t loss_t(const LossArgs& a, hipStream_t stream) {
                                          plan_for(a.V, a.N, a.d + a.r, L.any, a.d == 0, false), stream)) != hipSuccess)
     return e;
   // few rows: all threads of a workgroup on one row's tiles; many: neighbours
-  // in a wave read neighbouring rows
+  // in a wave read neighbouring rows (whole call, V = 151936, rank 16, us: 256
+  // rows 36 against 39, 512 rows 62 against 61, 2048 rows 209 against 186)
   const int tiles = (a.V + bm - 1) / bm;
   if (a.N <= 512)
     hipLaunchKernelGGL((join_kernel<256>), dim3(unsigned(a.N)), dim3(256), 0, stream, a.N, tiles, p.place, stat,
@@ -603,7 +604,10 @@ hipError_t loss_backward_t(const LossArgs& a, hipStream_t stream) {
   }
   if (a.N == 0) return hipSuccess;
   const unsigned rows = unsigned(a.N);
-  // split sums are many values for few rows: a launch of their own, spread over the columns
+  // split sums are many values for few rows: a launch of their own, spread over
+  // the columns below 1024 rows (whole call for dh and dW1, V = 30000, d = 2560,
+  // spread against not, us: 128 rows 110 against 117, 512 220 against 231, 1024
+  // 379 against 376, 4096 1351 against 1331)
   const bool join_e = dW1 && L.e.splits > 1, join_h = dh && (!dW1 || join_e || L.h.splits > 1);
   const unsigned wide = unsigned(((a.d > a.r ? a.d : a.r) + 255) / 256);
   if (join_e || join_h)

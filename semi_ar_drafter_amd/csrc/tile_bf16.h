@@ -589,7 +589,12 @@ using Tile16 = TileShape<128, 16, 4, 1, 4>;
 using Tile32 = TileShape<128, 32, 4, 1, 3>;
 using Tile64 = TileShape<128, 64, 2, 2, 3>;
 using Tile128 = TileShape<128, 128, 2, 2, 2>;
-using Tile128Deep = TileShape<128, 128, 2, 2, 4>;   // one workgroup per compute unit: two steps more in flight
+// Where there is at most one workgroup per compute unit anyhow: two steps more
+// in flight.  It pays where nearly all units have one and the contraction is
+// long (loss of 100 rows, V = 30000, d = 2048: 37.3 us against 42.4), and costs
+// a few per cent otherwise (1000 rows, V = 4000, d = 2048: 41.8 against 39.9;
+// 250 rows, V = 8192, d = 512: 18.4 against 18.1).
+using Tile128Deep = TileShape<128, 128, 2, 2, 4>;
 using Tile16Any = TileShape<128, 16, 4, 1, 2>;
 using Tile32Any = TileShape<128, 32, 4, 1, 2>;
 using Tile64Any = TileShape<128, 64, 2, 2, 2>;

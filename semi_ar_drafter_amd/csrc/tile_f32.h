@@ -157,14 +157,19 @@ using WideF32 = TileF32<128, 128, 2, 2>;
 using MidF32 = TileF32<64, 64, 2, 2>;
 using SlimF32 = TileF32<64, 16, 4, 1>;
 
-// 0: few rows; 1: too few wide tiles for the compute units; 2: wide.
+// 0: few rows; 1: too few wide tiles for the compute units; 2: wide.  With a
+// contraction of 1024, wide against narrow, us: 128 tiles 63 against 67, 192
+// 101 against 86 (its splits leave a quarter of the last round empty), 256 105
+// against 109, 512 (2048 long) 348 against 404, 1024 351 against 400.
 inline int f32_choice(int na, int nb) {
   if (nb <= 16) return 0;
   const long wide = long((na + 127) / 128) * ((nb + 127) / 128);
   return wide >= 192 ? 2 : 1;
 }
 // Splits of a contraction into fp32 sums, for about two workgroups per
-// compute unit, each with at least two steps.
+// compute unit, each with at least two steps (for one, two and four, us: 256 x
+// 1024 x 2048 30.6, 24.9 and 25.5; 128 x 4096 x 2560 62, 47 and 44.5; 8 x 4096
+// x 1024 13.1, 9.9 and 10.1).
 inline int f32_splits(int na, int nb, long K) {
   const int c = f32_choice(na, nb), bm = c == 2 ? 128 : 64, bn = c == 2 ? 128 : c == 1 ? 64 : 16;
   const long tiles = long((na + bm - 1) / bm) * ((nb + bn - 1) / bn), steps = (K + kStepF32 - 1) / kStepF32;
