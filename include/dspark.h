@@ -567,7 +567,8 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
 
 /*
  * dspark_linear_backward — gradients of dspark_linear:
- *   dz = dy act'(z)   (rounded to the storage type for the two products)
+ *   dz = dy act'(z)   (rounded to the storage type for the two products; fp32
+ *                      storage for callers to whom half a bf16 step matters)
  *   dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz
  * each summed in fp32 and rounded once; the residual's gradient is dy itself.
  * relu's slope at 0 is 0, at NaN it is NaN.
@@ -637,8 +638,10 @@ size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dty
  *   dU = dz,  dh = dz Wo,  dWo = dz^T h,  dW2 = sum_n W1[prev[n]] (x) dz_n,
  *   dW1[t] = sum over the rows n with prev[n] = t of W2 dz_n
  * The logits are computed again, piece by piece of the vocabulary; dz is
- * rounded to the storage type for the products, sums are fp32, each gradient
- * is rounded once.  Ignored rows have no part in any sum; their rows of dU
+ * rounded to the storage type for the products (fp32 storage for callers to
+ * whom half a bf16 step of it matters), sums are fp32, each gradient is
+ * rounded once.  A piece's dz, at most 512 MB, is the largest part of the
+ * workspace: up to about 1700 rows of 151936 tokens in bf16 it is all of them.  Ignored rows have no part in any sum; their rows of dU
  * and dh are zero.
  *
  * Arguments: inputs as dspark_markov_loss, and
