@@ -576,8 +576,9 @@ size_t dspark_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
  * Arguments: sizes, types and layouts as dspark_linear, and
  *   dy   [M][N]      16-byte aligned
  *   pre  fp32 [M][N] z as dspark_linear wrote it (NULL without activation)
- *   dx [M][K], dw [N][K], dbias [N] out; each may be NULL: not computed.
- *                 With M == 0, dw and dbias are zero; with N == 0, dx is.
+ *   dx [M][K], dw [N][K], dbias [N] out; each may be NULL: not computed
+ *                 (all three: nothing is enqueued).  With M == 0, dw and
+ *                 dbias are zero; with N == 0, dx is.
  *   workspace     >= dspark_linear_backward_act_workspace_bytes(M, N, K, dtype,
  *                 act) bytes, 256-byte aligned, any contents.
  * Outputs or a workspace that overlap another array are refused.
@@ -648,7 +649,8 @@ size_t dspark_markov_loss_workspace_bytes(int N, int V, int d, int r, dspark_dty
  *   g    fp32 [N]  gradient of the loss by nll (position weights, 1 / count)
  *   lse  fp32 [N]  as dspark_markov_loss wrote it
  *   dU [N][V], dh [N][d], dWo [V][d], dW1 [V][r], dW2 [r][V] out, in the
- *                 storage type; each may be NULL: not computed
+ *                 storage type; each may be NULL: not computed (all five:
+ *                 nothing is enqueued)
  *   workspace     >= dspark_markov_loss_backward_workspace_bytes(N, V, d, r, dtype)
  *                 bytes, 256-byte aligned, any contents
  * N == 0 leaves dWo, dW1 and dW2 zero.  Outputs or a workspace that overlap

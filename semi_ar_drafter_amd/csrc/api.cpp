@@ -541,6 +541,7 @@ dspark_status dspark_linear_backward(int M, int N, int K, dspark_dtype dtype, co
   if (any_overlap({{dx, m * k * elem}, {dw, n * k * elem}, {dbias, n * elem}, {workspace, need}},
                   {{dy, m * n * elem}, {x, m * k * elem}, {w, n * k * elem}, {pre, m * n * 4}}))
     return overlap_refused();
+  if (!dx && !dw && !dbias) return DSPARK_OK;
   dspark::LinearBackwardArgs a;
   a.M = M;
   a.N = N;
@@ -678,6 +679,7 @@ dspark_status dspark_markov_loss_backward(int N, int V, int d, int r, dspark_dty
   const std::initializer_list<Span> out = {
       {dU, n * V}, {dh, n * d}, {dWo, v * d}, {dW1, v * r}, {dW2, v * r}, {workspace, need}};
   if (overlaps_loss(out, a) || any_overlap(out, {{g, rows}, {lse, rows}})) return overlap_refused();
+  if (!dU && !dh && !dWo && !dW1 && !dW2) return DSPARK_OK;
   a.lse_in = lse;
   a.g = g;
   a.dU = dU;

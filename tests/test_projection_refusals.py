@@ -191,3 +191,12 @@ def test_a_workspace_that_is_short(lib, entry):
     need = getattr(lib, f"dspark_{entry.name}_workspace_bytes")(*size)
     for n in (0, 255, need - 1):
         refused(lib, entry, WORKSPACE, "smaller than", n=n)
+
+
+def test_no_gradient_asked_for_enqueues_nothing(lib):
+    """Here, where there is no device, a launch would be an error."""
+    assert LINEAR_BACKWARD(lib, dx=0, dw=0, db=0) == OK
+    assert LOSS_BACKWARD(lib, dU=0, dh=0, dWo=0, dW1=0, dW2=0) == OK
+    # the checks are made all the same
+    refused(lib, LINEAR_BACKWARD, WORKSPACE, "missing", dx=0, dw=0, db=0, ws=0)
+    refused(lib, LOSS_BACKWARD, INVALID, "null pointer", dU=0, dh=0, dWo=0, dW1=0, dW2=0, g=0)
