@@ -592,6 +592,12 @@ def _storage(t, name):
     return DSPARK_F32
 
 
+def _fits(*sizes):
+    """The C ABI takes sizes as int, which ctypes would cut to 32 bits."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise DSparkError(DSPARK_ERR_UNSUPPORTED, "a size over 2^31 - 1")
+
+
 def _act(act):
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
@@ -695,6 +701,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     _optional(pre, "pre", torch.float32, (M, N), dev)
     _optional(out, "out", x.dtype, (M, N), dev)
     a = _act(act)
+    _fits(M, N, K)
     _no_graph("linear", x, w, bias, residual)
     with _on(dev), _launching:
         y = out if out is not None else x.new_empty((M, N))
@@ -722,6 +729,7 @@ def linear_backward(dy, x, w, act: str = "none", pre=None, need=("dx", "dw", "db
     _optional(pre, "pre", torch.float32, (M, N), dev)
     if set(need) - {"dx", "dw", "dbias"}:
         raise ValueError("need names dx, dw and dbias")
+    _fits(M, N, K)
     _no_graph("linear_backward", dy, x, w, pre)
     with _on(dev), _launching:
         new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
@@ -754,6 +762,7 @@ def _loss_inputs(label, U, h, Wo, prev, W1, W2):
     _optional(prev, "prev", torch.int32, (N,), dev)
     _optional(W1, "W1", first.dtype, (V, r), dev)
     _optional(W2, "W2", first.dtype, (r, V), dev)
+    _fits(N, V, d, r)
     return N, V, d, r, dt, dev
 
 
@@ -837,6 +846,7 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
     _need(conf_w, "conf_w", torch.float32, (d + r,), dev)
     _need(sts_T, "sts_T", torch.float32, (gamma,), dev)
     _optional(U, "U", h.dtype, (B, gamma, V), dev)
+    _fits(B, gamma, V, r, d)
     with _on(dev), _launching:
         if U is None:
             U = torch.empty((B, gamma, V), dtype=h.dtype, device=dev)

@@ -152,6 +152,22 @@ def test_row_gradient_of_very_many_features():
     assert torch.equal(dx.float(), (64.0 * row)[:, None].expand(M, K))
 
 
+def test_sizes_that_an_int_does_not_hold_are_refused():
+    """More than 2^31 - 1 rows or tokens (of nothing, which takes no memory):
+    refused, not cut to 32 bits."""
+    none = lambda *sh, dtype=torch.bfloat16: torch.empty(sh, dtype=dtype, device=DEV)  # noqa: E731
+    ints, floats = none(1, dtype=torch.int32), none(0, dtype=torch.float32)
+    for M in (1 << 31, (1 << 32) + 4):
+        for call in (lambda: linear(none(M, 0), none(0, 0)), lambda: linear(none(0, 0), none(M, 0)),
+                     lambda: linear_backward(none(M, 0), none(M, 0), none(0, 0)),
+                     lambda: markov_loss(ints[:0], U=none(0, M)),
+                     lambda: markov_loss_backward(floats, floats, ints[:0], U=none(0, M)),
+                     lambda: hidden_draft(ints, none(1, 1, 0), none(M, 0), none(M, 0), none(0, M), floats, 0.0,
+                                          torch.ones(1, device=DEV))):
+            with pytest.raises(binding.DSparkError, match="over 2"):
+                call()
+
+
 # ---------------------------------------------------------------------------
 # workspaces
 # ---------------------------------------------------------------------------
