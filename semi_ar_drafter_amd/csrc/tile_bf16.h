@@ -613,10 +613,17 @@ static __global__ __launch_bounds__(256) void pad_rows_kernel(long rows, long n,
   const u32x4_t v = load_any(s + c, s + (c < n ? n : c));
   *reinterpret_cast<u32x4_t*>(dst + at * 8) = v;
 }
+// At most 2^31 threads a launch, where a grid holds less than 2^32.
 inline hipError_t pad_rows(long rows, long n, long ld, const bf16_t* src, bf16_t* dst, hipStream_t stream) {
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned((rows * (ld / 8) + 255) / 256)), dim3(256), 0, stream, rows, n, ld,
-                     src, dst);
-  return hipGetLastError();
+  const long most = (1l << 31) / (ld / 8);
+  for (long r0 = 0; r0 < rows; r0 += most) {
+    const long some = rows - r0 < most ? rows - r0 : most;
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned((some * (ld / 8) + 255) / 256)), dim3(256), 0, stream, some, n, ld,
+                       src + r0 * n, dst + r0 * ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 // Weights whose rows are not 16-byte aligned are copied up to this size, where
 // their product is long: the copy takes a few microseconds, and direct loads

@@ -346,6 +346,24 @@ def test_loss_of_the_most_rows(dtype):
         assert (off <= tol + h_ * (want.abs() + tol)).all(), k
 
 
+def test_linear_of_unaligned_rows_that_are_very_many_values():
+    """2^20 rows of 32771 values: their aligned copy is more 16-byte pieces
+    than one launch has threads.  Two features in two places of each row: y is
+    the sum of x there, whole numbers below 16, exact."""
+    M, K = 1 << 20, 32771
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GB of free device memory")
+    x, w = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV), torch.zeros(2, K, dtype=torch.bfloat16, device=DEV)
+    at = torch.arange(M, device=DEV)
+    x[:, 0], x[:, K - 1] = (at % 5).to(torch.bfloat16), (at % 7).to(torch.bfloat16)
+    w[0, 0], w[0, K - 1], w[1, K - 1] = 1, 1, -1
+    y = linear(x, w, workspace=torch.empty(binding.load().dspark_linear_workspace_bytes(M, 2, K, 1), dtype=torch.uint8,
+                                           device=DEV)).float()
+    assert torch.equal(y[:, 0], (at % 5 + at % 7).float()) and torch.equal(y[:, 1], -(at % 7).float())
+    del x, y
+    torch.cuda.empty_cache()
+
+
 def test_loss_of_the_largest_vocabulary():
     """2^24 tokens: logits that are small whole numbers, so lse is known in
     closed form, and each row's label and gradient at both ends of the
