@@ -623,8 +623,9 @@ size_t dspark_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype 
  *                 bytes, 256-byte aligned, any contents.  Calls that can
  *                 overlap need separate ones.
  * Outputs or a workspace that overlap another array are refused.
- * Limits: N <= 2^20, V <= 2^24, d, r <= 65536.  Nothing depends on execution
- * order: the same inputs give the same bits.
+ * Limits: N <= 2^20, V <= 2^24, d, r <= 65536, and N * V < 2^38 (both rounded
+ * up to 128), which the gradient, made piece by piece, does not need.  Nothing
+ * depends on execution order: the same inputs give the same bits.
  */
 dspark_status dspark_markov_loss(
     int N, int V, int d, int r, dspark_dtype dtype, const int32_t* label, const void* U,

@@ -638,6 +638,9 @@ dspark_status dspark_markov_loss(int N, int V, int d, int r, dspark_dtype dtype,
   if (st != DSPARK_OK) return st;
   if (N == 0) return DSPARK_OK;
   if (!nll || !lse) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  // 256 threads for each 128 x 128 logits (the least that so many rows take): a launch holds less than 2^32
+  if ((long long)((V + 127) / 128) * ((N + 127) / 128) >= 1ll << 24)
+    return fail(DSPARK_ERR_UNSUPPORTED, "N * V (both rounded up to 128) >= 2^38");
   if (misaligned(nll, 4) || misaligned(lse, 4)) return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
   const size_t need = dspark_markov_loss_workspace_bytes(N, V, d, r, dtype);
   st = check_workspace(workspace, workspace_bytes, need, "dspark_markov_loss_workspace_bytes");

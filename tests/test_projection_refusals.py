@@ -200,3 +200,15 @@ def test_no_gradient_asked_for_enqueues_nothing(lib):
     # the checks are made all the same
     refused(lib, LINEAR_BACKWARD, WORKSPACE, "missing", dx=0, dw=0, db=0, ws=0)
     refused(lib, LOSS_BACKWARD, INVALID, "null pointer", dU=0, dh=0, dWo=0, dW1=0, dW2=0, g=0)
+
+
+def test_more_logits_than_a_launch_holds_are_refused(lib):
+    far = {a: (1 << 50) + (i << 44) for i, a in enumerate(LOSS.arrays)}
+    for N, V in ((1 << 20, 1 << 18), (1 << 14, 1 << 24), ((1 << 20) - 127, (1 << 18) - 127), (1 << 20, 1 << 24)):
+        refused(lib, LOSS, UNSUPPORTED, "N * V", N=N, V=V, **far)
+    # one tile fewer is past this check
+    refused(lib, LOSS, WORKSPACE, "smaller", N=1 << 20, V=(1 << 18) - 128, **far)
+    refused(lib, LOSS, WORKSPACE, "smaller", N=1 << 20, V=151936, **far)
+    # the gradient goes piece by piece
+    far = {a: (1 << 50) + (i << 44) for i, a in enumerate(LOSS_BACKWARD.arrays)}
+    refused(lib, LOSS_BACKWARD, WORKSPACE, "smaller", N=1 << 20, V=1 << 18, **far)
