@@ -9,8 +9,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from semi_ar_drafter_amd import (binding, hidden_draft, linear, linear_backward, markov_loss,  # noqa: E402
-                                 markov_loss_backward)
+from semi_ar_drafter_amd import (binding, hidden_draft, linear, linear_backward, markov_draft,  # noqa: E402
+                                 markov_loss, markov_loss_backward)
 
 DEV = "cuda:0"
 U32 = 2.0 ** -24
@@ -186,6 +186,84 @@ def test_gradient_workspace_of_the_stated_size_is_enough(dtype):
         assert (room[:off] == 91).all() and (room[off + n:] == 91).all()
         more = torch.empty(n + (64 << 20), dtype=torch.uint8, device=DEV)
         assert all(torch.equal(a, b) for a, b in zip(got, linear_backward(dy, x, w, workspace=more)))
+
+
+# ---------------------------------------------------------------------------
+# as a program uses them
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 64), (3, 40, 64), (16, 300, 129), (77, 1027, 1001), (300, 512, 4096)])
+def test_residual_in_place_is_the_residual(M, N, K, dtype):
+    """Added in place by every kernel (few rows, tiles, joined splits): the same
+    bits as into another array."""
+    x, w, b, res = rand(1, M, K, dtype=dtype), rand(2, N, K, sd=0.1, dtype=dtype), rand(3, N, dtype=dtype), rand(4, M, N, dtype=dtype)
+    for act in ("none", "silu"):
+        want = linear(x, w, bias=b, act=act, residual=res)
+        y = res.clone()
+        linear(x, w, bias=b, act=act, residual=y, out=y)
+        assert torch.equal(y, want)
+
+
+def test_two_graphs_replayed_at_once():
+    """Graphs of the same calls on two streams, replayed together and beside
+    eager calls: each has memory of its own."""
+    sets = []
+    for i in range(3):
+        N, V, d, r = 100 + 30 * i, 3001, 72, 24
+        s = dict(h=rand(10 * i, N, d, dtype=torch.bfloat16), Wo=rand(10 * i + 1, V, d, sd=0.2, dtype=torch.bfloat16),
+                 prev=torch.arange(N, device=DEV, dtype=torch.int32) % 50,
+                 W1=rand(10 * i + 2, V, r, sd=0.5, dtype=torch.bfloat16), W2=rand(10 * i + 3, r, V, sd=0.5, dtype=torch.bfloat16))
+        label = (torch.arange(N, device=DEV, dtype=torch.int32) * 29) % (V + 200)
+        x, w = rand(10 * i + 4, 77, 1001, dtype=torch.bfloat16), rand(10 * i + 5, 1027, 1001, sd=0.1, dtype=torch.bfloat16)
+        sets.append((s, label, torch.ones(N, device=DEV) / N, x, w))
+
+    def work(s, label, g, x, w):
+        nll, lse = markov_loss(label, **s)
+        return [nll, lse, *markov_loss_backward(g, lse, label, **s).values(), linear(x, w, act="gelu")]
+
+    want = [[t.clone() for t in work(*a)] for a in sets]
+    graphs = []
+    for a in sets[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = work(*a)
+        graphs.append((graph, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for graph, outs, stream in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = work(*sets[2])
+        torch.cuda.synchronize()
+        for got, ref in ((eager, want[2]), (graphs[0][1], want[0]), (graphs[1][1], want[1])):
+            assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_base_logits_aligned_to_their_element_only(dtype):
+    """U at an odd element of a larger array, with rows that would keep
+    four-value alignment: the same bits as at an aligned address."""
+    N, V = 70, 2000
+    U, label, g = rand(1, N, V, dtype=dtype), torch.arange(N, device=DEV, dtype=torch.int32) * 17, torch.ones(N, device=DEV)
+    label[5] = -1
+    moved = torch.empty(N * V + 1, dtype=dtype, device=DEV)[1:].view(N, V)
+    moved.copy_(U)
+    out = [(a, b, markov_loss_backward(g, b, label, U=t)["dU"]) for t in (U, moved) for a, b in [markov_loss(label, U=t)]]
+    assert all(torch.equal(p, q) for p, q in zip(*out)) and not out[0][2][5].any()
+
+
+def test_many_rows_all_ignored():
+    """No row has a label, above and below the number of rows that one launch
+    counts for itself."""
+    for N in (50, 9001):
+        s = dict(h=rand(1, N, 24), Wo=rand(2, 300, 24), prev=torch.zeros(N, dtype=torch.int32, device=DEV),
+                 W1=rand(3, 300, 8), W2=rand(4, 8, 300), U=rand(5, N, 300))
+        s["h"].fill_(math.nan)
+        label = torch.full((N,), 300, dtype=torch.int32, device=DEV)
+        nll, lse = markov_loss(label, **s)
+        grads = markov_loss_backward(torch.full((N,), math.nan, device=DEV), lse, label, **s)
+        assert not nll.any() and not lse.any() and len(grads) == 5
+        assert not any(t.any() for t in grads.values())
 
 
 # ---------------------------------------------------------------------------
@@ -399,3 +477,26 @@ def test_loss_of_the_largest_vocabulary():
         assert abs(float(grads["dW1"][int(prev[n]), 0]) - ref) <= 3 * 2.0 ** -8 * 4 * float(hot * p[n] + 1)
     grads["dW1"][prev.long()] = 0
     assert not grads["dW1"].any() and not grads["dW2"][1:].any()
+
+
+@pytest.mark.parametrize("mode", ["greedy", "gumbel"])
+@pytest.mark.parametrize("dtype,r", [(torch.bfloat16, 64), (torch.float32, 32)], ids=IDS)
+def test_hidden_draft_on_another_stream(dtype, r, mode):
+    """Both samplings on a stream of their own, shapes in turn on one
+    workspace: what linear and markov_draft give."""
+    stream = torch.cuda.Stream()
+    cases = [hidden_inputs(B, gamma, V, d, r, dtype, seed=B) for B, gamma, V, d in
+             ((1, 1, 40, 8), (5, 3, 1203, 33), (20, 4, 3000, 64), (5, 3, 700, 16))]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        got = []
+        with torch.cuda.stream(stream):
+            for a in cases:
+                got.append(hidden_draft(*a, mode=mode, seed=99))
+        torch.cuda.synchronize()
+        for a, out in zip(cases, got):
+            anchor, h, Wo, W1, W2, cw, cb, T = a
+            U = linear(h.view(-1, h.shape[2]), Wo).view(h.shape[0], h.shape[1], -1)
+            want = markov_draft(anchor, U, h, W1, W2, cw, cb, T, mode=mode, seed=99)
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(out, want)) and (out[0] >= 0).all()
