@@ -677,6 +677,9 @@ size_t dspark_markov_loss_backward_workspace_bytes(int N, int V, int d, int r, d
  *              bytes, 256-byte aligned: the drafting workspace, with its
  *              zero-fill rule, then the projection's.
  * Outputs (U among them) or a workspace that overlap another array are refused.
+ * Captured into a graph, its replays must not run beside other drafting calls:
+ * whether a replay is launched cooperatively, as dspark_markov_draft needs it
+ * there, is the runtime's choice.
  * Limits: those of both, and B * gamma <= 2^20.
  */
 dspark_status dspark_hidden_draft(

@@ -829,7 +829,8 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
     """markov_draft() from the hidden states alone: the base logits
     U = h @ Wo.T + bias are made first, in one call.  h [B, gamma, d],
     Wo [V, d], bias [V]; `U` [B, gamma, V] receives the base logits.  Other
-    arguments and the result as markov_draft."""
+    arguments and the result as markov_draft.  Replays of a graph that holds
+    the call must not run beside other drafting."""
     torch = _torch()
     lib = load()
     if mode not in ("greedy", "gumbel"):

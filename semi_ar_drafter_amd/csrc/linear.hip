@@ -10,9 +10,10 @@
 // dz is dy and nothing is rounded.
 //
 // Bound by reading w with few rows (8 rows, 151936 x 2560: 134 us, 5.8 TB/s), by
-// the matrix unit with many (1024 rows, 151936 x 4096: 1.04 ms, 1.22 PFLOP/s;
-// 4096 x 5120 x 5120 with its gradients: 267 + 271 + 247 us, dz_kernel 38 us
-// for 168 MB).
+// the main loop of the matrix unit's tiles with many (1024 rows, 151936 x 4096:
+// 1.07 ms, 1.19 PFLOP/s; 4096 x 5120 x 5120 with its gradients: 242 + 246 + 212
+// us, whose last rounds of tiles fill a part of the compute units, dz_kernel 37
+// us for 168 MB).
 #include "launch.h"
 #include "projection.h"
 #include "tile_bf16.h"

@@ -17,13 +17,13 @@
 //   dX += dz [Wo | W2^T]     (fp32, over the pieces in order)
 //   dWo = dz^T h,  dW2 = e^T dz    (final: rows are not split)
 // and at the end dX is rounded into dh and summed into dW1, rows with the
-// same previous token in row order.  Nothing is added by atomics: results do
-// not depend on any order of execution.
+// same previous token in four interleaved sums, each in row order.  Nothing is
+// added by atomics: results do not depend on any order of execution.
 //
 // Bound by: the matrix unit with many rows (4096 rows, V = 151936, d = 5120, r
-// = 256: four products of 5.1 to 5.4 ms, 1.2 PFLOP/s), reading Wo and W2 with
-// few (8 rows, d = 2560: 145 us, 5.9 TB/s), the tiles' ends where the
-// contraction is short (rank 256 alone: 800 us for the statistics of 4096 rows,
+// = 256: four products of 4.9 to 5.4 ms, 1.2 PFLOP/s), reading Wo and W2 with
+// few (8 rows, d = 2560: 143 us, 6.0 TB/s), the tiles' ends where the
+// contraction is short (rank 256 alone: 770 us for the statistics of 4096 rows,
 // of which four steps' MFMAs are 150).
 #include "launch.h"
 #include "projection.h"
