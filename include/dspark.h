@@ -60,6 +60,11 @@ typedef enum {
   DSPARK_ACT_GELU = 2,  /* z Phi(z), Phi the standard normal's integral */
   DSPARK_ACT_SILU = 3   /* z / (1 + exp(-z))                            */
 } dspark_activation;
+/* Normalisation of dspark_norm. */
+typedef enum {
+  DSPARK_NORM_LAYER = 0,  /* mean and variance of the row */
+  DSPARK_NORM_RMS = 1     /* its mean square              */
+} dspark_norm_kind;
 /* Verify-length policy of dspark_serve. */
 typedef enum {
   DSPARK_POLICY_GLOBAL = 0,           /* dspark_schedule on the iteration's own survivals */
@@ -690,6 +695,65 @@ dspark_status dspark_hidden_draft(
     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t dspark_hidden_draft_workspace_bytes(int B, int gamma, int V, int r, int d, dspark_dtype dtype);
+
+/*
+ * dspark_norm — normalisation of rows, with the residual stream's sum in the
+ * same pass: what stands before each projection of a backbone's layer.
+ *
+ * Defined by: [P-blog] §4 parallel stage (the backbone whose hidden states
+ * the heads read); the formula, for every row:
+ *   s    = x + residual                     (rounded to the storage type; s = x without one)
+ *   mu   = mean_c s          (LAYER; RMS: 0)
+ *   rstd = 1 / sqrt(mean_c (s - mu)^2 + eps)
+ *   y    = (s - mu) rstd weight + bias      (fp32, rounded once)
+ *
+ * Arguments
+ *   M, C          rows, channels (M == 0 or C == 0: no-op)
+ *   dtype         storage of x, residual, weight, bias, sum, y
+ *   x         [M][C]
+ *   residual  [M][C] or NULL
+ *   weight    [C]    or NULL (1),  bias [C] or NULL (0)
+ *   eps           >= 0 and finite
+ *   sum       [M][C] out: s (with a residual, else NULL); may be x or
+ *                 residual itself
+ *   y         [M][C] out
+ *   stat fp32 [M][2] out, or NULL: (mu, rstd), which dspark_norm_backward takes
+ * All arrays need element alignment only (stat 8 bytes).  Outputs that overlap
+ * another array are refused, but for sum == x and sum == residual.  Results do
+ * not depend on execution order.  Limits: M <= 2^20, C <= 32768.
+ */
+dspark_status dspark_norm(
+    int M, int C, dspark_dtype dtype, dspark_norm_kind kind, const void* x, const void* residual,
+    const void* weight, const void* bias, float eps, void* sum, void* y, float* stat, hipStream_t stream);
+
+/*
+ * dspark_norm_backward — gradients of dspark_norm, with q = dy weight and
+ * n = (x - mu) rstd:
+ *   dx      = rstd (q - mean_c q - n mean_c (q n)) + dsum   (RMS: without mean_c q)
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ * in fp32, each rounded once.
+ *
+ * Arguments: sizes, types and alignment as dspark_norm, and
+ *   dy    [M][C]
+ *   x     [M][C]     what was normalised: dspark_norm's sum, or its x without a residual
+ *   stat fp32 [M][2] as dspark_norm wrote it
+ *   weight [C] or NULL
+ *   dsum  [M][C] or NULL   the gradient that reaches the sum by its other path
+ *   dx    [M][C] out (of x, and of the residual alike); may be dsum itself
+ *   dweight, dbias [C] out; each of the three may be NULL: not computed (all
+ *                 three: nothing is enqueued).  With M == 0, dweight and dbias
+ *                 are zero.
+ *   workspace     >= dspark_norm_backward_workspace_bytes(M, C, dtype) bytes,
+ *                 256-byte aligned, any contents (NULL without dweight and dbias).
+ * Outputs or a workspace that overlap another array are refused, but for
+ * dx == dsum.
+ */
+dspark_status dspark_norm_backward(
+    int M, int C, dspark_dtype dtype, dspark_norm_kind kind, const void* dy, const void* x, const float* stat,
+    const void* weight, const void* dsum, void* dx, void* dweight, void* dbias,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
 
 /* Static description of a status code. */
 const char* dspark_status_string(dspark_status s);

@@ -97,7 +97,11 @@ def _declare(lib):
     lib.dspark_hidden_draft.argtypes = ([c_int] * 6 + [c_vp] * 7 + [c_f, c_vp, c_int, c_u64] + [c_vp] * 6 +
                                         [c_size, c_vp])
     lib.dspark_hidden_draft.restype = c_int
-    for name, n in (("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5), ("markov_loss_backward", 5),
+    lib.dspark_norm.argtypes = [c_int] * 4 + [c_vp] * 4 + [c_f] + [c_vp] * 4
+    lib.dspark_norm.restype = c_int
+    lib.dspark_norm_backward.argtypes = [c_int] * 4 + [c_vp] * 9 + [c_size, c_vp]
+    lib.dspark_norm_backward.restype = c_int
+    for name, n in (("norm_backward", 3), ("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5), ("markov_loss_backward", 5),
                     ("hidden_draft", 6)):
         f = getattr(lib, f"dspark_{name}_workspace_bytes")
         f.argtypes, f.restype = [c_int] * n, c_size
@@ -616,8 +620,7 @@ def _no_graph(name, *tensors):
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise RuntimeError(f"{name}() records no graph for autograd: call it under torch.no_grad() (or on "
-                                   "detached tensors); gradients come from linear_backward() and "
-                                   "markov_loss_backward()")
+                                   "detached tensors); gradients come from the _backward() functions")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -872,3 +875,89 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
             ctypes.c_uint64(seed & (2 ** 64 - 1)), _ptr(U), _ptr(tokens), _ptr(logit), _ptr(conf), _ptr(surv),
             _ptr(ws), ctypes.c_size_t(ws.numel()), _stream()))
     return tokens, logit, conf, surv
+
+
+# ----------------------------------------------------------------------------
+# a backbone's layer: normalisation
+# ----------------------------------------------------------------------------
+NORMS = {"layer": 0, "rms": 1}
+
+
+def _norm_kind(kind):
+    if kind not in NORMS:
+        raise ValueError(f"kind must be one of {sorted(NORMS)}")
+    return NORMS[kind]
+
+
+def _names(need, known):
+    need = (need,) if isinstance(need, str) else tuple(need)
+    if set(need) - set(known):
+        raise ValueError(f"need names {', '.join(known)}")
+    return need
+
+
+def norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, kind: str = "layer", stat=None, out=None,
+         sum_out=None):
+    """y = (s - mean) / sqrt(variance + eps) * weight + bias over the last axis
+    (kind "rms": s / sqrt(mean square + eps) * weight + bias) in one kernel;
+    returns y [M, C], or (y, s) with a residual: s = x + residual, rounded to
+    the storage type before it is normalised.
+
+    x and residual [M, C], weight and bias [C] are all float32 or all bfloat16
+    device tensors.  `stat`, a float32 [M, 2] tensor, receives (mean, 1 /
+    deviation) for norm_backward.  `out` takes y; `sum_out` takes s, and may be
+    x or residual.  Nothing is recorded for autograd, as for linear()."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, C = x.shape
+    dev = x.device
+    _optional(weight, "weight", x.dtype, (C,), dev)
+    _optional(bias, "bias", x.dtype, (C,), dev)
+    _optional(residual, "residual", x.dtype, (M, C), dev)
+    _optional(stat, "stat", torch.float32, (M, 2), dev)
+    _optional(out, "out", x.dtype, (M, C), dev)
+    _optional(sum_out, "sum_out", x.dtype, (M, C), dev)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out goes with residual")
+    k = _norm_kind(kind)
+    _fits(M, C)
+    _no_graph("norm", x, weight, bias, residual)
+    with _on(dev), _launching:
+        y = out if out is not None else x.new_empty((M, C))
+        s = sum_out if sum_out is not None or residual is None else x.new_empty((M, C))
+        _check(lib.dspark_norm(M, C, dt, k, _at(x), _at(residual), _at(weight), _at(bias), eps, _at(s), _at(y),
+                               _at(stat), _raw_stream(dev)))
+    return y if residual is None else (y, s)
+
+
+def norm_backward(dy, x, stat, weight=None, dsum=None, kind: str = "layer", need=("dx", "dweight", "dbias"), dx_out=None,
+                  workspace=None):
+    """Gradients of norm(); returns (dx [M, C], dweight [C], dbias [C]) in the
+    storage type, None for those not named in `need`.  x is what was normalised
+    (norm()'s s with a residual), stat what norm() wrote; dx is the gradient of
+    x and of the residual alike.  `dsum` [M, C], the gradient that reaches s by
+    its other path, is added to dx.  `dx_out` takes dx; it may be dsum."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, C = x.shape
+    dev = x.device
+    _is(dy, "dy", x.dtype, (M, C), dev)
+    _is(stat, "stat", torch.float32, (M, 2), dev)
+    _optional(weight, "weight", x.dtype, (C,), dev)
+    _optional(dsum, "dsum", x.dtype, (M, C), dev)
+    _optional(dx_out, "dx_out", x.dtype, (M, C), dev)
+    k = _norm_kind(kind)
+    need = _names(need, ("dx", "dweight", "dbias"))
+    _fits(M, C)
+    _no_graph("norm_backward", dy, x, stat, weight, dsum)
+    with _on(dev), _launching:
+        dx = None if "dx" not in need else dx_out if dx_out is not None else x.new_empty((M, C))
+        dw, db = (x.new_empty((C,)) if name in need else None for name in ("dweight", "dbias"))
+        ws, n = None, 0
+        if dw is not None or db is not None:
+            ws, n = _scratch(_bytes("norm_backward", M, C, dt), dev, "norm_backward", workspace)
+        _check(lib.dspark_norm_backward(M, C, dt, k, _at(dy), _at(x), _at(stat), _at(weight), _at(dsum), _at(dx),
+                                        _at(dw), _at(db), ws, n, _raw_stream(dev)))
+    return dx, dw, db

@@ -29,6 +29,7 @@ SOURCES = [
     ("sts_fit.hip", True),
     ("linear.hip", True),
     ("markov_loss.hip", True),
+    ("norm.hip", True),
 ]
 # Per-source flags.  The draft kernel's inputs are finite by contract, so its
 # maxima need not quiet signalling NaNs (no canonicalising instruction before

@@ -744,4 +744,101 @@ dspark_status dspark_hidden_draft(int B, int gamma, int V, int r, int d, dspark_
                     tokens, logit, conf, surv, workspace, workspace_bytes, stream);
 }
 
+namespace {
+
+dspark_status norm_sizes(int M, int C, dspark_dtype dtype, dspark_norm_kind kind) {
+  if (M < 0 || C < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
+  if (!known_dtype(dtype)) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype");
+  if (kind != DSPARK_NORM_LAYER && kind != DSPARK_NORM_RMS)
+    return fail(DSPARK_ERR_INVALID_ARG, "unknown normalisation");
+  if (M > dspark::kMaxRows) return fail(DSPARK_ERR_UNSUPPORTED, "M > 2^20");
+  if (C > dspark::kMaxChannels) return fail(DSPARK_ERR_UNSUPPORTED, "C > 32768");
+  return DSPARK_OK;
+}
+
+}  // namespace
+
+dspark_status dspark_norm(int M, int C, dspark_dtype dtype, dspark_norm_kind kind, const void* x, const void* residual,
+                          const void* weight, const void* bias, float eps, void* sum, void* y, float* stat,
+                          hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = norm_sizes(M, C, dtype, kind);
+  if (st != DSPARK_OK) return st;
+  if (!(eps >= 0.f && eps <= 3.4e38f)) return fail(DSPARK_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (M == 0 || C == 0) return DSPARK_OK;
+  if (!x || !y) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if ((residual != nullptr) != (sum != nullptr)) return fail(DSPARK_ERR_INVALID_ARG, "sum goes with residual");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(x, elem) || misaligned(residual, elem) || misaligned(weight, elem) || misaligned(bias, elem) ||
+      misaligned(sum, elem) || misaligned(y, elem) || misaligned(stat, 8))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t rows = size_t(M) * C * elem, row = size_t(C) * elem, stats = size_t(M) * 8;
+  // the sum may take its place over either of its parts, whose other overlaps are refused all the same
+  if (any_overlap({{sum, rows}}, {{sum == x ? nullptr : x, rows}, {sum == residual ? nullptr : residual, rows}}) ||
+      any_overlap({{sum, rows}, {y, rows}, {stat, stats}}, {{weight, row}, {bias, row}}) ||
+      any_overlap({{y, rows}, {stat, stats}}, {{x, rows}, {residual, rows}, {sum, rows}}))
+    return overlap_refused();
+  dspark::NormArgs a;
+  a.M = M;
+  a.C = C;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.center = kind == DSPARK_NORM_LAYER;
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.b = bias;
+  a.eps = eps;
+  a.sum = sum;
+  a.y = y;
+  a.stat = stat;
+  hipError_t e = dspark::launch_norm(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype) {
+  if (M <= 0 || C <= 0 || M > dspark::kMaxRows || C > dspark::kMaxChannels || !known_dtype(dtype)) return 0;
+  return dspark::norm_backward_workspace_bytes(M, C, dtype == DSPARK_BF16);
+}
+
+dspark_status dspark_norm_backward(int M, int C, dspark_dtype dtype, dspark_norm_kind kind, const void* dy,
+                                   const void* x, const float* stat, const void* weight, const void* dsum, void* dx,
+                                   void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = norm_sizes(M, C, dtype, kind);
+  if (st != DSPARK_OK) return st;
+  if (C == 0 || (!dx && !dweight && !dbias)) return DSPARK_OK;
+  if (M > 0 && (!dy || !x || !stat)) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(dy, elem) || misaligned(x, elem) || misaligned(stat, 8) || misaligned(weight, elem) ||
+      misaligned(dsum, elem) || misaligned(dx, elem) || misaligned(dweight, elem) || misaligned(dbias, elem))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t need = dweight || dbias ? dspark_norm_backward_workspace_bytes(M, C, dtype) : 0;
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_norm_backward_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  const size_t rows = size_t(M) * C * elem, row = size_t(C) * elem;
+  if (any_overlap({{dx, rows}, {dweight, row}, {dbias, row}, {workspace, need}},
+                  {{dy, rows}, {x, rows}, {stat, size_t(M) * 8}, {weight, row}, {dsum == dx ? nullptr : dsum, rows}}) ||
+      any_overlap({{dweight, row}, {dbias, row}, {workspace, need}}, {{dsum, rows}}))
+    return overlap_refused();
+  dspark::NormBackwardArgs a;
+  a.M = M;
+  a.C = C;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.center = kind == DSPARK_NORM_LAYER;
+  a.dy = dy;
+  a.x = x;
+  a.stat = stat;
+  a.w = weight;
+  a.dsum = dsum;
+  a.dx = dx;
+  a.dw = dweight;
+  a.db = dbias;
+  a.ws = workspace;
+  hipError_t e = dspark::launch_norm_backward(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
 }  // extern "C"

@@ -163,4 +163,27 @@ size_t loss_workspace_bytes(int N, int V, int d, int r, bool bf16, bool backward
 hipError_t launch_markov_loss(const LossArgs& a, hipStream_t stream);
 hipError_t launch_markov_loss_backward(const LossArgs& a, hipStream_t stream);
 
+// Normalisation of rows (x [M][C]) with the residual stream's sum, and its gradients.
+struct NormArgs {
+  int M, C;
+  bool bf16, center;   // center: layer normalisation, else root mean square
+  const void *x, *residual, *w, *b;
+  float eps;
+  void *sum, *y;
+  float* stat;
+};
+struct NormBackwardArgs {
+  int M, C;
+  bool bf16, center;
+  const void *dy, *x;
+  const float* stat;
+  const void *w, *dsum;
+  void *dx, *dw, *db;
+  void* ws;
+};
+constexpr int kMaxChannels = 32768;   // of a normalised row: 1024 threads keep it in registers
+size_t norm_backward_workspace_bytes(int M, int C, bool bf16);
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
+
 }  // namespace dspark

@@ -1,0 +1,387 @@
+// Layer and root-mean-square normalisation of rows with the residual stream's
+// sum, and its gradients.
+//
+//   s = x + residual,  y = (s - mu) rstd w + b            (rms: mu = 0)
+//   with q = dy w and n = (s - mu) rstd:
+//   ds = rstd (q - mean q - n mean(q n)) + dsum           (rms: without mean q)
+//   dw = sum over rows of dy n,  db = sum over rows of dy
+//
+// Bound by memory.  A row is read once and kept in registers as it is stored,
+// 16 bytes a lane and load; its mean and the sum of squares around it are made
+// wave by wave and joined in LDS (n_a, m_a, M_a with n_b, m_b, M_b: the squares
+// around the joint mean are M_a + M_b + (m_a - m_b)^2 n_a n_b / (n_a + n_b)),
+// so that no precision is lost to a mean that is large against the spread.
+#include "launch.h"
+#include "projection.h"
+
+namespace dspark {
+
+namespace {
+
+// 16 bytes of a row, at element alignment.
+template <typename T>
+struct Chunk {
+  static constexpr int N = 16 / sizeof(T);
+  u32x4_t raw;
+  __device__ __forceinline__ void load(const T* p, int n) {   // n values exist, zeros behind
+    if (n >= N) {
+      __builtin_memcpy(&raw, p, 16);
+      return;
+    }
+    T e[N] = {};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) e[i] = p[i];
+    __builtin_memcpy(&raw, e, 16);
+  }
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if (n >= N) {
+      __builtin_memcpy(p, &raw, 16);
+      return;
+    }
+    T e[N];
+    __builtin_memcpy(e, &raw, 16);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = e[i];
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(raw[i]);
+    else return i & 1 ? bf16_hi(raw[i >> 1]) : bf16_lo(raw[i >> 1]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[N]) {
+    T e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = from_f32<T>(v[i]);
+    __builtin_memcpy(&raw, e, 16);
+  }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+constexpr int kMaxWaves = 16;
+
+// Where a thread works: `waves` waves to a row (whole workgroup) or one (ONE:
+// every wave has rows of its own).
+struct Place {
+  int t, threads, wave, waves, unit, units;
+};
+template <bool ONE>
+__device__ __forceinline__ Place place() {
+  Place p;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = blockDim.x >> 6;
+  p.t = ONE ? threadIdx.x & 63 : threadIdx.x;
+  p.threads = ONE ? 64 : blockDim.x;
+  p.wave = ONE ? 0 : w;
+  p.waves = ONE ? 1 : n;
+  p.unit = ONE ? blockIdx.x * n + w : blockIdx.x;
+  p.units = ONE ? gridDim.x * n : gridDim.x;
+  return p;
+}
+
+// NV chunks per thread cover a row.  sum: where x + residual goes (with a
+// residual); stat: (mu, rstd) by row or null.
+template <typename T, int NV, bool ONE, bool CENTER>
+__global__ __launch_bounds__(NV > 2 ? 1024 : 512) void norm_kernel(int M, int C, const T* x, const T* residual,
+                                                                   const T* __restrict__ w, const T* __restrict__ b,
+                                                                   float eps, T* sum, T* __restrict__ y,
+                                                                   float2* __restrict__ stat) {
+  constexpr int N = Chunk<T>::N;
+  __shared__ float2 parts[2][kMaxWaves];
+  const Place p = place<ONE>();
+  const float each = 1.f / float(C);
+  int turn = 0;
+  for (int row = p.unit; row < M; row += p.units, turn ^= 1) {
+    Chunk<T> v[NV], r[NV];
+    const size_t at = size_t(row) * C;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.threads + p.t) * N;
+      v[i].load(x + at + c, C - c);
+    }
+    if (residual) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * p.threads + p.t) * N;
+        r[i].load(residual + at + c, C - c);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * p.threads + p.t) * N;
+        float s[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = v[i].get(e) + r[i].get(e);
+        v[i].set(s);   // what is stored is what is normalised: the gradient reads it again
+        if (c < C) v[i].store(sum + at + c, C - c);
+      }
+    }
+    // this wave's values: their number, mean and squares around it
+    float mean = 0.f, sq = 0.f;
+    if (CENTER) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) mean += v[i].get(e);
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) mine += min(max(C - (i * p.threads + p.wave * 64) * N, 0), 64 * N);
+      mean = wave_sum(mean);
+      mean = mine ? mean / float(mine) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int left = C - (i * p.threads + p.t) * N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float d = v[i].get(e) - mean;
+        sq += e < left ? d * d : 0.f;
+      }
+    }
+    sq = wave_sum(sq);
+    if (!ONE) {
+      if (p.t % 64 == 0) parts[turn][p.wave] = make_float2(mean, sq);
+      __syncthreads();
+      float n = 0.f;
+      mean = sq = 0.f;
+      for (int k = 0; k < p.waves; ++k) {
+        const float2 o = parts[turn][k];
+        if (CENTER) {
+          int has = 0;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) has += min(max(C - (i * p.threads + k * 64) * N, 0), 64 * N);
+          const float m = float(has), both = n + m;
+          if (has) {
+            const float d = o.x - mean;
+            sq += o.y + d * d * (n * m / both);
+            mean += d * (m / both);
+            n = both;
+          }
+        } else {
+          sq += o.y;
+        }
+      }
+    }
+    const float rstd = 1.f / sqrtf(sq * each + eps);
+    if (stat && p.t == 0) stat[row] = make_float2(mean, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.threads + p.t) * N;
+      if (c >= C) continue;
+      Chunk<T> cw, cb, o;
+      if (w) cw.load(w + c, C - c);
+      if (b) cb.load(b + c, C - c);
+      float s[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        s[e] = (v[i].get(e) - mean) * rstd;
+        if (w) s[e] *= cw.get(e);
+        if (b) s[e] += cb.get(e);
+      }
+      o.set(s);
+      o.store(y + at + c, C - c);
+    }
+  }
+}
+
+// Each unit (a workgroup, or ONE: a wave) goes through its rows and keeps its
+// share of dw and db in registers: part[unit][0 and 1][C].
+template <typename T, int NV, bool ONE, bool CENTER>
+__global__ __launch_bounds__(NV > 2 ? 1024 : 512) void norm_backward_kernel(
+    int M, int C, const T* __restrict__ dy, const T* __restrict__ x, const float2* __restrict__ stat,
+    const T* __restrict__ w, const T* dsum, T* dx, float* __restrict__ part) {
+  constexpr int N = Chunk<T>::N;
+  __shared__ float2 parts[2][kMaxWaves];
+  const Place p = place<ONE>();
+  const float each = 1.f / float(C);
+  float dw[NV][N] = {}, db[NV][N] = {};
+  int turn = 0;
+  for (int row = p.unit; row < M; row += p.units, turn ^= 1) {
+    Chunk<T> v[NV], g[NV], d[NV];
+    const size_t at = size_t(row) * C;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.threads + p.t) * N;
+      v[i].load(x + at + c, C - c);
+      g[i].load(dy + at + c, C - c);
+    }
+    const float2 st = stat[row];
+    float sq = 0.f, sn = 0.f;   // sums of q and of q n
+    if (dx) {
+      if (dsum) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * p.threads + p.t) * N;
+          d[i].load(dsum + at + c, C - c);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.threads + p.t) * N;
+      Chunk<T> cw;
+      if (w) cw.load(w + c, C - c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float n = (v[i].get(e) - st.x) * st.y, gy = g[i].get(e), q = w ? gy * cw.get(e) : gy;
+        sq += q;
+        if (c + e < C) sn += q * n;   // behind the end n is not 0
+        dw[i][e] += gy * n;
+        db[i][e] += gy;
+      }
+    }
+    if (!dx) continue;   // for all threads alike
+    if (CENTER) sq = wave_sum(sq);
+    sn = wave_sum(sn);
+    if (!ONE) {
+      if (p.t % 64 == 0) parts[turn][p.wave] = make_float2(sq, sn);
+      __syncthreads();
+      sq = sn = 0.f;
+      for (int k = 0; k < p.waves; ++k) {
+        const float2 o = parts[turn][k];
+        sq += o.x;
+        sn += o.y;
+      }
+    }
+    sq = CENTER ? sq * each : 0.f;
+    sn *= each;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.threads + p.t) * N;
+      if (c >= C) continue;
+      Chunk<T> cw, o;
+      if (w) cw.load(w + c, C - c);
+      float s[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float n = (v[i].get(e) - st.x) * st.y, gy = g[i].get(e), q = w ? gy * cw.get(e) : gy;
+        s[e] = st.y * (q - sq - n * sn);
+        if (dsum) s[e] += d[i].get(e);
+      }
+      o.set(s);
+      o.store(dx + at + c, C - c);
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * p.threads + p.t) * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e < C) {
+        part[(size_t(p.unit) * 2) * C + c + e] = dw[i][e];
+        part[(size_t(p.unit) * 2 + 1) * C + c + e] = db[i][e];
+      }
+  }
+}
+
+// dw and db (grid y: which): the units' shares, eight threads per column,
+// joined in order.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_join_kernel(int C, int units, const float* __restrict__ part, T* dw, T* db) {
+  __shared__ float sums[8][32];
+  T* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int l = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
+  float s = 0.f;
+  if (c < C) {
+#pragma unroll 8
+    for (int u = q; u < units; u += 8) s += part[(size_t(u) * 2 + blockIdx.y) * C + c];
+  }
+  sums[q][l] = s;
+  __syncthreads();
+  if (q == 0 && c < C) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sums[i][l];
+    out[c] = from_f32<T>(s);
+  }
+}
+
+// Launch shape: threads per workgroup, chunks per thread, whether a wave has
+// rows of its own, workgroups.
+struct Shape {
+  int threads, nv;
+  bool one;
+  int grid, units;
+};
+Shape shape_for(int M, int C, bool bf16, bool backward) {
+  const int chunks = (C + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
+  Shape s;
+  s.one = chunks <= 64;
+  s.nv = s.one ? 1 : chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 4096 ? 4 : 8;
+  s.threads = s.one ? 256 : (chunks + s.nv - 1) / s.nv;
+  s.threads = (s.threads + 63) / 64 * 64;
+  const int rows = s.one ? 4 : 1, groups = (M + rows - 1) / rows;
+  const int most = backward ? 1024 : 8192;
+  s.grid = groups < most ? groups : most;
+  s.units = s.grid * rows;
+  return s;
+}
+
+template <typename T, bool CENTER>
+hipError_t norm_t(const NormArgs& a, hipStream_t stream) {
+  const Shape s = shape_for(a.M, a.C, sizeof(T) == 2, false);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(s.grid), dim3(s.threads), 0, stream, a.M, a.C, static_cast<const T*>(a.x),
+                       static_cast<const T*>(a.residual), static_cast<const T*>(a.w), static_cast<const T*>(a.b), a.eps,
+                       static_cast<T*>(a.sum), static_cast<T*>(a.y), reinterpret_cast<float2*>(a.stat));
+    return hipGetLastError();
+  };
+  if (s.one) return go(norm_kernel<T, 1, true, CENTER>);
+  switch (s.nv) {
+    case 1: return go(norm_kernel<T, 1, false, CENTER>);
+    case 2: return go(norm_kernel<T, 2, false, CENTER>);
+    case 4: return go(norm_kernel<T, 4, false, CENTER>);
+    default: return go(norm_kernel<T, 8, false, CENTER>);
+  }
+}
+
+template <typename T, bool CENTER>
+hipError_t norm_backward_t(const NormBackwardArgs& a, hipStream_t stream) {
+  const Shape s = shape_for(a.M, a.C, sizeof(T) == 2, true);
+  float* part = a.dw || a.db ? static_cast<float*>(a.ws) : nullptr;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(s.grid), dim3(s.threads), 0, stream, a.M, a.C, static_cast<const T*>(a.dy),
+                       static_cast<const T*>(a.x), reinterpret_cast<const float2*>(a.stat), static_cast<const T*>(a.w),
+                       static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), part);
+    return hipGetLastError();
+  };
+  hipError_t e = hipSuccess;
+  if (a.M > 0) {
+    if (s.one)
+      e = go(norm_backward_kernel<T, 1, true, CENTER>);
+    else
+      switch (s.nv) {
+        case 1: e = go(norm_backward_kernel<T, 1, false, CENTER>); break;
+        case 2: e = go(norm_backward_kernel<T, 2, false, CENTER>); break;
+        case 4: e = go(norm_backward_kernel<T, 4, false, CENTER>); break;
+        default: e = go(norm_backward_kernel<T, 8, false, CENTER>); break;
+      }
+  }
+  if (e != hipSuccess || !(a.dw || a.db)) return e;
+  hipLaunchKernelGGL((norm_join_kernel<T>), dim3((a.C + 31) / 32, 2), dim3(256), 0, stream, a.C, a.M > 0 ? s.units : 0,
+                     part, static_cast<T*>(a.dw), static_cast<T*>(a.db));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t norm_backward_workspace_bytes(int M, int C, bool bf16) {
+  const size_t n = size_t(shape_for(M, C, bf16, true).units) * 2 * C * 4;
+  return (n + 255) & ~size_t(255);
+}
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  if (a.bf16) return a.center ? norm_t<bf16_t, true>(a, stream) : norm_t<bf16_t, false>(a, stream);
+  return a.center ? norm_t<float, true>(a, stream) : norm_t<float, false>(a, stream);
+}
+
+hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
+  if (a.bf16) return a.center ? norm_backward_t<bf16_t, true>(a, stream) : norm_backward_t<bf16_t, false>(a, stream);
+  return a.center ? norm_backward_t<float, true>(a, stream) : norm_backward_t<float, false>(a, stream);
+}
+
+}  // namespace dspark
