@@ -65,6 +65,11 @@ typedef enum {
   DSPARK_NORM_LAYER = 0,  /* mean and variance of the row */
   DSPARK_NORM_RMS = 1     /* its mean square              */
 } dspark_norm_kind;
+/* Gate of dspark_recurrence. */
+typedef enum {
+  DSPARK_GATE_SIGMOID = 0,  /* a logit per row and channel; the input enters by what the gate leaves */
+  DSPARK_GATE_DECAY = 1     /* a factor per channel, as in dspark_rnn_draft                          */
+} dspark_gate;
 /* Verify-length policy of dspark_serve. */
 typedef enum {
   DSPARK_POLICY_GLOBAL = 0,           /* dspark_schedule on the iteration's own survivals */
@@ -754,6 +759,83 @@ dspark_status dspark_norm_backward(
     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
+
+/*
+ * dspark_recurrence — a gated linear recurrence over packed sequences: the
+ * RNN head's state over whole sequences (DECAY), and the recurrent layer of a
+ * backbone (SIGMOID); with sequences of one row it is the step of a decoder.
+ *
+ * Defined by: [P-blog] §4 (RNN head: its state carries information from every
+ * earlier position; dspark_rnn_draft's reading is a per-channel decayed
+ * state); the formula, for the rows t of every sequence in order:
+ *   SIGMOID  a_t = 1 / (1 + exp(-gate[t])),  b_t = (1 - a_t) x[t]
+ *   DECAY    a_t = gate (per channel),       b_t = x[t]
+ *   h[t] = a_t h[t-1] + b_t        (the sequence's h0, or 0, before its first row)
+ * The state is carried in fp32; h is its rounding to the storage type
+ * (dspark_rnn_draft rounds the state itself at every step).
+ *
+ * Arguments
+ *   T, S, C       rows, sequences, channels (T * C == 0 with last NULL: no-op)
+ *   dtype         storage of x, h and of SIGMOID's gate
+ *   kind          of gate
+ *   offsets int32 [S + 1] or NULL   sequence s has the rows offsets[s] ..
+ *                 offsets[s + 1] - 1 (none allowed); not decreasing, from 0 on.
+ *                 Rows from offsets[S] on are left as they were.  NULL: T / S
+ *                 rows each (S divides T).  Offsets outside [0, T] are cut to it.
+ *   x         [T][C]
+ *   gate      [T][C] in the storage type (SIGMOID), or fp32 [C] (DECAY)
+ *   h0   fp32 [S][C] or NULL (zeros)
+ *   h         [T][C] out
+ *   last fp32 [S][C] out, or NULL: the state after each sequence's last row
+ *                 (h0 of a sequence without rows); may be h0 itself
+ *   states fp32 [ceil(T / 32)][C] out, or NULL: the state before each row whose
+ *                 index is a multiple of 32, which dspark_recurrence_backward
+ *                 takes.  Where such a row begins a sequence, or belongs to
+ *                 none, its states are left as they were or hold anything.
+ *   workspace     >= dspark_recurrence_workspace_bytes(T, S, C, dtype, kind)
+ *                 bytes (NULL if that is 0), 256-byte aligned, any contents.
+ *                 Calls that can overlap need separate ones.
+ * All arrays need element alignment only.  Outputs or a workspace that overlap
+ * another array are refused, but for last == h0.  Results do not depend on
+ * execution order, and no sequence's values on another's.
+ * Limits: T <= 2^24, S <= 2^20, C <= 65536.
+ */
+#define DSPARK_RECURRENCE_BLOCK 32
+dspark_status dspark_recurrence(
+    int T, int S, int C, dspark_dtype dtype, dspark_gate kind, const int32_t* offsets, const void* x,
+    const void* gate, const float* h0, void* h, float* last, float* states,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_recurrence_workspace_bytes(int T, int S, int C, dspark_dtype dtype, dspark_gate kind);
+
+/*
+ * dspark_recurrence_backward — gradients of dspark_recurrence:
+ *   d_t = dh[t] + a_{t+1} d_{t+1}          (a sequence's last row: dh[t] + dlast)
+ *   SIGMOID  dx = d (1 - a),  dgate[t] = d a (1 - a) (h[t-1] - x[t])
+ *   DECAY    dx = d,          dgate[c] = sum over all rows of d_t h[t-1]
+ *   dh0 = a d at the sequence's first row (dlast of a sequence without rows)
+ * in fp32, each rounded once; h[t-1] is made again in fp32 from `states`.
+ *
+ * Arguments: sizes, types, offsets and inputs as dspark_recurrence, and
+ *   dh         [T][C]
+ *   dlast fp32 [S][C] or NULL (zeros)
+ *   states fp32 [ceil(T / 32)][C] as dspark_recurrence wrote it
+ *   dx [T][C] out, dgate [T][C] in the storage type (SIGMOID) or fp32 [C]
+ *                 (DECAY) out, dh0 fp32 [S][C] out; each may be NULL: not
+ *                 computed (all three: nothing is enqueued).  dh0 may be dlast
+ *                 itself.  Rows of dx and dgate that belong to no sequence are
+ *                 left as they were.
+ *   workspace     >= dspark_recurrence_backward_workspace_bytes(T, S, C, dtype,
+ *                 kind) bytes (NULL if that is 0), 256-byte aligned, any contents.
+ * Outputs or a workspace that overlap another array are refused, but for
+ * dh0 == dlast.
+ */
+dspark_status dspark_recurrence_backward(
+    int T, int S, int C, dspark_dtype dtype, dspark_gate kind, const int32_t* offsets, const void* dh, const void* x,
+    const void* gate, const float* h0, const float* dlast, const float* states, void* dx, void* dgate, float* dh0,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_recurrence_backward_workspace_bytes(int T, int S, int C, dspark_dtype dtype, dspark_gate kind);
 
 /* Static description of a status code. */
 const char* dspark_status_string(dspark_status s);

@@ -101,8 +101,13 @@ def _declare(lib):
     lib.dspark_norm.restype = c_int
     lib.dspark_norm_backward.argtypes = [c_int] * 4 + [c_vp] * 9 + [c_size, c_vp]
     lib.dspark_norm_backward.restype = c_int
-    for name, n in (("norm_backward", 3), ("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5), ("markov_loss_backward", 5),
-                    ("hidden_draft", 6)):
+    lib.dspark_recurrence.argtypes = [c_int] * 5 + [c_vp] * 8 + [c_size, c_vp]
+    lib.dspark_recurrence.restype = c_int
+    lib.dspark_recurrence_backward.argtypes = [c_int] * 5 + [c_vp] * 11 + [c_size, c_vp]
+    lib.dspark_recurrence_backward.restype = c_int
+    for name, n in (("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5),
+                    ("markov_loss_backward", 5), ("hidden_draft", 6), ("norm_backward", 3), ("recurrence", 5),
+                    ("recurrence_backward", 5)):
         f = getattr(lib, f"dspark_{name}_workspace_bytes")
         f.argtypes, f.restype = [c_int] * n, c_size
     lib.dspark_status_string.argtypes = [c_int]
@@ -878,7 +883,7 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
 
 
 # ----------------------------------------------------------------------------
-# a backbone's layer: normalisation
+# a backbone's layer: normalisation, gated recurrence
 # ----------------------------------------------------------------------------
 NORMS = {"layer": 0, "rms": 1}
 
@@ -961,3 +966,95 @@ def norm_backward(dy, x, stat, weight=None, dsum=None, kind: str = "layer", need
         _check(lib.dspark_norm_backward(M, C, dt, k, _at(dy), _at(x), _at(stat), _at(weight), _at(dsum), _at(dx),
                                         _at(dw), _at(db), ws, n, _raw_stream(dev)))
     return dx, dw, db
+
+
+GATES = {"sigmoid": 0, "decay": 1}
+RECURRENCE_BLOCK = 32     # rows from one kept state to the next
+
+
+def _recurrence_inputs(x, gate, kind, offsets, sequences, h0):
+    """Checks the recurrence's inputs; returns (T, S, C, storage, gate kind, device)."""
+    torch = _torch()
+    dt = _storage(x, "x")
+    if kind not in GATES:
+        raise ValueError(f"kind must be one of {sorted(GATES)}")
+    T, C = x.shape
+    dev = x.device
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, None, dev)
+        if offsets.dim() != 1 or len(offsets) == 0:
+            raise ValueError("offsets must have shape (sequences + 1,)")
+        S = len(offsets) - 1
+        if sequences is not None and sequences != S:
+            raise ValueError(f"offsets of {S} sequences, not {sequences}")
+    else:
+        S = sequences if sequences is not None else len(h0) if h0 is not None else 1
+        if S < 0 or (T % S if S else T):
+            raise ValueError(f"{T} rows are no {S} sequences of equal length: give offsets")
+    _optional(h0, "h0", torch.float32, (S, C), dev)
+    if kind == "sigmoid":
+        _is(gate, "gate", x.dtype, (T, C), dev)
+    else:
+        _is(gate, "gate", torch.float32, (C,), dev)
+    _fits(T, S, C)
+    return T, S, C, dt, GATES[kind], dev
+
+
+def recurrence(x, gate, kind: str = "sigmoid", offsets=None, sequences=None, h0=None, states=None, last=None, out=None,
+               workspace=None):
+    """h[t] = a[t] * h[t - 1] + b[t] over the rows of each sequence; returns
+    h [T, C].
+
+    kind "sigmoid": a = sigmoid(gate), b = (1 - a) * x, with gate [T, C] of x's
+    type; kind "decay": a = gate, a float32 [C], b = x (the RNN head's state,
+    without rounding it at every step).  x [T, C] is float32 or bfloat16; the
+    state is carried in float32.
+
+    Sequences: `offsets`, int32 [S + 1], of packed ones (rows behind the last
+    are left as they were in `out`), or `sequences` of equal length (by default
+    as many as h0 has, or one); T rows in T sequences are a decoder's step.
+    `h0`, float32 [S, C], holds the states before the first rows (default 0);
+    `last`, float32 [S, C], receives those after the last ones, and may be h0.
+    `states`, a float32 [ceil(T / RECURRENCE_BLOCK), C] tensor, receives what
+    recurrence_backward needs.  Nothing is recorded for autograd, as for
+    linear()."""
+    torch = _torch()
+    lib = load()
+    T, S, C, dt, k, dev = _recurrence_inputs(x, gate, kind, offsets, sequences, h0)
+    _optional(states, "states", torch.float32, (-(-T // RECURRENCE_BLOCK), C), dev)
+    _optional(last, "last", torch.float32, (S, C), dev)
+    _optional(out, "out", x.dtype, (T, C), dev)
+    _no_graph("recurrence", x, gate, h0)
+    with _on(dev), _launching:
+        h = out if out is not None else x.new_empty((T, C))
+        ws, n = _scratch(_bytes("recurrence", T, S, C, dt, k), dev, "recurrence", workspace)
+        _check(lib.dspark_recurrence(T, S, C, dt, k, _at(offsets), _at(x), _at(gate), _at(h0), _at(h), _at(last),
+                                     _at(states), ws, n, _raw_stream(dev)))
+    return h
+
+
+def recurrence_backward(dh, x, gate, states, kind: str = "sigmoid", offsets=None, sequences=None, h0=None, dlast=None,
+                        need=("dx", "dgate", "dh0"), workspace=None):
+    """Gradients of recurrence(); returns (dx [T, C], dgate, dh0 float32
+    [S, C]), None for those not named in `need`; dgate is [T, C] in x's type
+    (sigmoid) or float32 [C] (decay).  `states` is what recurrence() wrote,
+    dh [T, C] the gradient of h, `dlast`, float32 [S, C], that of the last
+    states (default 0).  Rows of dx and dgate that belong to no sequence are
+    not written."""
+    torch = _torch()
+    lib = load()
+    T, S, C, dt, k, dev = _recurrence_inputs(x, gate, kind, offsets, sequences, h0)
+    _is(dh, "dh", x.dtype, (T, C), dev)
+    _is(states, "states", torch.float32, (-(-T // RECURRENCE_BLOCK), C), dev)
+    _optional(dlast, "dlast", torch.float32, (S, C), dev)
+    need = _names(need, ("dx", "dgate", "dh0"))
+    _no_graph("recurrence_backward", dh, x, gate, states, h0, dlast)
+    with _on(dev), _launching:
+        dx = torch.empty_like(x) if "dx" in need else None
+        dg = torch.empty_like(gate) if "dgate" in need else None
+        d0 = torch.empty((S, C), dtype=torch.float32, device=dev) if "dh0" in need else None
+        ws, n = _scratch(_bytes("recurrence_backward", T, S, C, dt, k), dev, "recurrence_backward", workspace)
+        _check(lib.dspark_recurrence_backward(T, S, C, dt, k, _at(offsets), _at(dh), _at(x), _at(gate), _at(h0),
+                                              _at(dlast), _at(states), _at(dx), _at(dg), _at(d0), ws, n,
+                                              _raw_stream(dev)))
+    return dx, dg, d0

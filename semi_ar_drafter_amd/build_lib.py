@@ -30,6 +30,7 @@ SOURCES = [
     ("linear.hip", True),
     ("markov_loss.hip", True),
     ("norm.hip", True),
+    ("recurrence.hip", True),
 ]
 # Per-source flags.  The draft kernel's inputs are finite by contract, so its
 # maxima need not quiet signalling NaNs (no canonicalising instruction before

@@ -841,4 +841,136 @@ dspark_status dspark_norm_backward(int M, int C, dspark_dtype dtype, dspark_norm
   return DSPARK_OK;
 }
 
+namespace {
+
+bool recurrence_sizes_fit(int T, int S, int C) {
+  return T >= 0 && S >= 0 && C >= 0 && T <= dspark::kMaxTokens && S <= dspark::kMaxRows && C <= kMaxD;
+}
+bool known_gate(dspark_gate k) { return k == DSPARK_GATE_SIGMOID || k == DSPARK_GATE_DECAY; }
+
+// Checks shared by the recurrence and its gradient.
+dspark_status recurrence_inputs(const dspark::RecurrenceArgs& a, dspark_dtype dtype, dspark_gate kind) {
+  if (a.T < 0 || a.S < 0 || a.C < 0) return fail(DSPARK_ERR_INVALID_ARG, "negative size");
+  if (!known_dtype(dtype)) return fail(DSPARK_ERR_INVALID_ARG, "unknown dtype");
+  if (!known_gate(kind)) return fail(DSPARK_ERR_INVALID_ARG, "unknown gate");
+  if (a.T > dspark::kMaxTokens) return fail(DSPARK_ERR_UNSUPPORTED, "T > 2^24");
+  if (a.S > dspark::kMaxRows) return fail(DSPARK_ERR_UNSUPPORTED, "S > 2^20");
+  if (a.C > kMaxD) return fail(DSPARK_ERR_UNSUPPORTED, "C > 65536");
+  if (!a.offsets && (a.S == 0 ? a.T > 0 : a.T % a.S != 0))
+    return fail(DSPARK_ERR_INVALID_ARG, "without offsets S has to divide T");
+  if (a.T > 0 && a.C > 0 && !a.x) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if (!a.gate && a.C > 0 && (a.T > 0 || !a.sigmoid)) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = a.bf16 ? 2 : 4;
+  if (misaligned(a.x, elem) || misaligned(a.gate, a.sigmoid ? elem : 4) || misaligned(a.offsets, 4) ||
+      misaligned(a.h0, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  return DSPARK_OK;
+}
+
+dspark::RecurrenceArgs recurrence_args(int T, int S, int C, dspark_dtype dtype, dspark_gate kind,
+                                       const int32_t* offsets, const void* x, const void* gate, const float* h0,
+                                       void* ws) {
+  dspark::RecurrenceArgs a = {};
+  a.T = T;
+  a.S = S;
+  a.C = C;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.sigmoid = kind == DSPARK_GATE_SIGMOID;
+  a.offsets = offsets;
+  a.x = x;
+  a.gate = gate;
+  a.h0 = h0;
+  a.ws = ws;
+  return a;
+}
+
+// Bytes of the arrays by row and channel, of the gate, by sequence and of the kept states.
+struct RecurrenceBytes {
+  size_t rows, gate, ends, states, offsets;
+};
+RecurrenceBytes recurrence_bytes(const dspark::RecurrenceArgs& a) {
+  const size_t c = size_t(a.C), rows = size_t(a.T) * c * (a.bf16 ? 2 : 4);
+  return {rows, a.sigmoid ? rows : c * 4, size_t(a.S) * c * 4,
+          (size_t(a.T) + DSPARK_RECURRENCE_BLOCK - 1) / DSPARK_RECURRENCE_BLOCK * c * 4, (size_t(a.S) + 1) * 4};
+}
+
+}  // namespace
+
+size_t dspark_recurrence_workspace_bytes(int T, int S, int C, dspark_dtype dtype, dspark_gate kind) {
+  if (!recurrence_sizes_fit(T, S, C) || !known_dtype(dtype) || !known_gate(kind) || T == 0 || S == 0 || C == 0) return 0;
+  return dspark::recurrence_workspace_bytes(T, S, C, dtype == DSPARK_BF16, kind == DSPARK_GATE_SIGMOID);
+}
+
+dspark_status dspark_recurrence(int T, int S, int C, dspark_dtype dtype, dspark_gate kind, const int32_t* offsets,
+                                const void* x, const void* gate, const float* h0, void* h, float* last, float* states,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark::RecurrenceArgs a = recurrence_args(T, S, C, dtype, kind, offsets, x, gate, h0, workspace);
+  dspark_status st = recurrence_inputs(a, dtype, kind);
+  if (st != DSPARK_OK) return st;
+  if (C == 0 || S == 0 || (T == 0 && !last)) return DSPARK_OK;
+  if (T > 0 && !h) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  if (misaligned(h, a.bf16 ? 2 : 4) || misaligned(last, 4) || misaligned(states, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t need = dspark_recurrence_workspace_bytes(T, S, C, dtype, kind);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_recurrence_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  const RecurrenceBytes n = recurrence_bytes(a);
+  if (any_overlap({{h, n.rows}, {last, n.ends}, {states, n.states}, {workspace, need}},
+                  {{offsets, n.offsets}, {x, n.rows}, {gate, n.gate}, {h0 == last ? nullptr : h0, n.ends}}) ||
+      any_overlap({{h, n.rows}, {states, n.states}, {workspace, need}}, {{h0, n.ends}}))
+    return overlap_refused();
+  a.h = h;
+  a.last = last;
+  a.states = states;
+  hipError_t e = dspark::launch_recurrence(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_recurrence_backward_workspace_bytes(int T, int S, int C, dspark_dtype dtype, dspark_gate kind) {
+  if (!recurrence_sizes_fit(T, S, C) || !known_dtype(dtype) || !known_gate(kind) || S == 0 || C == 0) return 0;
+  return dspark::recurrence_backward_workspace_bytes(T, S, C, dtype == DSPARK_BF16, kind == DSPARK_GATE_SIGMOID);
+}
+
+dspark_status dspark_recurrence_backward(int T, int S, int C, dspark_dtype dtype, dspark_gate kind,
+                                         const int32_t* offsets, const void* dh, const void* x, const void* gate,
+                                         const float* h0, const float* dlast, const float* states, void* dx,
+                                         void* dgate, float* dh0, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark::RecurrenceArgs a = recurrence_args(T, S, C, dtype, kind, offsets, x, gate, h0, workspace);
+  dspark_status st = recurrence_inputs(a, dtype, kind);
+  if (st != DSPARK_OK) return st;
+  if (C == 0 || (!dx && !dgate && !dh0)) return DSPARK_OK;
+  if (T > 0 && S > 0 && (!dh || !states)) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = a.bf16 ? 2 : 4;
+  if (misaligned(dh, elem) || misaligned(dx, elem) || misaligned(dgate, a.sigmoid ? elem : 4) ||
+      misaligned(dlast, 4) || misaligned(states, 4) || misaligned(dh0, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t need = dspark_recurrence_backward_workspace_bytes(T, S, C, dtype, kind);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_recurrence_backward_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  const RecurrenceBytes n = recurrence_bytes(a);
+  if (any_overlap({{dx, n.rows}, {dgate, n.gate}, {dh0, n.ends}, {workspace, need}},
+                  {{offsets, n.offsets},
+                   {dh, n.rows},
+                   {x, n.rows},
+                   {gate, n.gate},
+                   {h0, n.ends},
+                   {dlast == dh0 ? nullptr : dlast, n.ends},
+                   {states, n.states}}) ||
+      any_overlap({{dx, n.rows}, {dgate, n.gate}, {workspace, need}}, {{dlast, n.ends}}))
+    return overlap_refused();
+  a.dh = dh;
+  a.dlast = dlast;
+  a.states_in = states;
+  a.dx = dx;
+  a.dgate = dgate;
+  a.dh0 = dh0;
+  hipError_t e = dspark::launch_recurrence_backward(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
 }  // extern "C"

@@ -186,4 +186,27 @@ size_t norm_backward_workspace_bytes(int M, int C, bool bf16);
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
 
+// Gated linear recurrence over packed sequences (x [T][C]) and its gradients;
+// the gradient's members are unused by the forward call and the other way
+// round.
+struct RecurrenceArgs {
+  int T, S, C;
+  bool bf16, sigmoid;   // sigmoid: gate [T][C] in the storage type, else decay: fp32 [C]
+  const int32_t* offsets;
+  const void *x, *gate;
+  const float* h0;
+  void* h;
+  float *last, *states;
+  const void* dh;
+  const float *dlast, *states_in;
+  void *dx, *dgate;
+  float* dh0;
+  void* ws;
+};
+constexpr int kMaxTokens = 1 << 24;   // rows of the recurrence
+size_t recurrence_workspace_bytes(int T, int S, int C, bool bf16, bool sigmoid);
+size_t recurrence_backward_workspace_bytes(int T, int S, int C, bool bf16, bool sigmoid);
+hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t stream);
+hipError_t launch_recurrence_backward(const RecurrenceArgs& a, hipStream_t stream);
+
 }  // namespace dspark
