@@ -53,7 +53,7 @@ typedef enum {
   DSPARK_LAUNCH_COOPERATIVE = 0,  /* cooperative launch: every workgroup is guaranteed resident (default) */
   DSPARK_LAUNCH_EXCLUSIVE = 1     /* plain launch; the caller guarantees no other kernel runs meanwhile */
 } dspark_launch;
-/* Activation of dspark_linear. */
+/* Activation of dspark_linear and dspark_gated_linear. */
 typedef enum {
   DSPARK_ACT_NONE = 0,  /* z                                            */
   DSPARK_ACT_RELU = 1,  /* max(z, 0); NaN stays NaN                     */
@@ -836,6 +836,64 @@ dspark_status dspark_recurrence_backward(
     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 size_t dspark_recurrence_backward_workspace_bytes(int T, int S, int C, dspark_dtype dtype, dspark_gate kind);
+
+/*
+ * dspark_gated_linear — the gated feed-forward projection of a backbone's
+ * layer: both products, the activation and their product in one kernel.
+ *
+ * Defined by: [P-blog] §4 parallel stage (the backbone whose hidden states the
+ * heads read); the formula:
+ *   zg = x wg^T + bg,  zu = x wu^T + bu     (fp32 accumulate)
+ *   y  = act(zg) zu                         (fp32, rounded once to the storage type)
+ *
+ * Arguments
+ *   M, N, K       rows, features, input features (M == 0 or N == 0 is a no-op;
+ *                 K == 0 leaves zg = bg, zu = bu)
+ *   dtype         storage of x, wg, wu, bg, bu, y
+ *   x  [M][K], wg [N][K], wu [N][K]   16-byte aligned
+ *   bg, bu    [N]    or NULL, each
+ *   act              activation (NONE: y = zg zu)
+ *   y         [M][N] out
+ *   pre  fp32 [2][M][N] out, or NULL: zg, then zu, which
+ *                 dspark_gated_linear_backward takes
+ *   workspace     >= dspark_gated_linear_workspace_bytes(M, N, K, dtype) bytes
+ *                 (NULL if that is 0), 256-byte aligned, any contents.  Calls
+ *                 that can overlap need separate ones.
+ * Outputs or a workspace that overlap another array are refused.  Results do
+ * not depend on execution order.  Limits: M <= 2^20, N <= 2^24, K <= 65536.
+ * The block's second projection, with the residual, is dspark_linear.
+ */
+dspark_status dspark_gated_linear(
+    int M, int N, int K, dspark_dtype dtype, const void* x, const void* wg, const void* wu, const void* bg,
+    const void* bu, dspark_activation act, void* y, float* pre, void* workspace, size_t workspace_bytes,
+    hipStream_t stream);
+
+size_t dspark_gated_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
+
+/*
+ * dspark_gated_linear_backward — gradients of dspark_gated_linear:
+ *   dzg = dy zu act'(zg),  dzu = dy act(zg)   (rounded to the storage type for the
+ *                      products, as in dspark_linear_backward)
+ *   dx  = dzg wg + dzu wu,  dwg = dzg^T x,  dwu = dzu^T x,
+ *   dbg, dbu = sums over rows of dzg, dzu
+ * each summed in fp32 and rounded once.  relu's slope at 0 is 0.
+ *
+ * Arguments: sizes, types and layouts as dspark_gated_linear, and
+ *   dy   [M][N]         16-byte aligned
+ *   pre  fp32 [2][M][N] as dspark_gated_linear wrote it
+ *   dx [M][K], dwg [N][K], dwu [N][K], dbg [N], dbu [N] out; each may be NULL:
+ *                 not computed (all five: nothing is enqueued).  With M == 0
+ *                 those of the weights and biases are zero; with N == 0, dx is.
+ *   workspace     >= dspark_gated_linear_backward_workspace_bytes(M, N, K, dtype)
+ *                 bytes, 256-byte aligned, any contents.
+ * Outputs or a workspace that overlap another array are refused.
+ */
+dspark_status dspark_gated_linear_backward(
+    int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x, const void* wg, const void* wu,
+    dspark_activation act, const float* pre, void* dx, void* dwg, void* dwu, void* dbg, void* dbu,
+    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t dspark_gated_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype);
 
 /* Static description of a status code. */
 const char* dspark_status_string(dspark_status s);

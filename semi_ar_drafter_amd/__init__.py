@@ -11,4 +11,4 @@ from .binding import (markov_draft, parallel_draft, schedule, schedule_threshold
                       verify, workspace_bytes, library_path, set_draft_launch, get_draft_launch, rnn_draft,
                       rnn_workspace_bytes, schedule_workspace_bytes, step, linear, linear_backward, markov_loss,
                       markov_loss_backward, hidden_draft, norm, norm_backward, recurrence,
-                      recurrence_backward, RECURRENCE_BLOCK)
+                      recurrence_backward, RECURRENCE_BLOCK, gated_linear, gated_linear_backward)

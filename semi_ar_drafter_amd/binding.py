@@ -105,9 +105,13 @@ def _declare(lib):
     lib.dspark_recurrence.restype = c_int
     lib.dspark_recurrence_backward.argtypes = [c_int] * 5 + [c_vp] * 11 + [c_size, c_vp]
     lib.dspark_recurrence_backward.restype = c_int
-    for name, n in (("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5), ("markov_loss", 5),
-                    ("markov_loss_backward", 5), ("hidden_draft", 6), ("norm_backward", 3), ("recurrence", 5),
-                    ("recurrence_backward", 5)):
+    lib.dspark_gated_linear.argtypes = [c_int] * 4 + [c_vp] * 5 + [c_int] + [c_vp] * 3 + [c_size, c_vp]
+    lib.dspark_gated_linear.restype = c_int
+    lib.dspark_gated_linear_backward.argtypes = [c_int] * 4 + [c_vp] * 4 + [c_int] + [c_vp] * 7 + [c_size, c_vp]
+    lib.dspark_gated_linear_backward.restype = c_int
+    for name, n in (("gated_linear", 4), ("gated_linear_backward", 4), ("linear", 4), ("linear_backward", 4), ("linear_backward_act", 5),
+                    ("markov_loss", 5), ("markov_loss_backward", 5), ("hidden_draft", 6), ("norm_backward", 3),
+                    ("recurrence", 5), ("recurrence_backward", 5)):
         f = getattr(lib, f"dspark_{name}_workspace_bytes")
         f.argtypes, f.restype = [c_int] * n, c_size
     lib.dspark_status_string.argtypes = [c_int]
@@ -883,7 +887,7 @@ def hidden_draft(anchor, h, Wo, W1, W2, conf_w, conf_b: float, sts_T, bias=None,
 
 
 # ----------------------------------------------------------------------------
-# a backbone's layer: normalisation, gated recurrence
+# a backbone's layer: normalisation, gated recurrence, gated feed-forward
 # ----------------------------------------------------------------------------
 NORMS = {"layer": 0, "rms": 1}
 
@@ -1058,3 +1062,62 @@ def recurrence_backward(dh, x, gate, states, kind: str = "sigmoid", offsets=None
                                               _at(dlast), _at(states), _at(dx), _at(dg), _at(d0), ws, n,
                                               _raw_stream(dev)))
     return dx, dg, d0
+
+
+def gated_linear(x, wg, wu, bg=None, bu=None, act: str = "silu", pre=None, out=None, workspace=None):
+    """y = act(x @ wg.T + bg) * (x @ wu.T + bu) in one kernel; returns y [M, N].
+
+    x [M, K], wg and wu [N, K], bg and bu [N] are all float32 or all bfloat16
+    device tensors; act is as for linear().  `pre`, a float32 [2, M, N] tensor,
+    receives the two sums for gated_linear_backward.  Nothing is recorded for
+    autograd, as for linear().  linear() with a residual is the block's second
+    projection."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, K = x.shape
+    N = wg.shape[0]
+    dev = x.device
+    _is(wg, "wg", x.dtype, (N, K), dev)
+    _is(wu, "wu", x.dtype, (N, K), dev)
+    _optional(bg, "bg", x.dtype, (N,), dev)
+    _optional(bu, "bu", x.dtype, (N,), dev)
+    _optional(pre, "pre", torch.float32, (2, M, N), dev)
+    _optional(out, "out", x.dtype, (M, N), dev)
+    a = _act(act)
+    _fits(M, N, K)
+    _no_graph("gated_linear", x, wg, wu, bg, bu)
+    with _on(dev), _launching:
+        y = out if out is not None else x.new_empty((M, N))
+        ws, n = _scratch(_bytes("gated_linear", M, N, K, dt), dev, "gated_linear", workspace)
+        _check(lib.dspark_gated_linear(M, N, K, dt, _at(x), _at(wg), _at(wu), _at(bg), _at(bu), a, _at(y), _at(pre),
+                                       ws, n, _raw_stream(dev)))
+    return y
+
+
+def gated_linear_backward(dy, x, wg, wu, pre, act: str = "silu", need=("dx", "dwg", "dwu", "dbg", "dbu"),
+                          workspace=None):
+    """Gradients of gated_linear(); returns (dx [M, K], dwg [N, K], dwu [N, K],
+    dbg [N], dbu [N]) in the storage type, None for those not named in `need`.
+    `pre` is what gated_linear() wrote."""
+    torch = _torch()
+    lib = load()
+    dt = _storage(x, "x")
+    M, K = x.shape
+    N = wg.shape[0]
+    dev = x.device
+    _is(wg, "wg", x.dtype, (N, K), dev)
+    _is(wu, "wu", x.dtype, (N, K), dev)
+    _is(dy, "dy", x.dtype, (M, N), dev)
+    _is(pre, "pre", torch.float32, (2, M, N), dev)
+    a = _act(act)
+    need = _names(need, ("dx", "dwg", "dwu", "dbg", "dbu"))
+    _fits(M, N, K)
+    _no_graph("gated_linear_backward", dy, x, wg, wu, pre)
+    with _on(dev), _launching:
+        new = lambda name, *sh: x.new_empty(sh) if name in need else None  # noqa: E731
+        grads = new("dx", M, K), new("dwg", N, K), new("dwu", N, K), new("dbg", N), new("dbu", N)
+        ws, n = _scratch(_bytes("gated_linear_backward", M, N, K, dt), dev, "gated_linear_backward", workspace)
+        _check(lib.dspark_gated_linear_backward(M, N, K, dt, _at(dy), _at(x), _at(wg), _at(wu), a, _at(pre),
+                                                *[_at(g) for g in grads], ws, n, _raw_stream(dev)))
+    return grads

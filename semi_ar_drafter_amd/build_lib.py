@@ -29,6 +29,7 @@ SOURCES = [
     ("sts_fit.hip", True),
     ("linear.hip", True),
     ("markov_loss.hip", True),
+    ("gated.hip", True),
     ("norm.hip", True),
     ("recurrence.hip", True),
 ]

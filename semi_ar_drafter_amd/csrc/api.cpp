@@ -744,6 +744,106 @@ dspark_status dspark_hidden_draft(int B, int gamma, int V, int r, int d, dspark_
                     tokens, logit, conf, surv, workspace, workspace_bytes, stream);
 }
 
+size_t dspark_gated_linear_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+  if (M <= 0 || N <= 0 || K < 0 || M > dspark::kMaxRows || N > kMaxV || K > kMaxD || !known_dtype(dtype)) return 0;
+  return dspark::gated_workspace_bytes(M, N, K, dtype == DSPARK_BF16);
+}
+
+dspark_status dspark_gated_linear(int M, int N, int K, dspark_dtype dtype, const void* x, const void* wg,
+                                  const void* wu, const void* bg, const void* bu, dspark_activation act, void* y,
+                                  float* pre, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = linear_sizes(M, N, K, dtype, act);
+  if (st != DSPARK_OK) return st;
+  if (M == 0 || N == 0) return DSPARK_OK;
+  if (!y || (K > 0 && (!x || !wg || !wu))) return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(x, 16) || misaligned(wg, 16) || misaligned(wu, 16))
+    return fail(DSPARK_ERR_INVALID_ARG, "x, wg and wu need 16-byte alignment");
+  if (misaligned(bg, elem) || misaligned(bu, elem) || misaligned(y, elem) || misaligned(pre, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t need = dspark_gated_linear_workspace_bytes(M, N, K, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_gated_linear_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+  if (any_overlap({{y, m * n * elem}, {pre, m * n * 8}, {workspace, need}},
+                  {{x, m * k * elem}, {wg, n * k * elem}, {wu, n * k * elem}, {bg, n * elem}, {bu, n * elem}}))
+    return overlap_refused();
+  dspark::GatedArgs a;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.act = int(act);
+  a.x = x;
+  a.wg = wg;
+  a.wu = wu;
+  a.bg = bg;
+  a.bu = bu;
+  a.y = y;
+  a.pre = pre;
+  a.ws = workspace;
+  hipError_t e = dspark::launch_gated(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
+size_t dspark_gated_linear_backward_workspace_bytes(int M, int N, int K, dspark_dtype dtype) {
+  if (M < 0 || N < 0 || K < 0 || M > dspark::kMaxRows || N > kMaxV || K > kMaxD || !known_dtype(dtype)) return 0;
+  return dspark::gated_backward_workspace_bytes(M, N, K, dtype == DSPARK_BF16);
+}
+
+dspark_status dspark_gated_linear_backward(int M, int N, int K, dspark_dtype dtype, const void* dy, const void* x,
+                                           const void* wg, const void* wu, dspark_activation act, const float* pre,
+                                           void* dx, void* dwg, void* dwu, void* dbg, void* dbu, void* workspace,
+                                           size_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = '\0';
+  dspark_status st = linear_sizes(M, N, K, dtype, act);
+  if (st != DSPARK_OK) return st;
+  const bool some = M > 0 && N > 0;
+  if (some && (!dy || !pre || (dx && K > 0 && (!wg || !wu)) || ((dwg || dwu) && K > 0 && !x)))
+    return fail(DSPARK_ERR_INVALID_ARG, "null pointer argument");
+  const size_t elem = dtype == DSPARK_BF16 ? 2 : 4;
+  if (misaligned(x, 16) || misaligned(wg, 16) || misaligned(wu, 16) || misaligned(dy, 16))
+    return fail(DSPARK_ERR_INVALID_ARG, "x, wg, wu and dy need 16-byte alignment");
+  if (misaligned(dx, elem) || misaligned(dwg, elem) || misaligned(dwu, elem) || misaligned(dbg, elem) ||
+      misaligned(dbu, elem) || misaligned(pre, 4))
+    return fail(DSPARK_ERR_INVALID_ARG, "misaligned tensor");
+  const size_t need = dspark_gated_linear_backward_workspace_bytes(M, N, K, dtype);
+  st = check_workspace(workspace, workspace_bytes, need, "dspark_gated_linear_backward_workspace_bytes");
+  if (st != DSPARK_OK) return st;
+  const size_t m = size_t(M), n = size_t(N), k = size_t(K);
+  if (any_overlap({{dx, m * k * elem},
+                   {dwg, n * k * elem},
+                   {dwu, n * k * elem},
+                   {dbg, n * elem},
+                   {dbu, n * elem},
+                   {workspace, need}},
+                  {{dy, m * n * elem}, {x, m * k * elem}, {wg, n * k * elem}, {wu, n * k * elem}, {pre, m * n * 8}}))
+    return overlap_refused();
+  if (!dx && !dwg && !dwu && !dbg && !dbu) return DSPARK_OK;
+  dspark::GatedBackwardArgs a;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = dtype == DSPARK_BF16;
+  a.act = int(act);
+  a.dy = dy;
+  a.x = x;
+  a.wg = wg;
+  a.wu = wu;
+  a.pre = pre;
+  a.dx = dx;
+  a.dwg = dwg;
+  a.dwu = dwu;
+  a.dbg = dbg;
+  a.dbu = dbu;
+  a.ws = workspace;
+  hipError_t e = dspark::launch_gated_backward(a, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  return DSPARK_OK;
+}
+
 namespace {
 
 dspark_status norm_sizes(int M, int C, dspark_dtype dtype, dspark_norm_kind kind) {

@@ -1,0 +1,468 @@
+// Gated feed-forward projection: y = act(x wg^T + bg) * (x wu^T + bu), and its
+// gradients.
+//
+//   forward    C(a = feature of wg and of wu, b = row): one product whose a
+//              operand is both matrices, 64 (or 32, 16) features of the one and
+//              the same of the other in a wave's share of a tile, so that a lane
+//              holds a feature's gate and value: the activation and the product
+//              are the epilogue
+//   dz         dzg = dy zu act'(zg),  dzu = dy act(zg), once, side by side:
+//              [row][dzg, padded to 64 | dzu, padded to 64]
+//   dx         C(a = input, b = row) = sum_n wg[n][a] dzg[b][n] + wu[n][a] dzu[b][n]:
+//              one contraction of two parts
+//   dwg, dwu   C(a = input, b = column of dz) = sum_m x[m][a] dz[m][b]: one product
+// dz is rounded to the storage type, which the products take (see linear.hip);
+// the pre-activations that the gradient reads are fp32: rounded to bf16 they
+// would add half a bf16 step of zu to every dzg.
+#include "launch.h"
+#include "product.h"
+
+namespace dspark {
+
+namespace {
+
+template <typename T>
+struct GatedEpi {
+  const T *bg, *bu;
+  T* y;
+  float *zg, *zu;   // pre-activations, or null
+  int act, na;
+  bool vec;         // rows of na values keep four-value alignment, and so do the biases
+  template <int FM, int FN>
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+    acc_zero(acc);
+  }
+  __device__ __forceinline__ void finish(f32x4_t g, f32x4_t u, int b, int a, int n) const {
+    const size_t at = size_t(b) * na + a;
+    if (bg) g += load4(bg + a, n, vec);
+    if (bu) u += load4(bu + a, n, vec);
+    if (zg) {
+      store4(zg + at, g, n, vec);
+      store4(zu + at, u, n, vec);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] *= act_value<T>(act, g[e]);
+    store4(y + at, u, n, vec);
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM / 2; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb) finish(acc[i][j], acc[i + FM / 2][j], b, a, na - a);
+      }
+    }
+  }
+};
+
+// A split's sums: part[split][b][zg, ld values | zu, ld values].
+struct GatedAddEpi {
+  float* part;
+  long ld, split;
+  int na;
+  template <int FM, int FN>
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+    acc_zero(acc);
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * (i % (FM / 2)) + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb)
+          store4(part + blockIdx.y * split + size_t(b) * 2 * ld + (i < FM / 2 ? 0 : ld) + a, acc[i][j], na - a, true);
+      }
+    }
+  }
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void join_gated_kernel(int M, int splits, const float* __restrict__ part, long ld,
+                                                         GatedEpi<T> epi) {
+  const int quads = (epi.na + 3) / 4;
+  const long at = long(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= long(M) * quads) return;
+  const int b = int(at / quads), a = int(at % quads) * 4;
+  f32x4_t g = {0.f, 0.f, 0.f, 0.f}, u = g;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + (size_t(s) * M + b) * 2 * ld + a;
+    g += *reinterpret_cast<const f32x4_t*>(p);
+    u += *reinterpret_cast<const f32x4_t*>(p + ld);
+  }
+  epi.finish(g, u, b, a, epi.na - a);
+}
+
+// A few rows (M <= 16), as in linear.hip: both weights are read once, straight
+// into the matrix instruction's operand registers.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_gated_kernel(int M, int N, int K, const bf16_t* __restrict__ x,
+                                                                    const bf16_t* __restrict__ wg,
+                                                                    const bf16_t* __restrict__ wu,
+                                                                    GatedEpi<bf16_t> epi) {
+  __shared__ f32x4_t part[WAVES][2][64];
+#if defined(__HIP_DEVICE_COMPILE__)
+  // uniform: matrix instructions ignore the lane mask, so nothing around them may diverge
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int a0 = blockIdx.x * 16;
+  const int full = K / 32;   // whole steps of 32
+  const int s0 = full * wave / WAVES, s1 = full * (wave + 1) / WAVES;
+  const long row = long(min(a0 + l, N - 1)) * K + q * 8;
+  const bf16_t *pg = wg + row, *pu = wu + row;
+  const bf16_t* px = x + long(min(l, M - 1)) * K + q * 8;
+  f32x4_t ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
+  auto step = [&](u32x4_t g, u32x4_t u, u32x4_t b) {
+    const bf16x8_t vb = __builtin_bit_cast(bf16x8_t, b);
+    ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, g), vb, ag, 0, 0, 0);
+    au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u), vb, au, 0, 0, 0);
+  };
+  constexpr int U = 4;   // steps in flight: 8 KiB of weights per wave
+  for (int s = s0; s < s1; s += U) {
+    u32x4_t g[U], u[U], b[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (s + i < s1) {
+        __builtin_memcpy(&g[i], pg + (s + i) * 32, 16);
+        __builtin_memcpy(&u[i], pu + (s + i) * 32, 16);
+        __builtin_memcpy(&b[i], px + (s + i) * 32, 16);
+      }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (s + i < s1) step(g[i], u[i], b[i]);
+  }
+  if (wave == WAVES - 1 && full * 32 < K) {   // the rest, zero behind the row's end
+    const int n = K - full * 32 - q * 8;
+    uint32_t g[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) {
+        g[e >> 1] |= uint32_t(pg[full * 32 + e]) << (16 * (e & 1));
+        u[e >> 1] |= uint32_t(pu[full * 32 + e]) << (16 * (e & 1));
+        b[e >> 1] |= uint32_t(px[full * 32 + e]) << (16 * (e & 1));
+      }
+    step(u32x4_t{g[0], g[1], g[2], g[3]}, u32x4_t{u[0], u[1], u[2], u[3]}, u32x4_t{b[0], b[1], b[2], b[3]});
+  }
+  part[wave][0][lane] = ag;
+  part[wave][1][lane] = au;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) {
+      ag += part[v][0][lane];
+      au += part[v][1][lane];
+    }
+    const int a = a0 + 4 * q;
+    if (l < M && a < N) epi.finish(ag, au, l, a, N - a);
+  }
+#endif
+}
+
+constexpr int kGatedRows = 16;   // rows per workgroup of gated_dz_kernel where it sums, 4 where it does not
+
+// dz[m][0][n] and dz[m][1][n] into rows of 2 ld values (columns N..ld of each
+// half and rows M..rows zero), and part[chunk][2][n] = the chunk's sums over its
+// rows, in fp32, before the rounding to T.  256 threads, four columns each.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_dz_kernel(int M, int rows, int N, int act, const T* __restrict__ dy,
+                                                       const float* __restrict__ zg, const float* __restrict__ zu,
+                                                       T* __restrict__ dz, long ld, float* __restrict__ part, bool vec,
+                                                       int per) {
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int m0 = blockIdx.y * per, m1 = min(rows, m0 + per);
+  if (n >= ld) return;
+  const int left = N - n;
+  f32x4_t sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
+#pragma unroll 4
+  for (int m = m0; m < m1; ++m) {
+    f32x4_t dg = {0.f, 0.f, 0.f, 0.f}, du = dg;
+    if (m < M && left > 0) {
+      const size_t at = size_t(m) * N + n;
+      const f32x4_t d = load4(dy + at, left, vec), g = load4(zg + at, left, vec), u = load4(zu + at, left, vec);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dg[e] = d[e] * u[e] * act_slope<T>(act, g[e]);
+        du[e] = d[e] * act_value<T>(act, g[e]);
+      }
+    }
+    if (dz) {
+      store4(dz + size_t(m) * 2 * ld + n, dg, 4, true);
+      store4(dz + size_t(m) * 2 * ld + ld + n, du, 4, true);
+    }
+    sg += dg;
+    su += du;
+  }
+  if (part) {
+    float* p = part + size_t(blockIdx.y) * 2 * N + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) {
+        p[e] = sg[e];
+        p[N + e] = su[e];
+      }
+  }
+}
+
+// dbg and dbu: sums over the chunks of the columns of both, 8 threads each,
+// joined in order.  32 columns per workgroup.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_dbias_kernel(int N, int chunks, const float* __restrict__ part, T* dbg,
+                                                          T* dbu) {
+  __shared__ float sums[8][32];
+  const int c = threadIdx.x & 31, q = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (n < 2 * N) {
+#pragma unroll 8
+    for (int i = q; i < chunks; i += 8) s += part[size_t(i) * 2 * N + n];
+  }
+  sums[q][c] = s;
+  __syncthreads();
+  if (q == 0 && n < 2 * N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sums[i][c];
+    T* out = n < N ? dbg : dbu;
+    if (out) out[n < N ? n : n - N] = from_f32<T>(s);
+  }
+}
+
+// The weights' gradients: row b of the product is a row of dwg (b < half) or of dwu.
+template <typename T>
+struct TwoOutEpi {
+  T *g, *u;
+  int half, N, na;
+  bool vec;
+  template <int FM, int FN>
+  __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
+    acc_zero(acc);
+  }
+  __device__ __forceinline__ void join(f32x4_t v, int b, int a, int n) const {
+    T* out = b < half ? g : u;
+    const int row = b < half ? b : b - half;
+    if (out && row < N) store4(out + size_t(row) * na + a, v, n, vec);
+  }
+  template <int FM, int FN>
+  __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int a = t.a0 + 16 * i + 4 * (lane >> 4);
+      if (a >= na) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int b = t.b0 + 16 * j + (lane & 15);
+        if (b < t.nb) join(acc[i][j], b, a, na - a);
+      }
+    }
+  }
+};
+
+template <typename T>
+GatedEpi<T> gated_epi(const GatedArgs& a) {
+  GatedEpi<T> epi;
+  epi.bg = static_cast<const T*>(a.bg);
+  epi.bu = static_cast<const T*>(a.bu);
+  epi.y = static_cast<T*>(a.y);
+  epi.zg = a.pre;
+  epi.zu = a.pre ? a.pre + size_t(a.M) * a.N : nullptr;
+  epi.act = a.act;
+  epi.na = a.N;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.bg) | reinterpret_cast<uintptr_t>(a.bu);
+  epi.vec = a.N % 4 == 0 && at % (4 * sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
+  return epi;
+}
+
+// Where the rows are few enough for few_rows_gated_kernel.
+bool few_gated_rows(int M, int N, int K) { return K % 8 != 0 ? M <= 16 : M <= 4 || (M <= 16 && N <= 4096); }
+
+Plan gated_plan(int M, int N, int K, bool bf16) {
+  return bf16 ? plan_for(2 * N, M, K, false, false, true) : Plan{0, f32_splits(2 * N, M, K)};
+}
+size_t gated_split_bytes(int M, int N, int K, bool bf16) {
+  const int s = gated_plan(M, N, K, bf16).splits;
+  return s > 1 ? up256(size_t(s) * M * 2 * up64(N) * 4) : 0;
+}
+// Bytes of a copy of `rows` rows of K values to rows of whole steps.
+size_t padded_bytes(long rows, int K) { return up256(size_t(rows) * up64(K) * 2); }
+
+// A copy of `rows` rows at *ws, which moves on behind it; *p and *ld become the copy's.
+hipError_t padded(long rows, int K, const bf16_t** p, long* ld, unsigned char** ws, hipStream_t stream) {
+  bf16_t* copy = reinterpret_cast<bf16_t*>(*ws);
+  *ws += padded_bytes(rows, K);
+  *ld = up64(K);
+  const hipError_t e = pad_rows(rows, K, *ld, *p, copy, stream);
+  *p = copy;
+  return e;
+}
+
+template <typename T>
+hipError_t gated_product(const GatedArgs& a, const Product<T>& g, float* part, hipStream_t stream) {
+  const GatedEpi<T> epi = gated_epi<T>(a);
+  const Plan plan = gated_plan(a.M, a.N, a.K, sizeof(T) == 2);
+  auto run = [&](auto&& make) {
+    if constexpr (sizeof(T) == 2)
+      return launch_bf16_dual(g, make, a.N, a.M, plan, stream);
+    else
+      return launch_f32_dual(g, make, a.N, a.M, plan.splits, stream);
+  };
+  if (plan.splits == 1) return run([&](auto) { return epi; });
+  const long ld = up64(a.N);
+  const hipError_t e = run([&](auto) { return GatedAddEpi{part, ld, long(a.M) * 2 * ld, a.N}; });
+  if (e != hipSuccess) return e;
+  const long quads = long(a.M) * ((a.N + 3) / 4);
+  hipLaunchKernelGGL((join_gated_kernel<T>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, stream, a.M,
+                     plan.splits, part, ld, epi);
+  return hipGetLastError();
+}
+
+hipError_t gated_bf16(const GatedArgs& a, hipStream_t stream) {
+  const bf16_t *x = static_cast<const bf16_t*>(a.x), *wg = static_cast<const bf16_t*>(a.wg),
+               *wu = static_cast<const bf16_t*>(a.wu);
+  if (few_gated_rows(a.M, a.N, a.K)) {
+    const dim3 grid(unsigned((a.N + 15) / 16));
+    // more waves share the contraction where there are too few workgroups to fill the compute units
+    if (a.N <= 16 * 2 * kComputeUnits)
+      hipLaunchKernelGGL((few_rows_gated_kernel<8>), grid, dim3(512), 0, stream, a.M, a.N, a.K, x, wg, wu,
+                         gated_epi<bf16_t>(a));
+    else
+      hipLaunchKernelGGL((few_rows_gated_kernel<4>), grid, dim3(256), 0, stream, a.M, a.N, a.K, x, wg, wu,
+                         gated_epi<bf16_t>(a));
+    return hipGetLastError();
+  }
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  hipError_t e = hipSuccess;
+  long ldx = a.K, ldw = a.K;
+  // the b operand has to end in zeros, and the a operand's rows to be aligned
+  if (a.K % kStep && (e = padded(a.M, a.K, &x, &ldx, &ws, stream)) != hipSuccess) return e;
+  if (a.K % 8 && ((e = padded(a.N, a.K, &wg, &ldw, &ws, stream)) != hipSuccess ||
+                  (e = padded(a.N, a.K, &wu, &ldw, &ws, stream)) != hipSuccess))
+    return e;
+  Product<bf16_t> g = {};
+  g.A[0] = {wg, ldw, 1, a.N};
+  g.A[1] = {wu, ldw, 1, a.N};
+  g.B[0] = {x, ldx, 1, a.M};
+  g.K[0] = a.K;
+  return gated_product(a, g, reinterpret_cast<float*>(ws), stream);
+}
+
+hipError_t gated_f32(const GatedArgs& a, hipStream_t stream) {
+  Product<float> g = {};
+  g.A[0] = {static_cast<const float*>(a.wg), a.K, 1, a.N};
+  g.A[1] = {static_cast<const float*>(a.wu), a.K, 1, a.N};
+  g.B[0] = {static_cast<const float*>(a.x), a.K, 1, a.M};
+  g.K[0] = a.K;
+  return gated_product(a, g, static_cast<float*>(a.ws), stream);
+}
+
+long dz_rows(int M, bool bf16) { return bf16 ? up64(M) : M; }
+size_t part_bytes(int M, int N) {
+  return up256(size_t((up64(M) + kGatedRows - 1) / kGatedRows) * 2 * N * 4);
+}
+
+template <typename T>
+hipError_t gated_backward_t(const GatedBackwardArgs& a, hipStream_t stream) {
+  constexpr bool bf16 = sizeof(T) == 2;
+  const long ld = up64(a.N), rows = dz_rows(a.M, bf16);
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  float* part = reinterpret_cast<float*>(ws);
+  ws += part_bytes(a.M, a.N);
+  T* dz = reinterpret_cast<T*>(ws);
+  ws += up256(size_t(rows) * 2 * ld * sizeof(T));
+  const bool sums = a.dbg || a.dbu, products = (a.dx || a.dwg || a.dwu) && a.K > 0;
+  // the grid's second axis holds 65535 chunks
+  const int per = rows > 65535l * kGatedRows ? 2 * kGatedRows : sums || rows > 65535l * 4 ? kGatedRows : 4;
+  hipError_t e = hipSuccess;
+  if (rows > 0 && a.N > 0) {
+    const float* zu = a.pre + size_t(a.M) * a.N;
+    hipLaunchKernelGGL((gated_dz_kernel<T>), dim3(unsigned((ld + 1023) / 1024), unsigned((rows + per - 1) / per)),
+                       dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, zu,
+                       products ? dz : nullptr, ld, sums ? part : nullptr,
+                       a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0, per);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (sums && a.N > 0) {
+    hipLaunchKernelGGL((gated_dbias_kernel<T>), dim3(unsigned((2l * a.N + 31) / 32)), dim3(256), 0, stream, a.N,
+                       int((rows + per - 1) / per), part, static_cast<T*>(a.dbg), static_cast<T*>(a.dbu));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dx && a.K > 0 && a.M > 0) {
+    const T *wg = static_cast<const T*>(a.wg), *wu = static_cast<const T*>(a.wu);
+    unsigned char* behind = ws;
+    long ldw = a.K;
+    if constexpr (bf16) {
+      if (a.K % 8 && a.N > 0 && ((e = padded(a.N, a.K, &wg, &ldw, &behind, stream)) != hipSuccess ||
+                                 (e = padded(a.N, a.K, &wu, &ldw, &behind, stream)) != hipSuccess))
+        return e;
+    }
+    Product<T> g = {};
+    g.A[0] = {wg, 1, ldw, a.K};
+    g.A[1] = {wu, 1, ldw, a.K};
+    g.B[0] = {dz, 2 * ld, 1, a.M};
+    g.B[1] = {dz + ld, 2 * ld, 1, a.M};
+    g.K[0] = g.K[1] = a.N;
+    LinearEpi<T> epi = {};
+    epi.y = static_cast<T*>(a.dx);
+    epi.na = a.K;
+    epi.vec = aligned4<T>(a.dx, a.K);
+    e = product<kCols, kRows>(g, false, epi, a.K, a.M, reinterpret_cast<float*>(behind), stream);
+    if (e != hipSuccess) return e;
+  }
+  if ((a.dwg || a.dwu) && a.K > 0 && a.N > 0) {
+    const T* x = static_cast<const T*>(a.x);
+    unsigned char* behind = ws;
+    long ldx = a.K;
+    if constexpr (bf16) {
+      if (a.K % 8 && a.M > 0 && (e = padded(a.M, a.K, &x, &ldx, &behind, stream)) != hipSuccess) return e;
+    }
+    Product<T> g = {};
+    g.A[0] = {x, 1, ldx, a.K};
+    g.B[0] = {dz, 1, 2 * ld, int(2 * ld)};
+    g.K[0] = a.M;
+    TwoOutEpi<T> epi;
+    epi.g = static_cast<T*>(a.dwg);
+    epi.u = static_cast<T*>(a.dwu);
+    epi.half = int(ld);
+    epi.N = a.N;
+    epi.na = a.K;
+    epi.vec = (!a.dwg || aligned4<T>(a.dwg, a.K)) && (!a.dwu || aligned4<T>(a.dwu, a.K));
+    return product<kCols, kCols>(g, false, epi, a.K, int(2 * ld), reinterpret_cast<float*>(behind), stream);
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t gated_workspace_bytes(int M, int N, int K, bool bf16) {
+  if (!bf16) return gated_split_bytes(M, N, K, false);
+  if (few_gated_rows(M, N, K)) return 0;
+  return (K % kStep ? padded_bytes(M, K) : 0) + (K % 8 ? 2 * padded_bytes(N, K) : 0) + gated_split_bytes(M, N, K, true);
+}
+
+size_t gated_backward_workspace_bytes(int M, int N, int K, bool bf16) {
+  const long ld = up64(N);
+  const size_t dz = part_bytes(M, N) + up256(size_t(dz_rows(M, bf16)) * 2 * ld * (bf16 ? 2 : 4));
+  const bool copies = bf16 && K % 8 != 0;
+  // dx reads the weights, dwg and dwu read x, one after the other
+  const size_t dx = (copies ? 2 * padded_bytes(N, K) : 0) + split_bytes(K, M, 2l * N, bf16, false, true);
+  const size_t dw = (copies ? padded_bytes(M, K) : 0) + split_bytes(K, int(2 * ld), M, bf16, false, true);
+  return dz + (dx > dw ? dx : dw);
+}
+
+hipError_t launch_gated(const GatedArgs& a, hipStream_t stream) {
+  return a.bf16 ? gated_bf16(a, stream) : gated_f32(a, stream);
+}
+
+hipError_t launch_gated_backward(const GatedBackwardArgs& a, hipStream_t stream) {
+  return a.bf16 ? gated_backward_t<bf16_t>(a, stream) : gated_backward_t<float>(a, stream);
+}
+
+}  // namespace dspark

@@ -209,4 +209,28 @@ size_t recurrence_backward_workspace_bytes(int T, int S, int C, bool bf16, bool 
 hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t stream);
 hipError_t launch_recurrence_backward(const RecurrenceArgs& a, hipStream_t stream);
 
+// Gated feed-forward projection (x [M][K], wg and wu [N][K], pre [2][M][N]) and its gradients.
+struct GatedArgs {
+  int M, N, K;
+  bool bf16;
+  int act;
+  const void *x, *wg, *wu, *bg, *bu;
+  void* y;
+  float* pre;
+  void* ws;
+};
+struct GatedBackwardArgs {
+  int M, N, K;
+  bool bf16;
+  int act;
+  const void *dy, *x, *wg, *wu;
+  const float* pre;
+  void *dx, *dwg, *dwu, *dbg, *dbu;
+  void* ws;
+};
+size_t gated_workspace_bytes(int M, int N, int K, bool bf16);
+size_t gated_backward_workspace_bytes(int M, int N, int K, bool bf16);
+hipError_t launch_gated(const GatedArgs& a, hipStream_t stream);
+hipError_t launch_gated_backward(const GatedBackwardArgs& a, hipStream_t stream);
+
 }  // namespace dspark

@@ -15,9 +15,7 @@
 // us, whose last rounds of tiles fill a part of the compute units, dz_kernel 37
 // us for 168 MB).
 #include "launch.h"
-#include "projection.h"
-#include "tile_bf16.h"
-#include "tile_f32.h"
+#include "product.h"
 
 namespace dspark {
 
@@ -153,34 +151,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(int M, int N, int 
 #endif
 }
 
-// y = act(sum over splits + bias) + residual, the splits in order: four
-// values per thread.
-template <typename T>
-__global__ __launch_bounds__(256) void join_splits_kernel(int M, int N, int splits, const float* __restrict__ part,
-                                                          long ld, LinearEpi<T> epi) {
-  const int quads = (N + 3) / 4;
-  const long at = long(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= long(M) * quads) return;
-  const int b = int(at / quads), a = int(at % quads) * 4, n = N - a;
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(part + (size_t(s) * M + b) * ld + a);
-  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  epi.finish(v, epi.bias ? load4(epi.bias + a, n, epi.vec) : zero,
-             epi.residual ? load4(epi.residual + size_t(b) * N + a, n, epi.vec) : zero, b, a, n);
-}
-
-inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-inline long up64(long x) { return (x + 63) / 64 * 64; }
 inline long dz_stride(int N) { return up64(N); }
 inline int dz_chunks(int M) { return int((up64(M) + kDzRows - 1) / kDzRows); }
-
-// Splits of a product's contraction into partial sums [split][rows][up64(na)].
-inline size_t split_bytes(int na, int nb, long K, bool bf16, bool any, bool cols) {
-  if (na == 0 || nb == 0) return 0;
-  const int s = bf16 ? plan_for(na, nb, K, any, cols, true).splits : f32_splits(na, nb, K);
-  return s > 1 ? up256(size_t(s) * nb * up64(na) * 4) : 0;
-}
 
 template <typename T>
 LinearEpi<T> linear_epi(const LinearArgs& a) {
@@ -195,32 +167,6 @@ LinearEpi<T> linear_epi(const LinearArgs& a) {
                        reinterpret_cast<uintptr_t>(a.bias);
   epi.vec = a.N % 4 == 0 && at % (4 * sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0;
   return epi;
-}
-
-// A product into epi, or by way of split partial sums in `part`; LA, LB and
-// any are for bf16 (fp32 kernels read any layout).
-template <int LA, int LB, typename T>
-hipError_t product(const Product<T>& g, bool any, const LinearEpi<T>& epi, int na, int nb, float* part,
-                   hipStream_t stream) {
-  if (na == 0 || nb == 0) return hipSuccess;
-  constexpr bool bf16 = sizeof(T) == 2;
-  const Plan plan = bf16 ? plan_for(na, nb, g.K[0], any, LA == kCols, true) : Plan{0, f32_splits(na, nb, g.K[0])};
-  const int splits = plan.splits;
-  auto run = [&](auto&& make) {
-    if constexpr (bf16)
-      return any ? launch_bf16<LA, LA, LB, true>(g, make, na, nb, plan, stream)
-                 : launch_bf16<LA, LA, LB, false>(g, make, na, nb, plan, stream);
-    else
-      return launch_f32(g, make, na, nb, splits, stream);
-  };
-  if (splits == 1) return run([&](auto) { return epi; });
-  const long ld = up64(na);
-  const hipError_t e = run([&](auto) { return AddEpi{part, ld, na, true, long(nb) * ld}; });
-  if (e != hipSuccess) return e;
-  const long quads = long(nb) * ((na + 3) / 4);
-  hipLaunchKernelGGL((join_splits_kernel<T>), dim3(unsigned((quads + 255) / 256)), dim3(256), 0, stream, nb, na,
-                     splits, part, ld, epi);
-  return hipGetLastError();
 }
 
 // Where few_rows_kernel beats the tiles (per call, in a graph): for one row
@@ -321,11 +267,6 @@ hipError_t make_dz(const LinearBackwardArgs& a, bool copy, long rows, const T** 
     hipLaunchKernelGGL((dbias_kernel<T>), dim3(unsigned((a.N + 31) / 32)), dim3(256), 0, stream, a.N,
                        rows > 0 ? int((rows + per - 1) / per) : 0, part, static_cast<T*>(a.dbias));
   return hipGetLastError();
-}
-
-template <typename T>
-bool aligned4(const void* p, int n) {
-  return n % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0;
 }
 
 // The gradient's products through the same epilogue as the forward one,

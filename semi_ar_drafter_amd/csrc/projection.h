@@ -245,6 +245,10 @@ struct LinearEpi {
     if (residual) v += rv;
     store4(y + at, v, n, vec);
   }
+  __device__ __forceinline__ void join(f32x4_t v, int b, int a, int n) const {
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    finish(v, bias ? load4(bias + a, n, vec) : zero, residual ? load4(residual + size_t(b) * na + a, n, vec) : zero, b, a, n);
+  }
   template <int FM, int FN>
   __device__ __forceinline__ void done(f32x4_t (&acc)[FM][FN], const TileAt& t, void*) const {
     const int lane = threadIdx.x & 63;

@@ -82,7 +82,10 @@ constexpr int loads_per_wave(int n, int waves) { return (n + waves - 1) / waves;
 
 // One operand's staging by one wave: per-lane byte offsets from the tile's
 // base, fixed over the steps.
-template <int LAYOUT, int ROWS, int LOADS>
+// PAIR > 0 (kRows): the tile's rows are those of two matrices, PAIR of the one
+// and PAIR of the other in turn (a wave's share of the tile is 2 PAIR rows, so
+// that its accumulators of both lie in the same lanes).
+template <int LAYOUT, int ROWS, int LOADS, int PAIR = 0>
 struct Stager {
   static constexpr int units = ROWS * kStep / 512;   // 1 KiB each
   static constexpr int chunks = LAYOUT == kRows ? kStep / 8 : ROWS / 8;   // in a row of LDS
@@ -102,7 +105,8 @@ struct Stager {
       const int row = (unit_of(w, i) * 64 + lane) / chunks;
       if (LAYOUT == kRows) {
         // rows behind the last one repeat it: their results are not stored
-        off[i] = uint32_t(min(row, n - 1 - first)) * uint32_t(ld * 2) + uint32_t(chunk_of(lane)) * 16;
+        const int r = PAIR ? row / (2 * PAIR + !PAIR) * PAIR + row % (PAIR + !PAIR) : row;
+        off[i] = uint32_t(min(r, n - 1 - first)) * uint32_t(ld * 2) + uint32_t(chunk_of(lane)) * 16;
       } else {
         const int c = (unit_of(w, i) * 64 + lane) % chunks ^ (pair_turn(ROWS, row) << 1);
         // chunks behind the last one repeat it
@@ -110,6 +114,9 @@ struct Stager {
       }
     }
   }
+
+  // Whether load i of wave w is of the second matrix.
+  __device__ __forceinline__ static bool other(int w, int i) { return PAIR && unit_of(w, i) * 8 / (PAIR + !PAIR) % 2; }
 
   // The last step of a contraction that ends inside it: whether the chunk
   // (kRows) or row (kCols) of a load lies behind its end.  left: what is left of it.
@@ -185,17 +192,22 @@ __device__ __forceinline__ void tile_place(int id, int tiles_a, int tiles_b, int
 }
 
 // grid: x tiles, y splits of the contraction.  LA0, LA1: layout of the a
-// operand in the two parts of the contraction; LB of b.
-template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi>
+// operand in the two parts of the contraction; LB of b.  DUAL: the a operand
+// is two matrices of na rows, A[0] and A[1], multiplied by the same b over one
+// contraction; a wave's accumulators i < FM / 2 belong to the first, the others
+// to the same rows of the second.
+template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi, bool DUAL = false>
 __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> g, Epi epi, int na, int nb) {
   extern __shared__ __align__(1024) unsigned char smem[];
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NA = loads_per_wave(Sh::la, Sh::waves), NB = loads_per_wave(Sh::lb, Sh::waves);
   constexpr bool two = LA0 != LA1;
+  constexpr int halves = DUAL ? 2 : 1, BM = Sh::BM / halves, pair = DUAL ? BM / Sh::WA : 0;
+  static_assert(!DUAL || (LA0 == kRows && LA1 == kRows && !ANY && Sh::FM % 2 == 0 && pair % 8 == 0), "two matrices by rows");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tile_a, tile_b;
-  tile_place(blockIdx.x, (na + Sh::BM - 1) / Sh::BM, (nb + Sh::BN - 1) / Sh::BN, &tile_a, &tile_b);
-  const int a_first = tile_a * Sh::BM, b_first = tile_b * Sh::BN;
+  tile_place(blockIdx.x, (na + BM - 1) / BM, (nb + Sh::BN - 1) / Sh::BN, &tile_a, &tile_b);
+  const int a_first = tile_a * BM, b_first = tile_b * Sh::BN;
   if (g.nb) nb = *g.nb;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
   const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
@@ -205,12 +217,12 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
   TileAt at;
   at.wave_a = wave / Sh::WB;
   at.wave_b = wave % Sh::WB;
-  at.a0 = a_first + at.wave_a * (Sh::BM / Sh::WA);
+  at.a0 = a_first + at.wave_a * (BM / Sh::WA);
   at.b0 = b_first + at.wave_b * (Sh::BN / Sh::WB);
   at.nb = nb;
   at.tile_a = tile_a;
 
-  Stager<LA0, Sh::BM, NA> sa0;
+  Stager<LA0, Sh::BM, NA, pair> sa0;
   Stager<LA1, Sh::BM, NA> sa1;
   Stager<LB, Sh::BN, NB> sb;
   const long lda0 = LA0 == kRows ? g.A[0].sa : g.A[0].sk, lda1 = LA1 == kRows ? g.A[1].sa : g.A[1].sk;
@@ -257,7 +269,13 @@ __global__ __launch_bounds__(Sh::threads) void tile_bf16_kernel(Product<bf16_t> 
         return;
       }
     }
-    if (!two || !second) {
+    if (DUAL) {
+      const rsrc_t r0 = make_rsrc(a0 + k), r1 = make_rsrc(a1 + k);
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+        buffer_to_lds16(sa0.other(wave, i) ? r1 : r0, st + sa0.unit_of(wave, i) * 1024,
+                        left < kStep ? sa0.tail(i, wave, lane, left) : sa0.off[i]);
+    } else if (!two || !second) {
       const rsrc_t ra = make_rsrc((second ? a1 : a0) + (LA0 == kRows ? long(k) : long(k) * (second ? lda1 : lda0)));
       if (left < kStep) {
 #pragma unroll
@@ -391,16 +409,18 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
-template <int LA0, int LA1, int LB, class Epi>
+template <int LA0, int LA1, int LB, class Epi, bool DUAL = false>
 __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi, int na, int nb) {
   extern __shared__ __align__(1024) unsigned char smem[];
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef Tile256 Sh;
   constexpr bool two = LA0 != LA1;
+  constexpr int BM = DUAL ? 128 : 256;
+  static_assert(!DUAL || (LA0 == kRows && LA1 == kRows), "two matrices by rows");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tile_a, tile_b;
-  tile_place(blockIdx.x, (na + 255) / 256, (nb + 255) / 256, &tile_a, &tile_b);
-  const int a_first = tile_a * 256, b_first = tile_b * 256;
+  tile_place(blockIdx.x, (na + BM - 1) / BM, (nb + 255) / 256, &tile_a, &tile_b);
+  const int a_first = tile_a * BM, b_first = tile_b * 256;
   if (g.nb) nb = *g.nb;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
   const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
@@ -410,7 +430,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   TileAt at;
   at.wave_a = wave >> 2;
   at.wave_b = wave & 3;
-  at.a0 = a_first + at.wave_a * 128;
+  at.a0 = a_first + at.wave_a * (BM / 2);
   at.b0 = b_first + at.wave_b * 64;
   at.nb = nb;
   at.tile_a = tile_a;
@@ -422,8 +442,10 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   // a half that lies wholly behind the operand's end repeats its last row
   const int n0 = g.A[0].n, n1 = g.A[1].n, nbo = g.B[0].n;
   const int f0 = min(at.a0, LA0 == kRows ? n0 - 1 : (n0 - 1) & ~7), f1 = min(at.a0, LA1 == kRows ? n1 - 1 : (n1 - 1) & ~7);
-  const bf16_t* a0 = g.A[0].p + (LA0 == kRows ? long(f0) * lda0 : long(f0));
+  // DUAL: of a half's 128 rows the first 64, which waves 0 and 1 load, are of A[0]
+  const bf16_t* a0 = (DUAL && w4 >= 2 ? g.A[1].p : g.A[0].p) + (LA0 == kRows ? long(f0) * lda0 : long(f0));
   const bf16_t* a1 = g.A[1].p + (LA1 == kRows ? long(f1) * lda1 : long(f1));
+  const int unit_a = (DUAL ? w4 & 1 : w4) * 4;
   // kRows: from the wave's own 32 rows on, since 256 rows can be longer than a 32-bit offset reaches
   const int bf = LB == kRows ? min(b_first + wave * 32, nbo - 1) : b_first;
   const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(bf) * ldb : long(bf));
@@ -448,7 +470,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
         const int n = second ? n1 - f1 : n0 - f0, vlane = here(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          off_a[i] = unit_offset<LA0, 128>(w4 * 4 + i, vlane, uint32_t(ld * 2), n, left);
+          off_a[i] = unit_offset<LA0, 128>(unit_a + i, vlane, uint32_t(ld * 2), n, left);
       }
     } else {
       rsrc_a = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));
@@ -552,29 +574,31 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
 #endif
 }
 
-template <int LA0, int LA1, int LB, class Epi>
+template <int LA0, int LA1, int LB, bool DUAL = false, class Epi>
 hipError_t launch_tile256(const Product<bf16_t>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
   if (na <= 0 || nb <= 0) return hipSuccess;
-  const unsigned tiles = unsigned((na + 255) / 256) * unsigned((nb + 255) / 256);
+  constexpr int BM = DUAL ? 128 : 256;
+  const unsigned tiles = unsigned((na + BM - 1) / BM) * unsigned((nb + 255) / 256);
   static std::atomic<uint64_t> allowed{0};
   const hipError_t e =
-      allow_lds(reinterpret_cast<const void*>(&tile256_kernel<LA0, LA1, LB, Epi>), Tile256::lds, allowed);
+      allow_lds(reinterpret_cast<const void*>(&tile256_kernel<LA0, LA1, LB, Epi, DUAL>), Tile256::lds, allowed);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((tile256_kernel<LA0, LA1, LB, Epi>), dim3(tiles, unsigned(splits)), dim3(512), Tile256::lds,
+  hipLaunchKernelGGL((tile256_kernel<LA0, LA1, LB, Epi, DUAL>), dim3(tiles, unsigned(splits)), dim3(512), Tile256::lds,
                      stream, g, epi, na, nb);
   return hipGetLastError();
 }
 
-template <class Sh, int LA0, int LA1, int LB, bool ANY, class Epi>
+template <class Sh, int LA0, int LA1, int LB, bool ANY, bool DUAL = false, class Epi>
 hipError_t launch_tile_bf16(const Product<bf16_t>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
   static_assert(!ANY || Sh::S == 2, "register staging is double buffered");
   if (na <= 0 || nb <= 0) return hipSuccess;
-  const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
+  constexpr int BM = DUAL ? Sh::BM / 2 : Sh::BM;
+  const unsigned tiles = unsigned((na + BM - 1) / BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
   static std::atomic<uint64_t> allowed{0};
   const hipError_t e =
-      allow_lds(reinterpret_cast<const void*>(&tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>), Sh::lds, allowed);
+      allow_lds(reinterpret_cast<const void*>(&tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi, DUAL>), Sh::lds, allowed);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads),
+  hipLaunchKernelGGL((tile_bf16_kernel<Sh, LA0, LA1, LB, ANY, Epi, DUAL>), dim3(tiles, unsigned(splits)), dim3(Sh::threads),
                      Sh::lds, stream, g, epi, na, nb);
   return hipGetLastError();
 }
@@ -695,6 +719,19 @@ hipError_t launch_bf16(const Product<bf16_t>& g, const Make& make, int na, int n
         return launch_tile_bf16<Tile128, LA0, LA1, LB, false>(g, make(Tile128()), na, nb, s, stream);
       default: return launch_tile256<LA0, LA1, LB>(g, make(Tile256()), na, nb, s, stream);
     }
+  }
+}
+
+// The same for two matrices of na rows each, whose plan is that of 2 na.
+template <class Make>
+hipError_t launch_bf16_dual(const Product<bf16_t>& g, const Make& make, int na, int nb, Plan plan, hipStream_t stream) {
+  const int s = plan.splits;
+  switch (plan.tile) {
+    case 0: return launch_tile_bf16<Tile16, kRows, kRows, kRows, false, true>(g, make(Tile16()), na, nb, s, stream);
+    case 1: return launch_tile_bf16<Tile32, kRows, kRows, kRows, false, true>(g, make(Tile32()), na, nb, s, stream);
+    case 2: return launch_tile_bf16<Tile64, kRows, kRows, kRows, false, true>(g, make(Tile64()), na, nb, s, stream);
+    case 3: return launch_tile_bf16<Tile128, kRows, kRows, kRows, false, true>(g, make(Tile128()), na, nb, s, stream);
+    default: return launch_tile256<kRows, kRows, kRows, true>(g, make(Tile256()), na, nb, s, stream);
   }
 }
 

@@ -29,12 +29,14 @@ struct TileF32 {
 };
 
 // One operand's step: `ROWS` rows of a by 32 of k, LOADS 16-byte chunks per thread.
-template <int ROWS, int THREADS>
+// PAIR > 0: PAIR rows of o and PAIR of `other` in turn, both by rows.
+template <int ROWS, int THREADS, int PAIR = 0>
 struct StepF32 {
   static constexpr int chunks = ROWS * kStepF32 / 4, loads = (chunks + THREADS - 1) / THREADS;
   f32x4_t v[loads];
 
-  __device__ __forceinline__ void load(const Operand<float>& o, int first, int k0, int K, int tid) {
+  __device__ __forceinline__ void load(const Operand<float>& o, int first, int k0, int K, int tid,
+                                       const float* other = nullptr) {
 #pragma unroll
     for (int i = 0; i < loads; ++i) {
       const int at = tid + i * THREADS;
@@ -42,10 +44,11 @@ struct StepF32 {
       f32x4_t r = {0.f, 0.f, 0.f, 0.f};
       int n;           // values of the chunk that exist
       const float* p;
-      if (o.sk == 1) {
-        const int a = first + at / 8, k = k0 + at % 8 * 4;
+      if (PAIR || o.sk == 1) {
+        const int row = at / 8, k = k0 + at % 8 * 4;
+        const int a = first + (PAIR ? row / (2 * PAIR + !PAIR) * PAIR + row % (PAIR + !PAIR) : row);
         n = a < o.n ? K - k : 0;
-        p = o.p + long(a) * o.sa + k;
+        p = (PAIR && row / (PAIR + !PAIR) % 2 ? other : o.p) + long(a) * o.sa + k;
       } else {
         const int k = k0 + at / (ROWS / 4), a = first + at % (ROWS / 4) * 4;
         n = k < K ? o.n - a : 0;
@@ -89,15 +92,19 @@ __device__ __forceinline__ f32x4_t frag_f32(const float* lds, bool rows, int a, 
   return r;
 }
 
-// grid: x tiles (of b fastest), y splits of the contraction.
-template <class Sh, class Epi>
+// grid: x tiles (of b fastest), y splits of the contraction.  DUAL: the a
+// operand is two matrices of na rows, A[0] and A[1], multiplied by the same b
+// over one contraction; a wave's accumulators i < FM / 2 belong to the first.
+template <class Sh, class Epi, bool DUAL = false>
 __global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g, Epi epi, int na, int nb) {
   extern __shared__ __align__(128) float smem_f32[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_b = (nb + Sh::BN - 1) / Sh::BN;
   if (g.nb) nb = *g.nb;
   const int tile_a = blockIdx.x / tiles_b, tile_b = blockIdx.x % tiles_b;
-  const int a_first = tile_a * Sh::BM, b_first = tile_b * Sh::BN;
+  constexpr int BM = DUAL ? Sh::BM / 2 : Sh::BM;
+  static_assert(!DUAL || Sh::FM % 2 == 0, "two matrices by rows");
+  const int a_first = tile_a * BM, b_first = tile_b * Sh::BN;
   if (b_first >= nb) return;   // all its rows are behind the last one in use
   const int K0 = g.k0 ? *g.k0 : g.K[0], K1 = g.K[1];
   const int T0 = (K0 + kStepF32 - 1) / kStepF32, T = T0 + (K1 + kStepF32 - 1) / kStepF32;
@@ -105,17 +112,17 @@ __global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g,
   TileAt t;
   t.wave_a = wave / Sh::WB;
   t.wave_b = wave % Sh::WB;
-  t.a0 = a_first + t.wave_a * (Sh::BM / Sh::WA);
+  t.a0 = a_first + t.wave_a * (BM / Sh::WA);
   t.b0 = b_first + t.wave_b * (Sh::BN / Sh::WB);
   t.nb = nb;
   t.tile_a = tile_a;
 
-  StepF32<Sh::BM, Sh::threads> sa;
+  StepF32<Sh::BM, Sh::threads, DUAL ? BM / Sh::WA : 0> sa;
   StepF32<Sh::BN, Sh::threads> sb;
   auto load = [&](int s) {
     const int part = s >= T0;
     const int k = (part ? s - T0 : s) * kStepF32, K = part ? K1 : K0;
-    sa.load(g.A[part], a_first, k, K, tid);
+    sa.load(g.A[part], a_first, k, K, tid, g.A[1].p);
     sb.load(g.B[part], b_first, k, K, tid);
   };
   if (t_begin < t_end) load(t_begin);
@@ -156,6 +163,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g,
 using WideF32 = TileF32<128, 128, 2, 2>;
 using MidF32 = TileF32<64, 64, 2, 2>;
 using SlimF32 = TileF32<64, 16, 4, 1>;
+using SlimDualF32 = TileF32<128, 16, 4, 1>;   // two matrices take an even number of fragments
 
 // 0: few rows; 1: too few wide tiles for the compute units; 2: wide.  With a
 // contraction of 1024, wide against narrow, us: 128 tiles 63 against 67, 192
@@ -178,13 +186,14 @@ inline int f32_splits(int na, int nb, long K) {
   return s < 1 ? 1 : s > 64 ? 64 : int(s);
 }
 
-template <class Sh, class Epi>
+template <class Sh, bool DUAL = false, class Epi>
 hipError_t launch_tile_f32(const Product<float>& g, const Epi& epi, int na, int nb, int splits, hipStream_t stream) {
-  const unsigned tiles = unsigned((na + Sh::BM - 1) / Sh::BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
+  constexpr int BM = DUAL ? Sh::BM / 2 : Sh::BM;
+  const unsigned tiles = unsigned((na + BM - 1) / BM) * unsigned((nb + Sh::BN - 1) / Sh::BN);
   static std::atomic<uint64_t> allowed{0};
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&tile_f32_kernel<Sh, Epi>), Sh::lds, allowed);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(&tile_f32_kernel<Sh, Epi, DUAL>), Sh::lds, allowed);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((tile_f32_kernel<Sh, Epi>), dim3(tiles, unsigned(splits)), dim3(Sh::threads), Sh::lds, stream, g,
+  hipLaunchKernelGGL((tile_f32_kernel<Sh, Epi, DUAL>), dim3(tiles, unsigned(splits)), dim3(Sh::threads), Sh::lds, stream, g,
                      epi, na, nb);
   return hipGetLastError();
 }
@@ -197,6 +206,17 @@ hipError_t launch_f32(const Product<float>& g, const Make& make, int na, int nb,
     case 0: return launch_tile_f32<SlimF32>(g, make(SlimF32()), na, nb, splits, stream);
     case 1: return launch_tile_f32<MidF32>(g, make(MidF32()), na, nb, splits, stream);
     default: return launch_tile_f32<WideF32>(g, make(WideF32()), na, nb, splits, stream);
+  }
+}
+
+// The same for two matrices of na rows each, chosen and split as 2 na.
+template <class Make>
+hipError_t launch_f32_dual(const Product<float>& g, const Make& make, int na, int nb, int splits, hipStream_t stream) {
+  if (na <= 0 || nb <= 0) return hipSuccess;
+  switch (f32_choice(2 * na, nb)) {
+    case 0: return launch_tile_f32<SlimDualF32, true>(g, make(SlimDualF32()), na, nb, splits, stream);
+    case 1: return launch_tile_f32<MidF32, true>(g, make(MidF32()), na, nb, splits, stream);
+    default: return launch_tile_f32<WideF32, true>(g, make(WideF32()), na, nb, splits, stream);
   }
 }
 
