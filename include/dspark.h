@@ -788,8 +788,8 @@ size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
  *   h         [T][C] out
  *   last fp32 [S][C] out, or NULL: the state after each sequence's last row
  *                 (h0 of a sequence without rows); may be h0 itself
- *   states fp32 [ceil(T / 32)][C] out, or NULL: the state before each row whose
- *                 index is a multiple of 32, which dspark_recurrence_backward
+ *   states fp32 [ceil(T / 16)][C] out, or NULL: the state before each row whose
+ *                 index is a multiple of 16, which dspark_recurrence_backward
  *                 takes.  Where such a row begins a sequence, or belongs to
  *                 none, its states are left as they were or hold anything.
  *   workspace     >= dspark_recurrence_workspace_bytes(T, S, C, dtype, kind)
@@ -800,7 +800,7 @@ size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
  * execution order, and no sequence's values on another's.
  * Limits: T <= 2^24, S <= 2^20, C <= 65536.
  */
-#define DSPARK_RECURRENCE_BLOCK 32
+#define DSPARK_RECURRENCE_BLOCK 16
 dspark_status dspark_recurrence(
     int T, int S, int C, dspark_dtype dtype, dspark_gate kind, const int32_t* offsets, const void* x,
     const void* gate, const float* h0, void* h, float* last, float* states,
@@ -819,7 +819,7 @@ size_t dspark_recurrence_workspace_bytes(int T, int S, int C, dspark_dtype dtype
  * Arguments: sizes, types, offsets and inputs as dspark_recurrence, and
  *   dh         [T][C]
  *   dlast fp32 [S][C] or NULL (zeros)
- *   states fp32 [ceil(T / 32)][C] as dspark_recurrence wrote it
+ *   states fp32 [ceil(T / 16)][C] as dspark_recurrence wrote it
  *   dx [T][C] out, dgate [T][C] in the storage type (SIGMOID) or fp32 [C]
  *                 (DECAY) out, dh0 fp32 [S][C] out; each may be NULL: not
  *                 computed (all three: nothing is enqueued).  dh0 may be dlast

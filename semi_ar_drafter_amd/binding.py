@@ -973,7 +973,7 @@ def norm_backward(dy, x, stat, weight=None, dsum=None, kind: str = "layer", need
 
 
 GATES = {"sigmoid": 0, "decay": 1}
-RECURRENCE_BLOCK = 32     # rows from one kept state to the next
+RECURRENCE_BLOCK = 16     # rows from one kept state to the next
 
 
 def _recurrence_inputs(x, gate, kind, offsets, sequences, h0):

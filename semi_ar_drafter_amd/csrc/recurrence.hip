@@ -10,7 +10,7 @@
 //
 // The state is fp32 throughout; the rounding of h to the storage type is of
 // the output alone.  The gradient makes h_{t-1} again from the inputs, block
-// by block of 32 rows, from the fp32 states that the forward pass kept.
+// by block of 16 rows, from the fp32 states that the forward pass kept.
 #include "launch.h"
 #include "projection.h"
 
@@ -18,7 +18,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kBlock = 32;   // rows from one kept state to the next
+constexpr int kBlock = 16;   // rows from one kept state to the next
 
 // Two neighbouring channels of a row, as stored, at element alignment.
 template <typename T> struct Pair;
@@ -54,26 +54,22 @@ __device__ __forceinline__ void store2(T* p, float a, float b, bool both) {
   }
 }
 
-// a = 1 / (1 + exp(-g)) and 1 - a, each to its own relative accuracy: by
-// exp(-|g|), so that nothing cancels for gates near 1.  An error of a is
-// multiplied by the number of rows that a state lives, and states are fp32
-// for both types: the reciprocal gets a Newton step.
+// a = 1 / (1 + exp(-g)) and 1 - a = exp(-g) a, each to its own relative accuracy:
+// nothing cancels for gates near 1.  exp(-g) is held below 2^120, so that the
+// product with a = 2^-120 stays 1; minimum() passes NaN on.  For bf16 logits by
+// the hardware's base-2 exponential and reciprocal (one unit in the last place
+// each: a is off by 2^-23, which a state multiplies by the rows that it lives).
 template <typename T>
 __device__ __forceinline__ void gate_of(float g, float* a, float* rest) {
-  float e, r;
   if constexpr (sizeof(T) == 4) {
-    e = expf(-fabsf(g));
-    r = 1.f / (1.f + e);
+    const float e = expf(__builtin_elementwise_minimum(-g, 83.f));
+    *a = 1.f / (1.f + e);
+    *rest = e * *a;
   } else {
-    e = __expf(-fabsf(g));
-    const float d = 1.f + e;
-    r = __builtin_amdgcn_rcpf(d);
-    r = fmaf(r, fmaf(-d, r, 1.f), r);
+    const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(g * -1.44269504088896341f, 120.f));
+    *a = __builtin_amdgcn_rcpf(1.f + e);
+    *rest = e * *a;
   }
-  const float small = e * r;
-  *a = g >= 0.f ? r : small;
-  *rest = g >= 0.f ? small : r;
-  if (g != g) *a = *rest = g;
 }
 
 // First and last row (exclusive) of sequence s.
@@ -249,24 +245,26 @@ __global__ __launch_bounds__(256) void gate_join_kernel(int C, int units, const 
 // ---------------------------------------------------------------------------
 // Long sequences: the rows are split into tiles as well
 // ---------------------------------------------------------------------------
-// A tile is W waves of 32 rows by 128 channels, read once and kept in
+// A tile is W waves of 16 rows by 128 channels, read once and kept in
 // registers.  What rows do to the state before them is h -> A h + B; a wave
-// makes its (A, B), LDS joins the waves', and the tile's is published.  The
-// state before the tile is then the fold, in order, of the published pairs
-// since the last kept state; every kGroup-th tile publishes the state behind
-// it, so that no fold is longer than kGroup and the tiles wait for one another
-// once in kGroup only.  The order of all sums is fixed: results do not depend
-// on which tile comes first.
+// makes its (A, B), LDS joins the waves', and the tile's pair is published.
+// Every kSub-th tile publishes the pair of the last kSub, and every kGroup-th
+// the state behind it; a tile folds, in order, the last such state, the pairs
+// of kSub tiles since then and the single ones since then: 14 words at most,
+// and the tiles wait for one another in a row once in kGroup only.  The order
+// of all sums is fixed: results do not depend on which tile comes first.
 //
-// A tile takes its number (rows first, then channels) from a counter, so
+// A tile takes its number along the rows from a counter of its channels, so
 // that every tile it waits for belongs to a workgroup that is already running
-// and itself waits for lower numbers only.
+// and itself waits for lower numbers only.  (One counter for all channels
+// hands out a number every 56 ns: 10240 tiles then took 577 us.)
 //
 // Where a sequence begins, A = 0 and B holds what its h0 gives: join() then
 // ignores the state before, whatever it is.
-constexpr int kGroup = 16;
+constexpr int kSub = 8, kGroup = 64;
 constexpr int kSpin = 1 << 22;   // polls of a few hundred nanoseconds; a state not seen by then is NaN
 constexpr uint64_t kEmpty = ~uint64_t(0);
+constexpr int kLine = 32;   // 32-bit words
 
 __device__ __forceinline__ float join(float a, float b, float before) {
   return a == 0.f || before == 0.f ? b : fmaf(a, before, b);
@@ -286,11 +284,13 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* at) {
 
 // What the tiles share in the workspace.
 struct TileSpace {
-  uint32_t* ctrl;    // the counter, and the first row and the row behind the last one of any sequence
-  uint2* marks;      // per 32 rows: which begin, and which end, a sequence
+  uint32_t* ctrl;    // the first row of any sequence, and the row behind the last one
+  uint32_t* tickets; // a counter per 128 channels, each in a line of its own
+  uint32_t* marks;   // per 16 rows: which begin (low half), and which end (high half), a sequence
   int32_t* owner;    // of the marked rows: their sequence
   uint64_t* pairs;   // [tiles along the rows][C]
-  uint64_t* kept;    // [groups][C]: the state before the group, as B
+  uint64_t* subs;    // [kSub tiles][C]
+  uint64_t* kept;    // [kGroup tiles][C]: the state before the group, as B
 };
 
 // Before the tiles: counter, marks, empty words, and the ends of sequences
@@ -299,15 +299,15 @@ __global__ __launch_bounds__(256) void tile_setup_kernel(Sequences seq, int S, i
                                                          const float* from, float* to) {
   const int tid = blockIdx.x * 256 + threadIdx.x, all = gridDim.x * 256;
   if (tid == 0) {
-    ws.ctrl[0] = 0;
-    ws.ctrl[1] = seq.begin(0);
-    ws.ctrl[2] = seq.end(S - 1);
+    ws.ctrl[0] = seq.begin(0);
+    ws.ctrl[1] = seq.end(S - 1);
   }
-  for (size_t i = tid; i < words; i += all) ws.pairs[i] = kEmpty;   // kept lies behind pairs
+  for (int i = tid; i < (C + 127) / 128; i += all) ws.tickets[i * kLine] = 0;
+  for (size_t i = tid; i < words; i += all) ws.pairs[i] = kEmpty;   // subs and kept lie behind pairs
   for (int k = tid; k < (seq.T + kBlock - 1) / kBlock; k += all) {
     const int t0 = k * kBlock;
-    uint2 m = {0u, 0u};
-    // the first sequence that ends behind t0 and those that begin or end in the block
+    uint32_t m = 0u;
+    // the first sequence that ends behind t0, and those from it on that begin or end in the block
     int lo = 0, hi = S;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -321,11 +321,11 @@ __global__ __launch_bounds__(256) void tile_setup_kernel(Sequences seq, int S, i
       if (b >= t0 + kBlock) break;
       if (b >= e) continue;
       if (b >= t0) {
-        m.x |= 1u << (b - t0);
+        m |= 1u << (b - t0);
         ws.owner[b] = s;
       }
       if (e > t0 && e <= t0 + kBlock) {
-        m.y |= 1u << (e - 1 - t0);
+        m |= 0x10000u << (e - 1 - t0);
         ws.owner[e - 1] = s;
       }
     }
@@ -337,286 +337,389 @@ __global__ __launch_bounds__(256) void tile_setup_kernel(Sequences seq, int S, i
       for (int c = threadIdx.x; c < C; c += 256) to[size_t(s) * C + c] = from ? from[size_t(s) * C + c] : 0.f;
 }
 
-// The state before tile number k (in the order of the recurrence): what the
-// words of two channels from `at` on fold to.
-__device__ __forceinline__ void fold_before(const TileSpace& ws, int k, int C, int c, bool live, bool both, float* v0,
-                                            float* v1) {
-  const int group = k / kGroup, first = group * kGroup, n = k - first;
-  uint64_t kept0 = 0, kept1 = 0, w0[kGroup], w1[kGroup];
-  *v0 = *v1 = 0.f;
-  if (k == 0) return;
-  const uint64_t* pk = ws.kept + size_t(group) * C + c;
-  const uint64_t* pw = ws.pairs + size_t(first) * C + c;
-  bool ready = false;
-  for (int spin = 0; spin < kSpin; ++spin) {
-    ready = true;
-    if (live) {
-      if (group > 0) {
-        kept0 = peek(pk);
-        kept1 = both ? peek(pk + 1) : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kGroup - 1; ++j)
-        if (j < n) {
-          w0[j] = peek(pw + size_t(j) * C);
-          w1[j] = both ? peek(pw + size_t(j) * C + 1) : 0;
-        }
-      ready = kept0 != kEmpty && kept1 != kEmpty;
-#pragma unroll
-      for (int j = 0; j < kGroup - 1; ++j)
-        if (j < n) ready = ready && w0[j] != kEmpty && w1[j] != kEmpty;
-    }
-    if (__all(ready)) break;
-    __builtin_amdgcn_s_sleep(1);
-  }
-  if (!live) return;
-  if (!ready) {
-    *v0 = *v1 = __uint_as_float(0x7FC00000u);
-    return;
-  }
-  *v0 = __uint_as_float(uint32_t(kept0));
-  *v1 = __uint_as_float(uint32_t(kept1));
-#pragma unroll
-  for (int j = 0; j < kGroup - 1; ++j)
-    if (j < n) {
-      *v0 = join(__uint_as_float(uint32_t(w0[j] >> 32)), __uint_as_float(uint32_t(w0[j])), *v0);
-      *v1 = join(__uint_as_float(uint32_t(w1[j] >> 32)), __uint_as_float(uint32_t(w1[j])), *v1);
-    }
+// One lane's two channels of a word in LDS: (A, B) of both.
+__device__ __forceinline__ float4 wide(uint64_t w0, uint64_t w1) {
+  return make_float4(__uint_as_float(uint32_t(w0 >> 32)), __uint_as_float(uint32_t(w0)),
+                     __uint_as_float(uint32_t(w1 >> 32)), __uint_as_float(uint32_t(w1)));
 }
-
-// The waves' pairs, in the order of the recurrence, to the state before each
-// of them: wave 0 of the workgroup publishes the tile's pair, waits for the
-// state before the tile, and publishes the state behind it where a group ends.
-template <int W>
-__device__ __forceinline__ void waves_before(const TileSpace& ws, const float4 (&pairs)[W][64], float2 (&before)[W][64],
-                                             int k, int tiles, int C, int c, bool live, bool both, int lane) {
-  float a0 = 1.f, a1 = 1.f, b0 = 0.f, b1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const float4 p = pairs[w][lane];
+struct State2 {
+  float v0, v1;
+  __device__ __forceinline__ void behind(const float4& p) {
+    v0 = join(p.x, p.y, v0);
+    v1 = join(p.z, p.w, v1);
+  }
+};
+struct Pair2 {
+  float a0 = 1.f, b0 = 0.f, a1 = 1.f, b1 = 0.f;
+  __device__ __forceinline__ void behind(const float4& p) {
     b0 = join(p.x, p.y, b0);
     a0 = join_factor(p.x, a0);
     b1 = join(p.z, p.w, b1);
     a1 = join_factor(p.z, a1);
   }
-  if (live) {
-    uint64_t* at = ws.pairs + size_t(k) * C + c;
+  __device__ __forceinline__ void to(uint64_t* at, bool both) const {
     publish(at, a0, b0);
     if (both) publish(at + 1, a1, b1);
   }
-  float v0, v1;
-  fold_before(ws, k, C, c, live, both, &v0, &v1);
-  if (k % kGroup == kGroup - 1 && k + 1 < tiles && live) {
-    uint64_t* at = ws.kept + size_t(k / kGroup + 1) * C + c;
-    publish(at, 0.f, join(a0, b0, v0));
-    if (both) publish(at + 1, 0.f, join(a1, b1, v1));
+};
+
+// A tile's shared memory: its waves' pairs, and the words of the tiles before.
+template <int W>
+struct TileLds {
+  float4 pairs[W][64];
+  float4 words[2 * kSub - 1][64];   // of kSub tiles each, of single tiles, and the kept state
+};
+
+// The state before this wave's rows.  k: the tile's number, waves and tiles
+// counted in the order of the recurrence; the waves' pairs are in lds.
+template <int W>
+__device__ __forceinline__ State2 state_before(TileLds<W>& lds, const TileSpace& ws, int k, int tiles, int C, int c,
+                                               bool live, bool both, int wave, int lane) {
+  __syncthreads();
+  const int singles = k % kSub, subs = k % kGroup / kSub, group = k / kGroup;
+  if (wave == 0 && live) {
+    Pair2 p;
+#pragma unroll
+    for (int w = 0; w < W; ++w) p.behind(lds.pairs[w][lane]);
+    p.to(ws.pairs + size_t(k) * C + c, both);
+  }
+  // the waves share the words between them
+  constexpr int N = 2 * kSub - 1, per = (N + W - 1) / W;
+  const uint64_t* at[per];   // row of words, or null
+  uint64_t w0[per], w1[per];
+#pragma unroll
+  for (int i = 0; i < per; ++i) {
+    const int j = wave + i * W;
+    at[i] = nullptr;
+    if (j < kSub - 1) {
+      if (j < subs) at[i] = ws.subs + size_t(group * (kGroup / kSub) + j) * C;
+    } else if (j < N - 1) {
+      if (j - (kSub - 1) < singles) at[i] = ws.pairs + size_t(k - singles + j - (kSub - 1)) * C;
+    } else if (j == N - 1) {
+      if (group > 0) at[i] = ws.kept + size_t(group) * C;
+    }
+  }
+  bool ready = false;
+  for (int spin = 0; spin < kSpin; ++spin) {
+    // all lanes look at one word: a thousand waves that read all of theirs over
+    // and over would take the memory's whole bandwidth
+    bool some = true;
+#pragma unroll
+    for (int i = 0; i < per; ++i)
+      if (at[i]) some = some && peek(at[i] + (c - 2 * lane)) != kEmpty;
+    if (__all(some)) {
+      ready = true;
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+          if (at[i]) {
+            w0[i] = peek(at[i] + c);
+            w1[i] = both ? peek(at[i] + c + 1) : 0;
+          }
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+          if (at[i]) ready = ready && w0[i] != kEmpty && w1[i] != kEmpty;
+      }
+      if (__all(ready)) break;
+    }
+    __builtin_amdgcn_s_sleep(2);
   }
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    before[w][lane] = make_float2(v0, v1);
-    const float4 p = pairs[w][lane];
-    v0 = join(p.x, p.y, v0);
-    v1 = join(p.z, p.w, v1);
+  for (int i = 0; i < per; ++i) {
+    const int j = wave + i * W;
+    // what never came is NaN
+    if (at[i]) lds.words[j][lane] = ready ? wide(w0[i], w1[i]) : wide(0x7FC000007FC00000ull, 0x7FC000007FC00000ull);
   }
+  __syncthreads();
+  if (wave == 0 && live && singles == kSub - 1) {
+    Pair2 p;
+    for (int j = 0; j < kSub - 1; ++j) p.behind(lds.words[kSub - 1 + j][lane]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) p.behind(lds.pairs[w][lane]);
+    p.to(ws.subs + size_t(k / kSub) * C + c, both);
+  }
+  State2 v = {0.f, 0.f};
+  if (group > 0) {
+    const float4 p = lds.words[N - 1][lane];
+    v = {p.y, p.w};
+  }
+  for (int j = 0; j < subs; ++j) v.behind(lds.words[j][lane]);
+  for (int j = 0; j < singles; ++j) v.behind(lds.words[kSub - 1 + j][lane]);
+  for (int w = 0; w < wave; ++w) v.behind(lds.pairs[w][lane]);
+  if (wave == W - 1 && live && k % kGroup == kGroup - 1 && k + 1 < tiles) {
+    State2 end = v;
+    end.behind(lds.pairs[W - 1][lane]);
+    uint64_t* to = ws.kept + size_t(group + 1) * C + c;
+    publish(to, 0.f, end.v0);
+    if (both) publish(to + 1, 0.f, end.v1);
+  }
+  return v;
 }
 
-// The tile that this workgroup takes next: its number along the rows, and its
-// first channel.
-__device__ __forceinline__ void take_tile(const TileSpace& ws, int blocks, int* k, int* c0) {
+// The tile that this workgroup takes: its number along the rows, and its first channel.
+__device__ __forceinline__ void take_tile(const TileSpace& ws, int C, int* k, int* c0) {
   __shared__ uint32_t ticket;
+  const int block = blockIdx.x % ((C + 127) / 128);
   if (threadIdx.x == 0)
-    ticket = __hip_atomic_fetch_add(ws.ctrl, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    ticket = __hip_atomic_fetch_add(ws.tickets + block * kLine, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  const uint32_t t = __builtin_amdgcn_readfirstlane(ticket);
-  *k = int(t / blocks);
-  *c0 = int(t % blocks) * 128;
+  *k = int(__builtin_amdgcn_readfirstlane(ticket));
+  *c0 = block * 128;
+}
+
+// A wave's rows of a tile: those from lo to hi - 1 of 16 belong to a sequence.
+struct Rows {
+  int block, t0, lo, hi;
+  uint32_t marks;
+  bool whole;   // all 16, none of them the first or last of a sequence
+  __device__ __forceinline__ void init(const TileSpace& ws, int b) {
+    block = b;
+    t0 = b * kBlock;
+    lo = __builtin_amdgcn_readfirstlane(max(int(ws.ctrl[0]) - t0, 0));
+    hi = __builtin_amdgcn_readfirstlane(min(int(ws.ctrl[1]) - t0, kBlock));
+    marks = hi > lo ? __builtin_amdgcn_readfirstlane(ws.marks[b]) : 0u;
+    whole = lo == 0 && hi == kBlock && marks == 0u;
+  }
+  __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+  __device__ __forceinline__ bool begins(int i) const { return marks >> i & 1; }
+  __device__ __forceinline__ bool ends(int i) const { return marks >> (16 + i) & 1; }
+};
+
+// Two values by sequence (of the marked row i): v[owner][c] and its neighbour, or 0.
+__device__ __forceinline__ State2 of_sequence(const float* v, const TileSpace& ws, const Rows& r, int i, int C, int c,
+                                              bool both) {
+  if (!v) return {0.f, 0.f};
+  const float* p = v + size_t(ws.owner[r.t0 + i]) * C + c;
+  return {p[0], both ? p[1] : 0.f};
 }
 
 template <typename T, bool SIGMOID, int W>
-__global__ __launch_bounds__(64 * W) void tile_kernel(TileSpace ws, int tiles, int C, const T* __restrict__ x,
+__global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles, int C, const T* __restrict__ x,
                                                       const void* __restrict__ gate, const float* h0, T* __restrict__ h,
                                                       float* last, float* __restrict__ states) {
-  __shared__ float4 pairs[W][64];
-  __shared__ float2 before[W][64];
+  __shared__ TileLds<W> lds;
   int k, c0;
-  take_tile(ws, (C + 127) / 128, &k, &c0);
+  take_tile(ws, C, &k, &c0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = c0 + 2 * lane, block = k * W + wave, t0 = block * kBlock;
+  const int c = c0 + 2 * lane;
   const bool live = c < C, both = c + 1 < C;
-  const int lo = max(int(ws.ctrl[1]) - t0, 0), hi = min(int(ws.ctrl[2]) - t0, kBlock);   // this wave's rows
+  Rows r;
+  r.init(ws, k * W + wave);
   const T* gates = static_cast<const T*>(gate);
-  Pair<T> px[kBlock], pg[kBlock];
-  uint2 marks = {0u, 0u};
-  float a0 = 0.f, a1 = 0.f, A0 = 1.f, A1 = 1.f, s0 = 0.f, s1 = 0.f;
-  if (hi > lo) {
-    marks = ws.marks[block];
-    if (live) {
+  float decay0 = 0.f, decay1 = 0.f;
+  if (!SIGMOID && live) {
+    decay0 = static_cast<const float*>(gate)[c];
+    decay1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
+  }
+  // a row: state -> a state + b; one that is not there changes nothing, and the
+  // first of a sequence (a = 0, b from its h0) forgets what was before
+  float a0[kBlock], a1[kBlock], b0[kBlock], b1[kBlock];
+  Pair2 p;
+  if (live) {
+    Pair<T> px[kBlock], pg[kBlock];
+    auto load = [&](int i) {
+      const size_t at = size_t(r.t0 + i) * C + c;
+      px[i].load(x + at, both);
+      if (SIGMOID) pg[i].load(gates + at, both);
+    };
+    auto make = [&](int i) {
+      b0[i] = px[i].get(0);
+      b1[i] = px[i].get(1);
+      a0[i] = decay0;
+      a1[i] = decay1;
+      if (SIGMOID) {
+        float r0, r1;
+        gate_of<T>(pg[i].get(0), &a0[i], &r0);
+        gate_of<T>(pg[i].get(1), &a1[i], &r1);
+        b0[i] *= r0;
+        b1[i] *= r1;
+      }
+    };
+    if (r.whole) {
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) load(i);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) {
+        make(i);
+        p.b0 = fmaf(a0[i], p.b0, b0[i]);
+        p.b1 = fmaf(a1[i], p.b1, b1[i]);
+        p.a0 *= a0[i];
+        p.a1 *= a1[i];
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < kBlock; ++i)
-        if (i >= lo && i < hi) {
-          const size_t at = size_t(t0 + i) * C + c;
-          px[i].load(x + at, both);
-          if (SIGMOID) pg[i].load(gates + at, both);
+        if (r.has(i)) load(i);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) {
+        a0[i] = a1[i] = 1.f;
+        b0[i] = b1[i] = 0.f;
+        if (r.has(i)) {
+          make(i);
+          if (r.begins(i)) {
+            const State2 v = of_sequence(h0, ws, r, i, C, c, both);
+            b0[i] = fmaf(a0[i], v.v0, b0[i]);
+            b1[i] = fmaf(a1[i], v.v1, b1[i]);
+            a0[i] = a1[i] = 0.f;
+          }
         }
-      if (!SIGMOID) {
-        a0 = static_cast<const float*>(gate)[c];
-        a1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
+        p.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
       }
     }
   }
-  // one row: the state behind it from the one before it
-  auto step = [&](int i) {
-    float b0 = px[i].get(0), b1 = px[i].get(1);
-    if (SIGMOID) {
-      float r0, r1;
-      gate_of<T>(pg[i].get(0), &a0, &r0);
-      gate_of<T>(pg[i].get(1), &a1, &r1);
-      b0 *= r0;
-      b1 *= r1;
+  lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
+  State2 v = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);
+  if (!live || r.hi <= r.lo) return;
+  if (states) store2(states + size_t(r.block) * C + c, v.v0, v.v1, both);
+  T* out = h + size_t(r.t0) * C + c;
+  if (r.whole) {
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) {
+      v.v0 = fmaf(a0[i], v.v0, b0[i]);
+      v.v1 = fmaf(a1[i], v.v1, b1[i]);
+      store2(out + size_t(i) * C, v.v0, v.v1, both);
     }
-    if (marks.x >> i & 1) {
-      const float* p = h0 ? h0 + size_t(ws.owner[t0 + i]) * C + c : nullptr;
-      s0 = p ? p[0] : 0.f;
-      s1 = p && both ? p[1] : 0.f;
-      A0 = A1 = 0.f;
-    }
-    s0 = fmaf(a0, s0, b0);
-    s1 = fmaf(a1, s1, b1);
-    A0 = join_factor(A0, a0);
-    A1 = join_factor(A1, a1);
-  };
-  if (live) {
+  } else {
 #pragma unroll
     for (int i = 0; i < kBlock; ++i)
-      if (i >= lo && i < hi) step(i);
+      if (r.has(i)) {
+        v.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
+        store2(out + size_t(i) * C, v.v0, v.v1, both);
+        if (last && r.ends(i)) store2(last + size_t(ws.owner[r.t0 + i]) * C + c, v.v0, v.v1, both);
+      }
   }
-  pairs[wave][lane] = make_float4(A0, s0, A1, s1);
-  __syncthreads();
-  if (wave == 0) waves_before<W>(ws, pairs, before, k, tiles, C, c, live, both, lane);
-  __syncthreads();
-  if (!live || hi <= lo) return;
-  s0 = before[wave][lane].x;
-  s1 = before[wave][lane].y;
-  if (states) store2(states + size_t(block) * C + c, s0, s1, both);
-#pragma unroll
-  for (int i = 0; i < kBlock; ++i)
-    if (i >= lo && i < hi) {
-      step(i);
-      store2(h + size_t(t0 + i) * C + c, s0, s1, both);
-      if (last && (marks.y >> i & 1)) store2(last + size_t(ws.owner[t0 + i]) * C + c, s0, s1, both);
-    }
 }
 
 // Backwards: tiles, waves and rows in the other order; what passes from row to
-// row is e = a d.
+// row is e = a d, e -> a (dh + e).
 template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
     TileSpace ws, int tiles, int C, const T* __restrict__ dh, const T* __restrict__ x, const void* __restrict__ gate,
     const float* __restrict__ h0, const float* dlast, const float* __restrict__ states, T* __restrict__ dx,
     T* __restrict__ dg, float* dh0, float* __restrict__ part) {
-  __shared__ float4 pairs[W][64];
-  __shared__ float2 before[W][64];
+  __shared__ TileLds<W> lds;
   int k, c0;
-  take_tile(ws, (C + 127) / 128, &k, &c0);
+  take_tile(ws, C, &k, &c0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = c0 + 2 * lane, block = (tiles - 1 - k) * W + W - 1 - wave, t0 = block * kBlock;
+  const int c = c0 + 2 * lane;
   const bool live = c < C, both = c + 1 < C;
-  const int lo = max(int(ws.ctrl[1]) - t0, 0), hi = min(int(ws.ctrl[2]) - t0, kBlock);   // this wave's rows
+  Rows r;
+  r.init(ws, (tiles - 1 - k) * W + W - 1 - wave);
   const T* gates = static_cast<const T*>(gate);
-  Pair<T> px[kBlock], pg[kBlock], pd[kBlock];
-  float h_0[kBlock], h_1[kBlock];   // the state before each row
-  uint2 marks = {0u, 0u};
-  float a0 = 0.f, a1 = 0.f, r0 = 0.f, r1 = 0.f, A0 = 1.f, A1 = 1.f, e0 = 0.f, e1 = 0.f, d0 = 0.f, d1 = 0.f;
-  auto gates_of = [&](int i) {
-    if (SIGMOID) {
-      gate_of<T>(pg[i].get(0), &a0, &r0);
-      gate_of<T>(pg[i].get(1), &a1, &r1);
-    }
-  };
-  if (hi > lo) {
-    marks = ws.marks[block];
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < kBlock; ++i)
-        if (i >= lo && i < hi) {
-          const size_t at = size_t(t0 + i) * C + c;
-          px[i].load(x + at, both);
-          if (SIGMOID) pg[i].load(gates + at, both);
-          pd[i].load(dh + at, both);
-        }
-      if (!SIGMOID) {
-        a0 = static_cast<const float*>(gate)[c];
-        a1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
+  float decay0 = 0.f, decay1 = 0.f;
+  if (!SIGMOID && live) {
+    decay0 = static_cast<const float*>(gate)[c];
+    decay1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
+  }
+  // a row's gate, what dx is of d (1 - a) and what dgate is of it (SIGMOID:
+  // a (1 - a) (h before - x), DECAY: h before)
+  float a0[kBlock], a1[kBlock], r0[kBlock], r1[kBlock], w0[kBlock], w1[kBlock];
+  Pair<T> pd[kBlock];
+  Pair2 p;
+  auto gate0 = [&](int i) { return SIGMOID ? a0[i] : decay0; };
+  auto gate1 = [&](int i) { return SIGMOID ? a1[i] : decay1; };
+  if (live && r.hi > r.lo) {
+    Pair<T> px[kBlock], pg[kBlock];
+    auto load = [&](int i) {
+      const size_t at = size_t(r.t0 + i) * C + c;
+      px[i].load(x + at, both);
+      if (SIGMOID) pg[i].load(gates + at, both);
+      pd[i].load(dh + at, both);
+    };
+    const float* from = states + size_t(r.block) * C + c;
+    State2 v = {from[0], both ? from[1] : 0.f};
+    auto make = [&](int i) {   // v: the state before the row, then behind it
+      const float x0 = px[i].get(0), x1 = px[i].get(1);
+      if (SIGMOID) {
+        gate_of<T>(pg[i].get(0), &a0[i], &r0[i]);
+        gate_of<T>(pg[i].get(1), &a1[i], &r1[i]);
+        w0[i] = a0[i] * (v.v0 - x0);
+        w1[i] = a1[i] * (v.v1 - x1);
+        v = {fmaf(a0[i], v.v0, r0[i] * x0), fmaf(a1[i], v.v1, r1[i] * x1)};
+      } else {
+        w0[i] = v.v0;
+        w1[i] = v.v1;
+        v = {fmaf(decay0, v.v0, x0), fmaf(decay1, v.v1, x1)};
       }
-      float s0 = states[size_t(block) * C + c], s1 = both ? states[size_t(block) * C + c + 1] : 0.f;
+    };
+    if (r.whole) {
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) load(i);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) make(i);
+#pragma unroll
+      for (int i = kBlock - 1; i >= 0; --i) {
+        p.b0 = gate0(i) * (pd[i].get(0) + p.b0);
+        p.b1 = gate1(i) * (pd[i].get(1) + p.b1);
+        p.a0 *= gate0(i);
+        p.a1 *= gate1(i);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < kBlock; ++i)
-        if (i >= lo && i < hi) {
-          if (marks.x >> i & 1) {
-            const float* p = h0 ? h0 + size_t(ws.owner[t0 + i]) * C + c : nullptr;
-            s0 = p ? p[0] : 0.f;
-            s1 = p && both ? p[1] : 0.f;
+        if (r.has(i)) load(i);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i)
+        if (r.has(i)) {
+          if (r.begins(i)) v = of_sequence(h0, ws, r, i, C, c, both);
+          make(i);
+        }
+#pragma unroll
+      for (int i = kBlock - 1; i >= 0; --i)
+        if (r.has(i)) {
+          if (r.ends(i)) {
+            const State2 e = of_sequence(dlast, ws, r, i, C, c, both);
+            p.a0 = p.a1 = 0.f;
+            p.b0 = e.v0;
+            p.b1 = e.v1;
           }
-          h_0[i] = s0;
-          h_1[i] = s1;
-          gates_of(i);
-          s0 = fmaf(a0, s0, SIGMOID ? r0 * px[i].get(0) : px[i].get(0));
-          s1 = fmaf(a1, s1, SIGMOID ? r1 * px[i].get(1) : px[i].get(1));
+          p.b0 = gate0(i) * (pd[i].get(0) + p.b0);
+          p.b1 = gate1(i) * (pd[i].get(1) + p.b1);
+          p.a0 = join_factor(p.a0, gate0(i));
+          p.a1 = join_factor(p.a1, gate1(i));
         }
     }
   }
-  auto step = [&](int i) {
-    if (marks.y >> i & 1) {
-      const float* p = dlast ? dlast + size_t(ws.owner[t0 + i]) * C + c : nullptr;
-      e0 = p ? p[0] : 0.f;
-      e1 = p && both ? p[1] : 0.f;
-      A0 = A1 = 0.f;
-    }
-    gates_of(i);
-    d0 = pd[i].get(0) + e0;
-    d1 = pd[i].get(1) + e1;
-    e0 = a0 * d0;
-    e1 = a1 * d1;
-    A0 = join_factor(A0, a0);
-    A1 = join_factor(A1, a1);
-  };
-  if (live) {
-#pragma unroll
-    for (int i = kBlock - 1; i >= 0; --i)
-      if (i >= lo && i < hi) step(i);
-  }
-  pairs[wave][lane] = make_float4(A0, e0, A1, e1);
-  __syncthreads();
-  if (wave == 0) waves_before<W>(ws, pairs, before, k, tiles, C, c, live, both, lane);
-  __syncthreads();
-  e0 = before[wave][lane].x;
-  e1 = before[wave][lane].y;
+  lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
+  State2 e = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);
   float sum0 = 0.f, sum1 = 0.f;
   if (live) {
-#pragma unroll
-    for (int i = kBlock - 1; i >= 0; --i)
-      if (i >= lo && i < hi) {
-        step(i);
-        const size_t at = size_t(t0 + i) * C + c;
-        if (SIGMOID) {
-          if (dx) store2(dx + at, d0 * r0, d1 * r1, both);
-          if (dg) store2(dg + at, d0 * r0 * (a0 * (h_0[i] - px[i].get(0))), d1 * r1 * (a1 * (h_1[i] - px[i].get(1))), both);
-        } else {
-          if (dx) store2(dx + at, d0, d1, both);
-          sum0 = fmaf(d0, h_0[i], sum0);
-          sum1 = fmaf(d1, h_1[i], sum1);
-        }
-        if (dh0 && (marks.x >> i & 1)) store2(dh0 + size_t(ws.owner[t0 + i]) * C + c, e0, e1, both);
+    auto row = [&](int i) {
+      const float d0 = pd[i].get(0) + e.v0, d1 = pd[i].get(1) + e.v1;
+      const size_t at = size_t(r.t0 + i) * C + c;
+      if (SIGMOID) {
+        const float u0 = d0 * r0[i], u1 = d1 * r1[i];
+        if (dx) store2(dx + at, u0, u1, both);
+        if (dg) store2(dg + at, u0 * w0[i], u1 * w1[i], both);
+      } else {
+        if (dx) store2(dx + at, d0, d1, both);
+        sum0 = fmaf(d0, w0[i], sum0);
+        sum1 = fmaf(d1, w1[i], sum1);
       }
+      e = {gate0(i) * d0, gate1(i) * d1};
+    };
+    if (r.whole) {
+#pragma unroll
+      for (int i = kBlock - 1; i >= 0; --i) row(i);
+    } else {
+#pragma unroll
+      for (int i = kBlock - 1; i >= 0; --i)
+        if (r.has(i)) {
+          if (r.ends(i)) e = of_sequence(dlast, ws, r, i, C, c, both);
+          row(i);
+          if (dh0 && r.begins(i)) store2(dh0 + size_t(ws.owner[r.t0 + i]) * C + c, e.v0, e.v1, both);
+        }
+    }
   }
   if (SIGMOID || !part) return;
-  before[wave][lane] = make_float2(sum0, sum1);   // each lane overwrites what it alone has read
+  __syncthreads();   // the waves' pairs have been read
+  lds.pairs[wave][lane] = make_float4(sum0, sum1, 0.f, 0.f);
   __syncthreads();
   if (wave == 0 && live) {
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-      sum0 += before[w][lane].x;
-      sum1 += before[w][lane].y;
+      sum0 += lds.pairs[w][lane].x;
+      sum1 += lds.pairs[w][lane].y;
     }
     store2(part + size_t(k) * C + c, sum0, sum1, both);
   }
@@ -632,26 +735,31 @@ bool tiled(int T, int S) { return T >= 128 * long(S); }
 // Offsets of TileSpace's parts, and of dgate's shares behind them.
 struct TileLayout {
   int tiles;
-  size_t marks, owner, pairs, kept, part, total, words;
+  size_t tickets, marks, owner, pairs, subs, kept, part, total, words;
 };
 TileLayout tile_layout(int T, int C, int waves, bool shares) {
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   TileLayout l;
   l.tiles = (T + kBlock * waves - 1) / (kBlock * waves);
-  const size_t row = size_t(C) * 8, groups = size_t((l.tiles + kGroup - 1) / kGroup);
-  l.marks = 256;
-  l.owner = l.marks + up(size_t((T + kBlock - 1) / kBlock) * 8);
+  const size_t row = size_t(C) * 8, subs = size_t((l.tiles + kSub - 1) / kSub),
+               groups = size_t((l.tiles + kGroup - 1) / kGroup);
+  l.tickets = 256;
+  l.marks = l.tickets + up(size_t((C + 127) / 128) * kLine * 4);
+  l.owner = l.marks + up(size_t(l.tiles) * waves * 4);
   l.pairs = l.owner + up(size_t(T) * 4);
-  l.kept = l.pairs + l.tiles * row;
-  l.words = (l.tiles + groups) * size_t(C);
+  l.subs = l.pairs + l.tiles * row;
+  l.kept = l.subs + subs * row;
+  l.words = (l.tiles + subs + groups) * size_t(C);
   l.part = up(l.kept + groups * row);
   l.total = l.part + (shares ? up(size_t(l.tiles) * C * 4) : 0);
   return l;
 }
 TileSpace tile_space(void* ws, const TileLayout& l) {
   unsigned char* p = static_cast<unsigned char*>(ws);
-  return {reinterpret_cast<uint32_t*>(p), reinterpret_cast<uint2*>(p + l.marks), reinterpret_cast<int32_t*>(p + l.owner),
-          reinterpret_cast<uint64_t*>(p + l.pairs), reinterpret_cast<uint64_t*>(p + l.kept)};
+  return {reinterpret_cast<uint32_t*>(p),          reinterpret_cast<uint32_t*>(p + l.tickets),
+          reinterpret_cast<uint32_t*>(p + l.marks), reinterpret_cast<int32_t*>(p + l.owner),
+          reinterpret_cast<uint64_t*>(p + l.pairs), reinterpret_cast<uint64_t*>(p + l.subs),
+          reinterpret_cast<uint64_t*>(p + l.kept)};
 }
 hipError_t tile_setup(const Sequences& seq, int S, int C, const TileSpace& ws, const TileLayout& l, const float* from,
                       float* to, hipStream_t stream) {
