@@ -168,49 +168,78 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_gated_kernel(int M, int N
 #endif
 }
 
-constexpr int kGatedRows = 16;   // rows per workgroup of gated_dz_kernel where it sums, 4 where it does not
+// Four values at element alignment, n of them inside the row.
+template <typename T>
+__device__ __forceinline__ f32x4_t load4_any(const T* p, int n) {
+  T v[4] = {};
+  if (n >= 4) {
+    __builtin_memcpy(v, p, sizeof v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i] = p[i];
+  }
+  return f32x4_t{to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3])};
+}
 
 // dz[m][0][n] and dz[m][1][n] into rows of 2 ld values (columns N..ld of each
-// half and rows M..rows zero), and part[chunk][2][n] = the chunk's sums over its
-// rows, in fp32, before the rounding to T.  256 threads, four columns each.
+// half and rows M..rows zero), and the sums of both over a chunk of `per` rows,
+// in fp32, before the rounding to T: part[chunk][2][n], or (one chunk) dbg and
+// dbu themselves.  64 x 4 threads: four columns and every fourth row each.
 template <typename T>
 __global__ __launch_bounds__(256) void gated_dz_kernel(int M, int rows, int N, int act, const T* __restrict__ dy,
                                                        const float* __restrict__ zg, const float* __restrict__ zu,
-                                                       T* __restrict__ dz, long ld, float* __restrict__ part, bool vec,
-                                                       int per) {
-  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
-  const int m0 = blockIdx.y * per, m1 = min(rows, m0 + per);
-  if (n >= ld) return;
-  const int left = N - n;
+                                                       T* __restrict__ dz, long ld, float* __restrict__ part, int per,
+                                                       T* dbg, T* dbu) {
+  __shared__ f32x4_t sums[3][2][64];
+  const int l = threadIdx.x & 63, q = threadIdx.x >> 6, n = (blockIdx.x * 64 + l) * 4;
+  const int m1 = min(rows, (int(blockIdx.y) + 1) * per), left = N - n;
   f32x4_t sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
+  if (n < ld) {
 #pragma unroll 4
-  for (int m = m0; m < m1; ++m) {
-    f32x4_t dg = {0.f, 0.f, 0.f, 0.f}, du = dg;
-    if (m < M && left > 0) {
-      const size_t at = size_t(m) * N + n;
-      const f32x4_t d = load4(dy + at, left, vec), g = load4(zg + at, left, vec), u = load4(zu + at, left, vec);
+    for (int m = blockIdx.y * per + q; m < m1; m += 4) {
+      f32x4_t dg = {0.f, 0.f, 0.f, 0.f}, du = dg;
+      if (m < M && left > 0) {
+        const size_t at = size_t(m) * N + n;
+        const f32x4_t d = load4_any(dy + at, left), g = load4_any(zg + at, left), u = load4_any(zu + at, left);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dg[e] = d[e] * u[e] * act_slope<T>(act, g[e]);
-        du[e] = d[e] * act_value<T>(act, g[e]);
+        for (int e = 0; e < 4; ++e) {
+          dg[e] = d[e] * u[e] * act_slope<T>(act, g[e]);
+          du[e] = d[e] * act_value<T>(act, g[e]);
+        }
       }
+      if (dz) {
+        store4(dz + size_t(m) * 2 * ld + n, dg, 4, true);
+        store4(dz + size_t(m) * 2 * ld + ld + n, du, 4, true);
+      }
+      sg += dg;
+      su += du;
     }
-    if (dz) {
-      store4(dz + size_t(m) * 2 * ld + n, dg, 4, true);
-      store4(dz + size_t(m) * 2 * ld + ld + n, du, 4, true);
-    }
-    sg += dg;
-    su += du;
   }
-  if (part) {
-    float* p = part + size_t(blockIdx.y) * 2 * N + n;
+  if (!part && !dbg && !dbu) return;
+  if (q > 0) {
+    sums[q - 1][0][l] = sg;
+    sums[q - 1][1][l] = su;
+  }
+  __syncthreads();
+  if (q > 0) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) {
+  for (int i = 0; i < 3; ++i) {
+    sg += sums[i][0][l];
+    su += sums[i][1][l];
+  }
+  float* p = part + size_t(blockIdx.y) * 2 * N + n;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) {
+      if (part) {
         p[e] = sg[e];
         p[N + e] = su[e];
+      } else {
+        if (dbg) dbg[n + e] = from_f32<T>(sg[e]);
+        if (dbu) dbu[n + e] = from_f32<T>(su[e]);
       }
-  }
+    }
 }
 
 // dbg and dbu: sums over the chunks of the columns of both, 8 threads each,
@@ -294,15 +323,55 @@ size_t gated_split_bytes(int M, int N, int K, bool bf16) {
 // Bytes of a copy of `rows` rows of K values to rows of whole steps.
 size_t padded_bytes(long rows, int K) { return up256(size_t(rows) * up64(K) * 2); }
 
-// A copy of `rows` rows at *ws, which moves on behind it; *p and *ld become the copy's.
-hipError_t padded(long rows, int K, const bf16_t** p, long* ld, unsigned char** ws, hipStream_t stream) {
-  bf16_t* copy = reinterpret_cast<bf16_t*>(*ws);
-  *ws += padded_bytes(rows, K);
-  *ld = up64(K);
-  const hipError_t e = pad_rows(rows, K, *ld, *p, copy, stream);
-  *p = copy;
-  return e;
+// Up to three matrices of K columns, copied to rows of ld values, zeros behind:
+// one launch (y: which), eight values per thread.
+struct Padded {
+  const bf16_t* src[3];
+  bf16_t* dst[3];
+  long rows[3];
+};
+__global__ __launch_bounds__(256) void pad_matrices_kernel(Padded p, long n, long ld) {
+  const bf16_t* src = blockIdx.y == 0 ? p.src[0] : blockIdx.y == 1 ? p.src[1] : p.src[2];
+  bf16_t* dst = blockIdx.y == 0 ? p.dst[0] : blockIdx.y == 1 ? p.dst[1] : p.dst[2];
+  const long rows = blockIdx.y == 0 ? p.rows[0] : blockIdx.y == 1 ? p.rows[1] : p.rows[2];
+  const uint32_t per = uint32_t(ld / 8);
+  const long at = long(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= rows * per) return;
+  const long r = at / per, c = (at - r * per) * 8;
+  const bf16_t* s = src + r * n;
+  *reinterpret_cast<u32x4_t*>(dst + at * 8) = load_any(s + c, s + (c < n ? n : c));
 }
+
+// Copies to be made; add() gives one its place in the workspace, which *ws is
+// moved on behind, and puts *p there.
+struct Copies {
+  Padded pad = {};
+  int count = 0;
+  void add(long rows, int K, const bf16_t** p, unsigned char** ws) {
+    bf16_t* copy = reinterpret_cast<bf16_t*>(*ws);
+    *ws += padded_bytes(rows, K);
+    pad.src[count] = *p;
+    pad.dst[count] = copy;
+    pad.rows[count++] = rows;
+    *p = copy;
+  }
+  hipError_t run(int K, hipStream_t stream) const {
+    long most = 0;
+    for (int i = 0; i < count; ++i) most = pad.rows[i] > most ? pad.rows[i] : most;
+    if (most == 0) return hipSuccess;
+    const long ld = up64(K), threads = most * (ld / 8);
+    if (threads > 1l << 30) {   // more than a grid of three holds: one by one, in pieces
+      for (int i = 0; i < count; ++i) {
+        const hipError_t e = pad_rows(pad.rows[i], K, ld, pad.src[i], pad.dst[i], stream);
+        if (e != hipSuccess) return e;
+      }
+      return hipSuccess;
+    }
+    hipLaunchKernelGGL(pad_matrices_kernel, dim3(unsigned((threads + 255) / 256), count), dim3(256), 0, stream, pad,
+                       long(K), ld);
+    return hipGetLastError();
+  }
+};
 
 template <typename T>
 hipError_t gated_product(const GatedArgs& a, const Product<T>& g, float* part, hipStream_t stream) {
@@ -339,13 +408,16 @@ hipError_t gated_bf16(const GatedArgs& a, hipStream_t stream) {
     return hipGetLastError();
   }
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  hipError_t e = hipSuccess;
-  long ldx = a.K, ldw = a.K;
   // the b operand has to end in zeros, and the a operand's rows to be aligned
-  if (a.K % kStep && (e = padded(a.M, a.K, &x, &ldx, &ws, stream)) != hipSuccess) return e;
-  if (a.K % 8 && ((e = padded(a.N, a.K, &wg, &ldw, &ws, stream)) != hipSuccess ||
-                  (e = padded(a.N, a.K, &wu, &ldw, &ws, stream)) != hipSuccess))
-    return e;
+  const long ldx = a.K % kStep ? up64(a.K) : a.K, ldw = a.K % 8 ? up64(a.K) : a.K;
+  Copies copies;
+  if (a.K % kStep) copies.add(a.M, a.K, &x, &ws);
+  if (a.K % 8) {
+    copies.add(a.N, a.K, &wg, &ws);
+    copies.add(a.N, a.K, &wu, &ws);
+  }
+  const hipError_t e = copies.run(a.K, stream);
+  if (e != hipSuccess) return e;
   Product<bf16_t> g = {};
   g.A[0] = {wg, ldw, 1, a.N};
   g.A[1] = {wu, ldw, 1, a.N};
@@ -364,8 +436,13 @@ hipError_t gated_f32(const GatedArgs& a, hipStream_t stream) {
 }
 
 long dz_rows(int M, bool bf16) { return bf16 ? up64(M) : M; }
+// Rows whose sums one workgroup of gated_dz_kernel makes: all of few, whose
+// bias gradients then need no second launch (8 x 256: 42 us against 38 for a
+// training pass), else 16; the grid's second axis holds 65535 chunks.
+int chunk_rows(long rows) { return rows <= 64 ? 64 : rows > 65535l * 16 ? 32 : 16; }
 size_t part_bytes(int M, int N) {
-  return up256(size_t((up64(M) + kGatedRows - 1) / kGatedRows) * 2 * N * 4);
+  const long rows = up64(M), per = chunk_rows(rows);
+  return rows <= per ? 0 : up256(size_t((rows + per - 1) / per) * 2 * N * 4);
 }
 
 template <typename T>
@@ -373,36 +450,41 @@ hipError_t gated_backward_t(const GatedBackwardArgs& a, hipStream_t stream) {
   constexpr bool bf16 = sizeof(T) == 2;
   const long ld = up64(a.N), rows = dz_rows(a.M, bf16);
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
-  float* part = reinterpret_cast<float*>(ws);
+  const bool sums = a.dbg || a.dbu, products = (a.dx || a.dwg || a.dwu) && a.K > 0;
+  const int per = chunk_rows(up64(a.M)), chunks = int((rows + per - 1) / per);
+  float* part = up64(a.M) > per ? reinterpret_cast<float*>(ws) : nullptr;   // one chunk: the sums are the gradients
   ws += part_bytes(a.M, a.N);
   T* dz = reinterpret_cast<T*>(ws);
   ws += up256(size_t(rows) * 2 * ld * sizeof(T));
-  const bool sums = a.dbg || a.dbu, products = (a.dx || a.dwg || a.dwu) && a.K > 0;
-  // the grid's second axis holds 65535 chunks
-  const int per = rows > 65535l * kGatedRows ? 2 * kGatedRows : sums || rows > 65535l * 4 ? kGatedRows : 4;
   hipError_t e = hipSuccess;
   if (rows > 0 && a.N > 0) {
     const float* zu = a.pre + size_t(a.M) * a.N;
-    hipLaunchKernelGGL((gated_dz_kernel<T>), dim3(unsigned((ld + 1023) / 1024), unsigned((rows + per - 1) / per)),
-                       dim3(256), 0, stream, a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, zu,
-                       products ? dz : nullptr, ld, sums ? part : nullptr,
-                       a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.pre) % 16 == 0, per);
+    hipLaunchKernelGGL((gated_dz_kernel<T>), dim3(unsigned((ld + 255) / 256), unsigned(chunks)), dim3(256), 0, stream,
+                       a.M, int(rows), a.N, a.act, static_cast<const T*>(a.dy), a.pre, zu, products ? dz : nullptr, ld,
+                       sums ? part : nullptr, per, part ? nullptr : static_cast<T*>(a.dbg),
+                       part ? nullptr : static_cast<T*>(a.dbu));
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (sums && a.N > 0) {
-    hipLaunchKernelGGL((gated_dbias_kernel<T>), dim3(unsigned((2l * a.N + 31) / 32)), dim3(256), 0, stream, a.N,
-                       int((rows + per - 1) / per), part, static_cast<T*>(a.dbg), static_cast<T*>(a.dbu));
+  if (sums && a.N > 0 && (part || rows == 0)) {
+    hipLaunchKernelGGL((gated_dbias_kernel<T>), dim3(unsigned((2l * a.N + 31) / 32)), dim3(256), 0, stream, a.N, chunks,
+                       part, static_cast<T*>(a.dbg), static_cast<T*>(a.dbu));
     if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const T *wg = static_cast<const T*>(a.wg), *wu = static_cast<const T*>(a.wu), *x = static_cast<const T*>(a.x);
+  long ldw = a.K;
+  if constexpr (bf16) {
+    if (a.K % 8) {   // the products' a operands need aligned rows
+      ldw = up64(a.K);
+      Copies copies;
+      if (a.dx && a.M > 0) {
+        copies.add(a.N, a.K, &wg, &ws);
+        copies.add(a.N, a.K, &wu, &ws);
+      }
+      if ((a.dwg || a.dwu) && a.N > 0) copies.add(a.M, a.K, &x, &ws);
+      if ((e = copies.run(a.K, stream)) != hipSuccess) return e;
+    }
   }
   if (a.dx && a.K > 0 && a.M > 0) {
-    const T *wg = static_cast<const T*>(a.wg), *wu = static_cast<const T*>(a.wu);
-    unsigned char* behind = ws;
-    long ldw = a.K;
-    if constexpr (bf16) {
-      if (a.K % 8 && a.N > 0 && ((e = padded(a.N, a.K, &wg, &ldw, &behind, stream)) != hipSuccess ||
-                                 (e = padded(a.N, a.K, &wu, &ldw, &behind, stream)) != hipSuccess))
-        return e;
-    }
     Product<T> g = {};
     g.A[0] = {wg, 1, ldw, a.K};
     g.A[1] = {wu, 1, ldw, a.K};
@@ -413,18 +495,12 @@ hipError_t gated_backward_t(const GatedBackwardArgs& a, hipStream_t stream) {
     epi.y = static_cast<T*>(a.dx);
     epi.na = a.K;
     epi.vec = aligned4<T>(a.dx, a.K);
-    e = product<kCols, kRows>(g, false, epi, a.K, a.M, reinterpret_cast<float*>(behind), stream);
+    e = product<kCols, kRows>(g, false, epi, a.K, a.M, reinterpret_cast<float*>(ws), stream);
     if (e != hipSuccess) return e;
   }
   if ((a.dwg || a.dwu) && a.K > 0 && a.N > 0) {
-    const T* x = static_cast<const T*>(a.x);
-    unsigned char* behind = ws;
-    long ldx = a.K;
-    if constexpr (bf16) {
-      if (a.K % 8 && a.M > 0 && (e = padded(a.M, a.K, &x, &ldx, &behind, stream)) != hipSuccess) return e;
-    }
     Product<T> g = {};
-    g.A[0] = {x, 1, ldx, a.K};
+    g.A[0] = {x, 1, ldw, a.K};
     g.B[0] = {dz, 1, 2 * ld, int(2 * ld)};
     g.K[0] = a.M;
     TwoOutEpi<T> epi;
@@ -434,7 +510,7 @@ hipError_t gated_backward_t(const GatedBackwardArgs& a, hipStream_t stream) {
     epi.N = a.N;
     epi.na = a.K;
     epi.vec = (!a.dwg || aligned4<T>(a.dwg, a.K)) && (!a.dwu || aligned4<T>(a.dwu, a.K));
-    return product<kCols, kCols>(g, false, epi, a.K, int(2 * ld), reinterpret_cast<float*>(behind), stream);
+    return product<kCols, kCols>(g, false, epi, a.K, int(2 * ld), reinterpret_cast<float*>(ws), stream);
   }
   return hipSuccess;
 }
@@ -450,11 +526,10 @@ size_t gated_workspace_bytes(int M, int N, int K, bool bf16) {
 size_t gated_backward_workspace_bytes(int M, int N, int K, bool bf16) {
   const long ld = up64(N);
   const size_t dz = part_bytes(M, N) + up256(size_t(dz_rows(M, bf16)) * 2 * ld * (bf16 ? 2 : 4));
-  const bool copies = bf16 && K % 8 != 0;
-  // dx reads the weights, dwg and dwu read x, one after the other
-  const size_t dx = (copies ? 2 * padded_bytes(N, K) : 0) + split_bytes(K, M, 2l * N, bf16, false, true);
-  const size_t dw = (copies ? padded_bytes(M, K) : 0) + split_bytes(K, int(2 * ld), M, bf16, false, true);
-  return dz + (dx > dw ? dx : dw);
+  const size_t copies = bf16 && K % 8 != 0 ? 2 * padded_bytes(N, K) + padded_bytes(M, K) : 0;
+  // the products come one after the other
+  const size_t dx = split_bytes(K, M, 2l * N, bf16, false, true), dw = split_bytes(K, int(2 * ld), M, bf16, false, true);
+  return dz + copies + (dx > dw ? dx : dw);
 }
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t stream) {

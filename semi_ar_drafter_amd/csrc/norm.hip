@@ -80,7 +80,7 @@ struct Place {
   int t, threads, wave, waves, unit, units;
 };
 template <bool ONE>
-__device__ __forceinline__ Place place() {
+__device__ __forceinline__ Place place(int grid) {
   Place p;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = blockDim.x >> 6;
   p.t = ONE ? threadIdx.x & 63 : threadIdx.x;
@@ -88,7 +88,7 @@ __device__ __forceinline__ Place place() {
   p.wave = ONE ? 0 : w;
   p.waves = ONE ? 1 : n;
   p.unit = ONE ? blockIdx.x * n + w : blockIdx.x;
-  p.units = ONE ? gridDim.x * n : gridDim.x;
+  p.units = ONE ? grid * n : grid;
   return p;
 }
 
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(MOST) void norm_kernel(int M, int C, const T* x, co
                                                     T* __restrict__ y, float2* __restrict__ stat) {
   constexpr int N = Chunk<T>::N;
   __shared__ float2 parts[2][kMaxWaves];
-  const Place p = place<ONE>();
+  const Place p = place<ONE>(gridDim.x);
   const float each = 1.f / float(C);
   int turn = 0;
   for (int row = p.unit; row < M; row += p.units, turn ^= 1) {
@@ -195,19 +195,54 @@ __global__ __launch_bounds__(MOST) void norm_kernel(int M, int C, const T* x, co
   }
 }
 
+// dw and db of 32 channels from all rows, by one workgroup: its threads take
+// every (threads / 32)-th row of a channel, joined in order.
+template <typename T>
+__device__ __forceinline__ void columns(int first, int M, int C, const T* __restrict__ dy, const T* __restrict__ x,
+                                        const float2* __restrict__ stat, T* dw, T* db) {
+  __shared__ float2 sums[32][33];
+  const int l = threadIdx.x & 31, q = threadIdx.x >> 5, parts = blockDim.x >> 5, c = first + l;
+  float sw = 0.f, sb = 0.f;
+  if (c < C) {
+#pragma unroll 8
+    for (int row = q; row < M; row += parts) {
+      const size_t at = size_t(row) * C + c;
+      const float2 st = stat[row];
+      const float g = to_f32(dy[at]);
+      sw = fmaf(g, (to_f32(x[at]) - st.x) * st.y, sw);
+      sb += g;
+    }
+  }
+  sums[q][l] = make_float2(sw, sb);
+  __syncthreads();
+  if (q == 0 && c < C) {
+    for (int i = 1; i < parts; ++i) {
+      sw += sums[i][l].x;
+      sb += sums[i][l].y;
+    }
+    if (dw) dw[c] = from_f32<T>(sw);
+    if (db) db[c] = from_f32<T>(sb);
+  }
+}
+
 // Each unit (a workgroup, or ONE: a wave) goes through its rows and keeps its
 // share of dw and db in registers: part[unit][0 and 1][C].  The next row's
 // loads are sent off before this one's sums, and nothing else is loaded in
-// between (loads come back in order): the weights stay in registers.
+// between (loads come back in order): the weights stay in registers.  With
+// few rows dw and db are made beside dx, by workgroups of their own.
 template <typename T, int NV, int MOST, bool ONE, bool CENTER>
 __global__ __launch_bounds__(MOST) void norm_backward_kernel(
     int M, int C, const T* __restrict__ dy, const T* __restrict__ x, const float2* __restrict__ stat,
-    const T* __restrict__ w, const T* dsum, T* dx, float* __restrict__ part) {
+    const T* __restrict__ w, const T* dsum, T* dx, float* __restrict__ part, int rows_grid, T* dw_out, T* db_out) {
   constexpr int N = Chunk<T>::N;
+  if (int(blockIdx.x) >= rows_grid) {   // the workgroups behind those of the rows, if any, take channels
+    columns((int(blockIdx.x) - rows_grid) * 32, M, C, dy, x, stat, dw_out, db_out);
+    return;
+  }
   // 1024 threads have 128 registers each, which hold no second row of bf16
   constexpr bool AHEAD = NV <= 2 && (MOST <= 512 || sizeof(T) == 4);
   __shared__ float2 parts[2][kMaxWaves];
-  const Place p = place<ONE>();
+  const Place p = place<ONE>(rows_grid);
   const float each = 1.f / float(C);
   float dw[NV][N] = {}, db[NV][N] = {};
   Chunk<T> cw[NV], v[NV], g[NV], d[NV];
@@ -329,15 +364,18 @@ __global__ __launch_bounds__(256) void norm_join_kernel(int C, int units, const 
 }
 
 // Launch shape: threads per workgroup, chunks per thread, whether a wave has
-// rows of its own, workgroups.  Backwards two workgroups stay on each compute
-// unit and go through the rows: 16384 x 5120 takes 152 us so and 7 us for
-// joining the shares, with 1024 workgroups 167 and 13, with 768 160 and 10.
+// rows of its own, workgroups.  Where these leave shares of dw and db (shares),
+// two workgroups stay on each compute unit and go through the rows (16384 x
+// 5120: 152 us so and 7 us for joining, with 1024 workgroups 167 and 13, with
+// 768 160 and 10), and fewer with fewer rows, whose shares would be as long as
+// the rows themselves (1024 x 5120, forward and backward: 39 us with 128, 46
+// with 512).
 struct Shape {
   int threads, nv;
   bool one;
   int grid, units;
 };
-Shape shape_for(int M, int C, bool bf16, bool backward) {
+Shape shape_for(int M, int C, bool bf16, bool shares) {
   const int chunks = (C + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
   Shape s;
   s.one = chunks <= 64;
@@ -345,7 +383,7 @@ Shape shape_for(int M, int C, bool bf16, bool backward) {
   s.threads = s.one ? 256 : (chunks + s.nv - 1) / s.nv;
   s.threads = (s.threads + 63) / 64 * 64;
   const int rows = s.one ? 4 : 1, groups = (M + rows - 1) / rows;
-  const int most = backward ? 512 : 8192;
+  const int most = !shares ? 8192 : groups >= 4096 ? 512 : groups >= 1024 ? groups / 8 : 128;
   s.grid = groups < most ? groups : most;
   s.units = s.grid * rows;
   return s;
@@ -372,19 +410,28 @@ hipError_t norm_t(const NormArgs& a, hipStream_t stream) {
   return DSPARK_NORM_SHAPES(norm_kernel, T, CENTER, s, go);
 }
 
+// Whether dw and db are made beside dx in one launch, from the inputs again,
+// instead of from shares in a second one (forward and backward, us, bf16: 128 x
+// 2560 9.2 against 13.3, 512 x 2560 13.9 against 18.2, 512 x 1001 16.4 against
+// 16.8, 1024 x 1001 27 against 23).
+bool beside(int M) { return M <= 512; }
+
 template <typename T, bool CENTER>
 hipError_t norm_backward_t(const NormBackwardArgs& a, hipStream_t stream) {
-  const Shape s = shape_for(a.M, a.C, sizeof(T) == 2, true);
-  float* part = a.dw || a.db ? static_cast<float*>(a.ws) : nullptr;
+  const bool sums = a.dw || a.db, one = sums && a.M > 0 && beside(a.M);
+  const Shape s = shape_for(a.M, a.C, sizeof(T) == 2, sums && !one);
+  float* part = sums && !one ? static_cast<float*>(a.ws) : nullptr;
+  const int rows_grid = one && !a.dx ? 0 : s.grid, grid = rows_grid + (one ? (a.C + 31) / 32 : 0);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(s.grid), dim3(s.threads), 0, stream, a.M, a.C, static_cast<const T*>(a.dy),
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(s.threads), 0, stream, a.M, a.C, static_cast<const T*>(a.dy),
                        static_cast<const T*>(a.x), reinterpret_cast<const float2*>(a.stat), static_cast<const T*>(a.w),
-                       static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), part);
+                       static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), part, rows_grid, static_cast<T*>(a.dw),
+                       static_cast<T*>(a.db));
     return hipGetLastError();
   };
   hipError_t e = hipSuccess;
   if (a.M > 0) e = DSPARK_NORM_SHAPES(norm_backward_kernel, T, CENTER, s, go);
-  if (e != hipSuccess || !(a.dw || a.db)) return e;
+  if (e != hipSuccess || !sums || one) return e;
   hipLaunchKernelGGL((norm_join_kernel<T>), dim3((a.C + 31) / 32, 2), dim3(256), 0, stream, a.C, a.M > 0 ? s.units : 0,
                      part, static_cast<T*>(a.dw), static_cast<T*>(a.db));
   return hipGetLastError();
@@ -393,6 +440,7 @@ hipError_t norm_backward_t(const NormBackwardArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int M, int C, bool bf16) {
+  if (beside(M)) return 0;
   const size_t n = size_t(shape_for(M, C, bf16, true).units) * 2 * C * 4;
   return (n + 255) & ~size_t(255);
 }
