@@ -124,6 +124,8 @@ def _declare(lib):
 def load(path: str | None = None):
     """Load (once) and return the ctypes handle of libdspark."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or library_path()
@@ -144,9 +146,15 @@ def _check(status: int):
 # ----------------------------------------------------------------------------
 # torch-facing wrappers
 # ----------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:      # an import statement costs every call, even of a loaded module
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -589,8 +597,8 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 def _is(t, name, dtype, shape, device):
     """_need() for calls of a few microseconds: one test of all that has to
     hold, the reasons only where it does not."""
-    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_cuda and t.is_contiguous()):
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.device == device and t.is_contiguous()):
         _need(t, name, dtype, shape, device)
 
 
@@ -650,6 +658,11 @@ def _scratch(nbytes, device, kind, workspace):
         return workspace.data_ptr(), workspace.numel()
     if nbytes == 0:
         return None, 0
+    if not _torch().cuda.is_current_stream_capturing():
+        # as _workspace(), without making a stream object where the cached one fits
+        ws, _ = _ws_cache.get(_workspace_key(kind, device.index, _raw_stream(device)), (None, None))
+        if ws is not None and ws.numel() >= nbytes:
+            return ws.data_ptr(), ws.numel()
     ws = _captured(nbytes, device) or _workspace(nbytes, device, kind)
     return ws.data_ptr(), ws.numel()
 
@@ -682,7 +695,7 @@ def _on(device):
     """The device the operands live on becomes the current one, so that its
     current stream takes the launches."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         return _HERE_ALREADY
     return torch.cuda.device(device)
 
