@@ -44,9 +44,16 @@ template <> struct Pair<float> {
   }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(raw[i]); }
 };
+// past: by the caches, which need not keep it.
 template <typename T>
-__device__ __forceinline__ void store2(T* p, float a, float b, bool both) {
-  if (both) {
+__device__ __forceinline__ void store2(T* p, float a, float b, bool both, bool past = false) {
+  if (both && past) {
+    typedef uint32_t pair_t __attribute__((ext_vector_type(sizeof(T) / 2), aligned(sizeof(T))));
+    T v[2] = {from_f32<T>(a), from_f32<T>(b)};
+    pair_t w;
+    __builtin_memcpy(&w, v, 2 * sizeof(T));
+    __builtin_nontemporal_store(w, reinterpret_cast<pair_t*>(p));
+  } else if (both) {
     T v[2] = {from_f32<T>(a), from_f32<T>(b)};
     __builtin_memcpy(p, v, 2 * sizeof(T));
   } else {
@@ -496,7 +503,7 @@ __device__ __forceinline__ State2 of_sequence(const float* v, const TileSpace& w
 template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles, int C, const T* __restrict__ x,
                                                       const void* __restrict__ gate, const float* h0, T* __restrict__ h,
-                                                      float* last, float* __restrict__ states) {
+                                                      float* last, float* __restrict__ states, bool past) {
   __shared__ TileLds<W> lds;
   int k, c0;
   take_tile(ws, C, &k, &c0);
@@ -577,14 +584,14 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
     for (int i = 0; i < kBlock; ++i) {
       v.v0 = fmaf(a0[i], v.v0, b0[i]);
       v.v1 = fmaf(a1[i], v.v1, b1[i]);
-      store2(out + size_t(i) * C, v.v0, v.v1, both);
+      store2(out + size_t(i) * C, v.v0, v.v1, both, past);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kBlock; ++i)
       if (r.has(i)) {
         v.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
-        store2(out + size_t(i) * C, v.v0, v.v1, both);
+        store2(out + size_t(i) * C, v.v0, v.v1, both, past);
         if (last && r.ends(i)) store2(last + size_t(ws.owner[r.t0 + i]) * C + c, v.v0, v.v1, both);
       }
   }
@@ -596,7 +603,7 @@ template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
     TileSpace ws, int tiles, int C, const T* __restrict__ dh, const T* __restrict__ x, const void* __restrict__ gate,
     const float* __restrict__ h0, const float* dlast, const float* __restrict__ states, T* __restrict__ dx,
-    T* __restrict__ dg, float* dh0, float* __restrict__ part) {
+    T* __restrict__ dg, float* dh0, float* __restrict__ part, bool past) {
   __shared__ TileLds<W> lds;
   int k, c0;
   take_tile(ws, C, &k, &c0);
@@ -689,10 +696,10 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
       const size_t at = size_t(r.t0 + i) * C + c;
       if (SIGMOID) {
         const float u0 = d0 * r0[i], u1 = d1 * r1[i];
-        if (dx) store2(dx + at, u0, u1, both);
-        if (dg) store2(dg + at, u0 * w0[i], u1 * w1[i], both);
+        if (dx) store2(dx + at, u0, u1, both, past);
+        if (dg) store2(dg + at, u0 * w0[i], u1 * w1[i], both, past);
       } else {
-        if (dx) store2(dx + at, d0, d1, both);
+        if (dx) store2(dx + at, d0, d1, both, past);
         sum0 = fmaf(d0, w0[i], sum0);
         sum1 = fmaf(d1, w1[i], sum1);
       }
@@ -731,6 +738,13 @@ constexpr int kWaves = 8, kWavesBackward = 4;
 
 // Whether the rows are split into tiles.
 bool tiled(int T, int S) { return T >= 128 * long(S); }
+
+// Whether the tiles' outputs go by the caches: with long rows, whose tiles are
+// bound by memory (in training, us with and without: 65536 x 2560 bf16 706
+// against 837, 16384 x 2560 178 and 221, 8192 x 1001 fp32 90 and 135); with
+// short ones a tile waits for the one before, and for its stores (16384 x 1024
+// bf16 122 against 108, x 512 120 against 97).
+bool past_caches(int C, size_t elem) { return C * elem >= 4000; }
 
 // Offsets of TileSpace's parts, and of dgate's shares behind them.
 struct TileLayout {
@@ -787,7 +801,7 @@ hipError_t forward_t(const RecurrenceArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((tile_kernel<T, SIGMOID, kWaves>), dim3(unsigned(l.tiles) * ((a.C + 127) / 128)),
                        dim3(64 * kWaves), 0, stream, ws, l.tiles, a.C, static_cast<const T*>(a.x), a.gate, a.h0,
-                       static_cast<T*>(a.h), a.last, a.states);
+                       static_cast<T*>(a.h), a.last, a.states, past_caches(a.C, sizeof(T)));
     return hipGetLastError();
   }
   const dim3 grid((a.C + 127) / 128, groups(a.S, false));
@@ -815,7 +829,8 @@ hipError_t backward_t(const RecurrenceArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((tile_backward_kernel<T, SIGMOID, kWavesBackward>),
                        dim3(unsigned(l.tiles) * ((a.C + 127) / 128)), dim3(64 * kWavesBackward), 0, stream, ws, l.tiles,
                        a.C, static_cast<const T*>(a.dh), static_cast<const T*>(a.x), a.gate, a.h0, a.dlast,
-                       a.states_in, static_cast<T*>(a.dx), SIGMOID ? static_cast<T*>(a.dgate) : nullptr, a.dh0, part);
+                       a.states_in, static_cast<T*>(a.dx), SIGMOID ? static_cast<T*>(a.dgate) : nullptr, a.dh0, part,
+                       past_caches(a.C, sizeof(T)));
     e = hipGetLastError();
   } else if (a.S > 0) {
     hipLaunchKernelGGL((rows_backward_kernel<T, SIGMOID>), dim3((a.C + 127) / 128, g), dim3(256), 0, stream,
