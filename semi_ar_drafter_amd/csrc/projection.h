@@ -228,6 +228,15 @@ struct LinearEpi {
   float* pre;
   int act, na;
   bool vec;   // rows of na values keep four-value alignment, and so does bias
+  // of the rows from b on (a multiple of four)
+  LinearEpi from(int b) const {
+    LinearEpi r = *this;
+    const size_t at = size_t(b) * na;
+    r.y += at;
+    if (r.residual) r.residual += at;
+    if (r.pre) r.pre += at;
+    return r;
+  }
   template <int FM, int FN>
   __device__ __forceinline__ void init(f32x4_t (&acc)[FM][FN], const TileAt&) const {
     acc_zero(acc);

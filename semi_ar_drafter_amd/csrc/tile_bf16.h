@@ -660,6 +660,7 @@ constexpr size_t kCopyBytes = size_t(64) << 20;
 // fp32 sums its contraction is split.
 struct Plan {
   int tile, splits;
+  double cost = 0;   // in steps of the 256 x 256 tile, as below
 };
 
 // any: register staging, which the large tile has no registers left for.
@@ -689,7 +690,7 @@ inline Plan plan_for(int na, int nb, long K, bool any, bool cols, bool split) {
       const double cost = rounds * (large ? steps_s + 7 + (s > 1 ? 12 : 0) : (cols ? 0.72 : 0.6) * steps_s + 3 + (s > 1 ? 4 : 0));
       if (cost < least * 0.97) {
         least = cost;
-        best = {c, s};
+        best = {c, s, cost};
       }
     }
   }

@@ -138,7 +138,8 @@ def test_activations(act, dtype):
     check(5, 70, 96, dtype, act, bias=False)
 
 
-@pytest.mark.parametrize("M,N,K", [(1500, 2056, 1096), (4000, 1032, 520), (2050, 1024, 1032)])
+@pytest.mark.parametrize("M,N,K", [(1500, 2056, 1096), (4000, 1032, 520), (2050, 1024, 1032), (2400, 10000, 2600),
+                                   (2700, 2560, 5120), (4503, 2000, 4104)])
 def test_large_tiles(M, N, K):
     say(f"[case] gated {M} x {N} x {K}")
     check(M, N, K, torch.bfloat16, "silu", bias=True)
