@@ -112,67 +112,105 @@ __global__ __launch_bounds__(256) void join_gated_kernel(int M, int splits, cons
   epi.finish(g, u, b, a, epi.na - a);
 }
 
-// A few rows (M <= 16), as in linear.hip: both weights are read once, straight
-// into the matrix instruction's operand registers.
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void few_rows_gated_kernel(int M, int N, int K, const bf16_t* __restrict__ x,
-                                                                    const bf16_t* __restrict__ wg,
-                                                                    const bf16_t* __restrict__ wu,
-                                                                    GatedEpi<bf16_t> epi) {
+// A few rows (M <= 16): both weights are read once, straight into the matrix
+// instruction's operand registers; each of eight waves takes a share of the
+// contraction, and LDS joins them (16384 x 4096, one row: 46.5 us, 5.8 TB/s, with
+// four waves 57).  16 features per workgroup.  Any K: rows need element alignment
+// only, and what is left of the contraction is masked.
+//
+// A load takes 128 bytes of each of 8 features, whole lines (with 64 bytes of
+// 16 features, as the instruction's operand wants them, 10240 x 5120 takes 55 us
+// for one row instead of 43): its operand rows l < 8 hold feature l and the
+// first 32 of 64 of the contraction, l >= 8 feature l - 8 and the other 32.  Two
+// instructions multiply it by both halves of x; of each result the half that
+// belongs together is used.
+__global__ __launch_bounds__(512) void few_rows_gated_kernel(int M, int N, int K, const bf16_t* __restrict__ x,
+                                                            const bf16_t* __restrict__ wg,
+                                                            const bf16_t* __restrict__ wu, GatedEpi<bf16_t> epi) {
+  constexpr int WAVES = 8;
   __shared__ f32x4_t part[WAVES][2][64];
 #if defined(__HIP_DEVICE_COMPILE__)
   // uniform: matrix instructions ignore the lane mask, so nothing around them may diverge
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int a0 = blockIdx.x * 16;
-  const int full = K / 32;   // whole steps of 32
+  const int full = K / 64;   // whole steps of 64
   const int s0 = full * wave / WAVES, s1 = full * (wave + 1) / WAVES;
-  const long row = long(min(a0 + l, N - 1)) * K + q * 8;
-  const bf16_t *pg = wg + row, *pu = wu + row;
+  const int chunk = (q + (l >> 3) * 4) * 8;   // this lane's place in a step, of the weights
+  const long row0 = long(min(a0 + (l & 7), N - 1)) * K + chunk, row1 = long(min(a0 + 8 + (l & 7), N - 1)) * K + chunk;
   const bf16_t* px = x + long(min(l, M - 1)) * K + q * 8;
-  f32x4_t ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
-  auto step = [&](u32x4_t g, u32x4_t u, u32x4_t b) {
-    const bf16x8_t vb = __builtin_bit_cast(bf16x8_t, b);
-    ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, g), vb, ag, 0, 0, 0);
-    au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u), vb, au, 0, 0, 0);
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[2][2][2] = {{{zero, zero}, {zero, zero}}, {{zero, zero}, {zero, zero}}};   // matrix, features, half
+  struct Step {
+    u32x4_t w[2][2], b[2];
   };
-  constexpr int U = 4;   // steps in flight: 8 KiB of weights per wave
+  auto multiply = [&](const Step& t) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[m][f][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, t.w[m][f]),
+                                                                 __builtin_bit_cast(bf16x8_t, t.b[h]), acc[m][f][h], 0, 0, 0);
+  };
+  constexpr int U = 2;   // steps in flight: 8 KiB of weights per wave
   for (int s = s0; s < s1; s += U) {
-    u32x4_t g[U], u[U], b[U];
+    Step t[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
       if (s + i < s1) {
-        __builtin_memcpy(&g[i], pg + (s + i) * 32, 16);
-        __builtin_memcpy(&u[i], pu + (s + i) * 32, 16);
-        __builtin_memcpy(&b[i], px + (s + i) * 32, 16);
+        const long at = long(s + i) * 64;
+        __builtin_memcpy(&t[i].w[0][0], wg + row0 + at, 16);
+        __builtin_memcpy(&t[i].w[0][1], wg + row1 + at, 16);
+        __builtin_memcpy(&t[i].w[1][0], wu + row0 + at, 16);
+        __builtin_memcpy(&t[i].w[1][1], wu + row1 + at, 16);
+        __builtin_memcpy(&t[i].b[0], px + at, 16);
+        __builtin_memcpy(&t[i].b[1], px + at + 32, 16);
       }
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (s + i < s1) step(g[i], u[i], b[i]);
+      if (s + i < s1) multiply(t[i]);
   }
-  if (wave == WAVES - 1 && full * 32 < K) {   // the rest, zero behind the row's end
-    const int n = K - full * 32 - q * 8;
-    uint32_t g[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  if (wave == WAVES - 1 && full * 64 < K) {   // the rest, zero behind the row's end
+    const long at = long(full) * 64;
+    const int left = K - full * 64;
+    auto some = [&](const bf16_t* p, int n) {
+      uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) {
-        g[e >> 1] |= uint32_t(pg[full * 32 + e]) << (16 * (e & 1));
-        u[e >> 1] |= uint32_t(pu[full * 32 + e]) << (16 * (e & 1));
-        b[e >> 1] |= uint32_t(px[full * 32 + e]) << (16 * (e & 1));
-      }
-    step(u32x4_t{g[0], g[1], g[2], g[3]}, u32x4_t{u[0], u[1], u[2], u[3]}, u32x4_t{b[0], b[1], b[2], b[3]});
+      for (int e = 0; e < 8; ++e)
+        if (e < n) v[e >> 1] |= uint32_t(p[e]) << (16 * (e & 1));
+      return u32x4_t{v[0], v[1], v[2], v[3]};
+    };
+    Step t;
+    t.w[0][0] = some(wg + row0 + at, left - chunk);
+    t.w[0][1] = some(wg + row1 + at, left - chunk);
+    t.w[1][0] = some(wu + row0 + at, left - chunk);
+    t.w[1][1] = some(wu + row1 + at, left - chunk);
+    t.b[0] = some(px + at, left - q * 8);
+    t.b[1] = some(px + at + 32, left - q * 8 - 32);
+    multiply(t);
   }
-  part[wave][0][lane] = ag;
-  part[wave][1][lane] = au;
+  // features 4 q + e: of the first eight in lanes q < 2, of the others in q >= 2;
+  // the other half of the contraction's sum is two quarters away
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    f32x4_t v = q < 2 ? acc[m][0][0] : acc[m][1][1];
+    const f32x4_t o = q < 2 ? acc[m][1][0] : acc[m][0][1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(o[e], 32, 64);
+    part[wave][m][lane] = v;
+  }
   __syncthreads();
   if (wave == 0) {
+    f32x4_t g = part[0][0][lane], u = part[0][1][lane];
 #pragma unroll
     for (int v = 1; v < WAVES; ++v) {
-      ag += part[v][0][lane];
-      au += part[v][1][lane];
+      g += part[v][0][lane];
+      u += part[v][1][lane];
     }
     const int a = a0 + 4 * q;
-    if (l < M && a < N) epi.finish(ag, au, l, a, N - a);
+    if (l < M && a < N) epi.finish(g, u, l, a, N - a);
   }
 #endif
 }
@@ -334,8 +372,13 @@ GatedEpi<T> gated_epi(const GatedArgs& a) {
   return epi;
 }
 
-// Where the rows are few enough for few_rows_gated_kernel.
-bool few_gated_rows(int M, int N, int K) { return K % 8 != 0 ? M <= 16 : M <= 4 || (M <= 16 && N <= 4096); }
+// Where the rows are few enough for few_rows_gated_kernel (weights from memory,
+// us, against the tiles: one row of 8192 x 2560 17.3 and 20.3, of 16384 x 4096
+// 46.5 and 60.7; sixteen 20.6 and 21.7, 50.9 and 60.3), whose rows of x come in
+// 64-byte pieces: a long contraction of more than four is the tiles' (10240 x
+// 5120, four rows 43.9 and 42.5, sixteen 50.8 and 44.2), unless they had to copy
+// unaligned weights first.
+bool few_gated_rows(int M, int K) { return M <= 4 || (M <= 16 && (K <= 4096 || K % 8 != 0)); }
 
 Plan gated_plan(int M, int N, int K, bool bf16) {
   return bf16 ? plan_for(2 * N, M, K, false, false, true) : Plan{0, f32_splits(2 * N, M, K)};
@@ -440,15 +483,9 @@ hipError_t gated_product(const GatedArgs& a, const Product<T>& g, float* part, h
 hipError_t gated_bf16(const GatedArgs& a, hipStream_t stream) {
   const bf16_t *x = static_cast<const bf16_t*>(a.x), *wg = static_cast<const bf16_t*>(a.wg),
                *wu = static_cast<const bf16_t*>(a.wu);
-  if (few_gated_rows(a.M, a.N, a.K)) {
-    const dim3 grid(unsigned((a.N + 15) / 16));
-    // more waves share the contraction where there are too few workgroups to fill the compute units
-    if (a.N <= 16 * 2 * kComputeUnits)
-      hipLaunchKernelGGL((few_rows_gated_kernel<8>), grid, dim3(512), 0, stream, a.M, a.N, a.K, x, wg, wu,
-                         gated_epi<bf16_t>(a));
-    else
-      hipLaunchKernelGGL((few_rows_gated_kernel<4>), grid, dim3(256), 0, stream, a.M, a.N, a.K, x, wg, wu,
-                         gated_epi<bf16_t>(a));
+  if (few_gated_rows(a.M, a.K)) {
+    hipLaunchKernelGGL(few_rows_gated_kernel, dim3(unsigned((a.N + 15) / 16)), dim3(512), 0, stream, a.M, a.N, a.K, x,
+                       wg, wu, gated_epi<bf16_t>(a));
     return hipGetLastError();
   }
   unsigned char* ws = static_cast<unsigned char*>(a.ws);
@@ -563,7 +600,7 @@ hipError_t gated_backward_t(const GatedBackwardArgs& a, hipStream_t stream) {
 
 size_t gated_workspace_bytes(int M, int N, int K, bool bf16) {
   if (!bf16) return gated_split_bytes(M, N, K, false);
-  if (few_gated_rows(M, N, K)) return 0;
+  if (few_gated_rows(M, K)) return 0;
   return (K % kStep ? padded_bytes(M, K) : 0) + (K % 8 ? 2 * padded_bytes(N, K) : 0) + gated_split_bytes(M, N, K, true);
 }
 
