@@ -736,8 +736,14 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
 // of registers) four, so that two workgroups share a compute unit.
 constexpr int kWaves = 8, kWavesBackward = 4;
 
-// Whether the rows are split into tiles.
-bool tiled(int T, int S) { return T >= 128 * long(S); }
+// Whether the rows are split into tiles.  In training, us: a wave takes 4 + 0.5
+// a row of the longest sequence (decay 0.3); tiles take 24, for three launches
+// and words that go round, and 0.006 a row of all sequences, as they wait for
+// one another (bf16, 256 channels: 1 sequence of 32 rows 20 against 26, of 64 38
+// and 26; 16 of 64 39 and 33, of 512 278 and 71; 128 of 64 41 and 75, of 512 293
+// and 398; with 2560 channels 16 of 512 296 and 106, 128 of 64 72 and 116).  Of
+// sequences that differ the longest is taken to be three times the mean.
+bool tiled(int T, int S, bool packed) { return 250l * (packed ? 3 : 1) * T >= S * (10000l + 3l * T); }
 
 // Whether the tiles' outputs go by the caches: with long rows, whose tiles are
 // bound by memory (in training, us with and without: 65536 x 2560 bf16 706
@@ -794,7 +800,7 @@ int groups(int S, bool backward) {
 template <typename T, bool SIGMOID>
 hipError_t forward_t(const RecurrenceArgs& a, hipStream_t stream) {
   if (a.S == 0) return hipSuccess;
-  if (tiled(a.T, a.S)) {
+  if (tiled(a.T, a.S, a.offsets != nullptr)) {
     const TileLayout l = tile_layout(a.T, a.C, kWaves, false);
     const TileSpace ws = tile_space(a.ws, l);
     const hipError_t e = tile_setup(sequences(a), a.S, a.C, ws, l, a.h0, a.last, stream);
@@ -819,7 +825,7 @@ hipError_t backward_t(const RecurrenceArgs& a, hipStream_t stream) {
   float* part = !SIGMOID && a.dgate ? static_cast<float*>(a.ws) : nullptr;
   int units = a.S > 0 ? 4 * g : 0;
   hipError_t e = hipSuccess;
-  if (a.S > 0 && tiled(a.T, a.S)) {
+  if (a.S > 0 && tiled(a.T, a.S, a.offsets != nullptr)) {
     const TileLayout l = tile_layout(a.T, a.C, kWavesBackward, !SIGMOID);
     const TileSpace ws = tile_space(a.ws, l);
     if (part) part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + l.part);
@@ -847,13 +853,14 @@ hipError_t backward_t(const RecurrenceArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// (what packed sequences take is enough for those of equal length)
 size_t recurrence_workspace_bytes(int T, int S, int C, bool bf16, bool sigmoid) {
-  return tiled(T, S) ? tile_layout(T, C, kWaves, false).total : 0;
+  return tiled(T, S, true) ? tile_layout(T, C, kWaves, false).total : 0;
 }
 size_t recurrence_backward_workspace_bytes(int T, int S, int C, bool bf16, bool sigmoid) {
-  if (tiled(T, S)) return tile_layout(T, C, kWavesBackward, !sigmoid).total;
-  if (sigmoid) return 0;
-  return (size_t(groups(S, true)) * 4 * C * 4 + 255) & ~size_t(255);
+  const size_t tiles = tiled(T, S, true) ? tile_layout(T, C, kWavesBackward, !sigmoid).total : 0;
+  const size_t rows = sigmoid ? 0 : (size_t(groups(S, true)) * 4 * C * 4 + 255) & ~size_t(255);
+  return tiles > rows ? tiles : rows;
 }
 
 hipError_t launch_recurrence(const RecurrenceArgs& a, hipStream_t stream) {
