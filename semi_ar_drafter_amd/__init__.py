@@ -1,6 +1,8 @@
 """MI355X-native DSpark Markov-head draft / prefix-schedule / verify path,
 plus RNN-head drafting, parallel-only drafting, the sequential-temperature fit,
-the output projection (a linear layer with its epilogue) and the heads' training loss.
+the output projection (a linear layer with its epilogue), the heads' training loss, and
+a recurrent backbone's layer (normalisation, gated recurrence, gated feed-forward
+projection) with its gradients.
 
 The compute runs in hand-written HIP kernels for gfx950 behind the C ABI of
 ``libdspark.so`` (declared in ``include/dspark.h``).  This package only

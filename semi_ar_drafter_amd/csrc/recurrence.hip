@@ -11,6 +11,10 @@
 // The state is fp32 throughout; the rounding of h to the storage type is of
 // the output alone.  The gradient makes h_{t-1} again from the inputs, block
 // by block of 16 rows, from the fp32 states that the forward pass kept.
+//
+// Bound by memory, and with long sequences by the words that tiles pass on:
+// 65536 rows of 2560 take 257 us forward for 1.0 GB, 436 backward for 1.7 GB (212
+// and 358 without the words); a step of 256 sequences 3.9 us.
 #include "launch.h"
 #include "projection.h"
 
@@ -783,7 +787,8 @@ TileSpace tile_space(void* ws, const TileLayout& l) {
 }
 hipError_t tile_setup(const Sequences& seq, int S, int C, const TileSpace& ws, const TileLayout& l, const float* from,
                       float* to, hipStream_t stream) {
-  const size_t blocks = (l.words + 1023) / 1024;
+  const size_t fill = (l.words + 1023) / 1024, marks = (size_t(seq.T) / kBlock + 255) / 256;
+  const size_t blocks = fill > marks ? fill : marks > 0 ? marks : 1;
   hipLaunchKernelGGL(tile_setup_kernel, dim3(unsigned(blocks < 1024 ? blocks : 1024)), dim3(256), 0, stream, seq, S, C,
                      ws, l.words, from, to);
   return hipGetLastError();
@@ -791,9 +796,10 @@ hipError_t tile_setup(const Sequences& seq, int S, int C, const TileSpace& ws, c
 
 Sequences sequences(const RecurrenceArgs& a) { return {a.offsets, a.T, a.S > 0 ? a.T / a.S : 0}; }
 
-// Workgroups of four waves along the sequences.
-int groups(int S, bool backward) {
-  const int g = (S + 3) / 4, most = backward ? 256 : 16384;
+// Workgroups of four waves along the sequences; fewer where each wave leaves a
+// share of dgate.
+int groups(int S, bool shares) {
+  const int g = (S + 3) / 4, most = shares ? 256 : 16384;
   return g < most ? g : most;
 }
 
@@ -821,7 +827,7 @@ hipError_t forward_t(const RecurrenceArgs& a, hipStream_t stream) {
 
 template <typename T, bool SIGMOID>
 hipError_t backward_t(const RecurrenceArgs& a, hipStream_t stream) {
-  const int g = groups(a.S, true);
+  const int g = groups(a.S, !SIGMOID);
   float* part = !SIGMOID && a.dgate ? static_cast<float*>(a.ws) : nullptr;
   int units = a.S > 0 ? 4 * g : 0;
   hipError_t e = hipSuccess;
