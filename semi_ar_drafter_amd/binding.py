@@ -972,6 +972,8 @@ def norm_backward(dy, x, stat, weight=None, dsum=None, kind: str = "layer", need
     _optional(dx_out, "dx_out", x.dtype, (M, C), dev)
     k = _norm_kind(kind)
     need = _names(need, ("dx", "dweight", "dbias"))
+    if dx_out is not None and "dx" not in need:
+        raise ValueError("dx_out goes with dx")
     _fits(M, C)
     _no_graph("norm_backward", dy, x, stat, weight, dsum)
     with _on(dev), _launching:

@@ -445,7 +445,6 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
   // DUAL: of a half's 128 rows the first 64, which waves 0 and 1 load, are of A[0]
   const bf16_t* a0 = (DUAL && w4 >= 2 ? g.A[1].p : g.A[0].p) + (LA0 == kRows ? long(f0) * lda0 : long(f0));
   const bf16_t* a1 = g.A[1].p + (LA1 == kRows ? long(f1) * lda1 : long(f1));
-  const int unit_a = (DUAL ? w4 & 1 : w4) * 4;
   // kRows: from the wave's own 32 rows on, since 256 rows can be longer than a 32-bit offset reaches
   const int bf = LB == kRows ? min(b_first + wave * 32, nbo - 1) : b_first;
   const bf16_t* b0 = g.B[0].p + (LB == kRows ? long(bf) * ldb : long(bf));
@@ -470,7 +469,7 @@ __global__ __launch_bounds__(512) void tile256_kernel(Product<bf16_t> g, Epi epi
         const int n = second ? n1 - f1 : n0 - f0, vlane = here(lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          off_a[i] = unit_offset<LA0, 128>(unit_a + i, vlane, uint32_t(ld * 2), n, left);
+          off_a[i] = unit_offset<LA0, 128>((DUAL ? w4 & 1 : w4) * 4 + i, vlane, uint32_t(ld * 2), n, left);
       }
     } else {
       rsrc_a = make_rsrc(a1 + (LA1 == kRows ? long(k) : long(k) * lda1));

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(Sh::threads) void tile_f32_kernel(Product<float> g,
   auto load = [&](int s) {
     const int part = s >= T0;
     const int k = (part ? s - T0 : s) * kStepF32, K = part ? K1 : K0;
-    sa.load(g.A[part], a_first, k, K, tid, g.A[1].p);
+    sa.load(g.A[part], a_first, k, K, tid, DUAL ? g.A[1].p : nullptr);
     sb.load(g.B[part], b_first, k, K, tid);
   };
   if (t_begin < t_end) load(t_begin);

@@ -270,6 +270,8 @@ def test_refusals():
         norm(torch.zeros((1, 32769), device=DEV))
     with pytest.raises(ValueError):
         norm_backward(x, x, stat, need=("dw",))
+    with pytest.raises(ValueError):
+        norm_backward(x, x, stat, need="dbias", dx_out=torch.empty_like(x))
     w = torch.ones(64, device=DEV, requires_grad=True)
     with pytest.raises(RuntimeError, match="autograd"):
         norm(x, w)
