@@ -27,7 +27,8 @@ from layers import DEV, HALF, IDS, TYPES, U32, generator, guarded, rand, replays
 ACTS = ["none", "relu", "gelu", "silu"]
 SHAPES = [(1, 1, 1), (1, 17, 8), (2, 3, 5), (1, 130, 64), (3, 64, 200), (8, 256, 64), (16, 300, 129), (17, 33, 65),
           (31, 128, 72), (64, 256, 128), (77, 131, 1001), (129, 257, 192), (255, 520, 333), (300, 512, 256),
-          (1, 4096, 520), (8, 2000, 2056), (513, 96, 40), (257, 1027, 136), (16, 5000, 64), (40, 64, 4096)]
+          (1, 4096, 520), (8, 2000, 2056), (513, 96, 40), (257, 1027, 136), (16, 5000, 64), (40, 64, 4096), (3, 50, 1001), (16, 33, 191),
+          (1, 70, 4095), (5, 19, 127)]
 NAMES = ("dx", "dwg", "dwu", "dbg", "dbu")
 
 
