@@ -602,13 +602,18 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
 }
 
 // Backwards: tiles, waves and rows in the other order; what passes from row to
-// row is e = a d, e -> a (dh + e).
+// row is e = a d, e -> a (dh + e).  dlast is read before the pair is published
+// and not again: behind that, the wave of the sequence's first row may have
+// written dh0, which may be dlast itself.  LDS keeps it (65536 rows of 2560 in
+// training 702 us; in registers 745, which leave two workgroups of bf16 to a
+// compute unit instead of three).
 template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
     TileSpace ws, int tiles, int C, const T* __restrict__ dh, const T* __restrict__ x, const void* __restrict__ gate,
     const float* __restrict__ h0, const float* dlast, const float* __restrict__ states, T* __restrict__ dx,
     T* __restrict__ dg, float* dh0, float* __restrict__ part, bool past) {
   __shared__ TileLds<W> lds;
+  __shared__ float2 ends[W][kBlock][64];   // dlast where a sequence ends
   int k, c0;
   take_tile(ws, C, &k, &c0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -680,9 +685,8 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
         if (r.has(i)) {
           if (r.ends(i)) {
             const State2 e = of_sequence(dlast, ws, r, i, C, c, both);
-            p.a0 = p.a1 = 0.f;
-            p.b0 = e.v0;
-            p.b1 = e.v1;
+            ends[wave][i][lane] = make_float2(e.v0, e.v1);
+            p = {0.f, e.v0, 0.f, e.v1};
           }
           p.b0 = gate0(i) * (pd[i].get(0) + p.b0);
           p.b1 = gate1(i) * (pd[i].get(1) + p.b1);
@@ -716,7 +720,7 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
 #pragma unroll
       for (int i = kBlock - 1; i >= 0; --i)
         if (r.has(i)) {
-          if (r.ends(i)) e = of_sequence(dlast, ws, r, i, C, c, both);
+          if (r.ends(i)) e = {ends[wave][i][lane].x, ends[wave][i][lane].y};
           row(i);
           if (dh0 && r.begins(i)) store2(dh0 + size_t(ws.owner[r.t0 + i]) * C + c, e.v0, e.v1, both);
         }
