@@ -797,7 +797,8 @@ size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
  *                 Calls that can overlap need separate ones.
  * All arrays need element alignment only.  Outputs or a workspace that overlap
  * another array are refused, but for last == h0.  Results do not depend on
- * execution order, and no sequence's values on another's.  Of long sequences
+ * execution order, and no sequence's values on another's.  A state that is not
+ * finite stays so to its sequence's end, in its channel.  Of long sequences
  * different workgroups make different rows and wait for one another; the waits
  * are bounded (seconds), and a state that has not come by then is NaN.
  * Limits: T <= 2^24, S <= 2^20, C <= 65536.

@@ -270,17 +270,25 @@ __global__ __launch_bounds__(256) void gate_join_kernel(int C, int units, const 
 // and itself waits for lower numbers only.  (One counter for all channels
 // hands out a number every 56 ns: 10240 tiles then took 577 us.)
 //
-// Where a sequence begins, A = 0 and B holds what its h0 gives: join() then
-// ignores the state before, whatever it is.
+// Where a sequence begins, A is NaN, which all products keep, and B holds what
+// its h0 gives: join() then ignores the state before, whatever it is.  (A gate
+// that is NaN makes B NaN as well.)  A product of gates that has become 0 (300
+// rows of ordinary gates are enough) is published as the smallest value that is
+// not, so that an infinity or NaN before it goes on to the sequence's end, as it
+// does row after row.  To a finite state that adds 2^-149 of itself, less than
+// 2^-21.
 constexpr int kSub = 8, kGroup = 64;
 constexpr int kSpin = 1 << 22;   // polls of a few hundred nanoseconds; a state not seen by then is NaN
 constexpr uint64_t kEmpty = ~uint64_t(0);
 constexpr int kLine = 32;   // 32-bit words
 
 __device__ __forceinline__ float join(float a, float b, float before) {
-  return a == 0.f || before == 0.f ? b : fmaf(a, before, b);
+  return a != a || before == 0.f ? b : fmaf(a, before, b);
 }
-__device__ __forceinline__ float join_factor(float a, float before) { return a == 0.f ? 0.f : a * before; }
+// A of rows with the product a of gates; begun: one of them begins a sequence.
+__device__ __forceinline__ float factor(float a, bool begun = false) {
+  return begun ? __uint_as_float(0x7FC00000u) : a == 0.f ? copysignf(__uint_as_float(1u), a) : a;
+}
 
 // A published pair in one 64-bit word, written and read whole: no order between
 // memory accesses is needed.  All ones mean that it is not there yet.
@@ -364,13 +372,13 @@ struct Pair2 {
   float a0 = 1.f, b0 = 0.f, a1 = 1.f, b1 = 0.f;
   __device__ __forceinline__ void behind(const float4& p) {
     b0 = join(p.x, p.y, b0);
-    a0 = join_factor(p.x, a0);
+    a0 *= p.x;
     b1 = join(p.z, p.w, b1);
-    a1 = join_factor(p.z, a1);
+    a1 *= p.z;
   }
   __device__ __forceinline__ void to(uint64_t* at, bool both) const {
-    publish(at, a0, b0);
-    if (both) publish(at + 1, a1, b1);
+    publish(at, factor(a0), b0);
+    if (both) publish(at + 1, factor(a1), b1);
   }
 };
 
@@ -522,8 +530,7 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
     decay0 = static_cast<const float*>(gate)[c];
     decay1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
   }
-  // a row: state -> a state + b; one that is not there changes nothing, and the
-  // first of a sequence (a = 0, b from its h0) forgets what was before
+  // a row: state -> a state + b; the first of a sequence: b, from its h0
   float a0[kBlock], a1[kBlock], b0[kBlock], b1[kBlock];
   Pair2 p;
   if (live) {
@@ -562,21 +569,25 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
       for (int i = 0; i < kBlock; ++i)
         if (r.has(i)) load(i);
 #pragma unroll
-      for (int i = 0; i < kBlock; ++i) {
-        a0[i] = a1[i] = 1.f;
-        b0[i] = b1[i] = 0.f;
+      for (int i = 0; i < kBlock; ++i)
         if (r.has(i)) {
           make(i);
           if (r.begins(i)) {
             const State2 v = of_sequence(h0, ws, r, i, C, c, both);
             b0[i] = fmaf(a0[i], v.v0, b0[i]);
             b1[i] = fmaf(a1[i], v.v1, b1[i]);
-            a0[i] = a1[i] = 0.f;
+            p.b0 = b0[i];
+            p.b1 = b1[i];
+          } else {
+            p.b0 = fmaf(a0[i], p.b0, b0[i]);
+            p.b1 = fmaf(a1[i], p.b1, b1[i]);
           }
+          p.a0 *= a0[i];
+          p.a1 *= a1[i];
         }
-        p.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
-      }
     }
+    p.a0 = factor(p.a0, r.marks & 0xFFFFu);
+    p.a1 = factor(p.a1, r.marks & 0xFFFFu);
   }
   lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
   State2 v = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);
@@ -594,7 +605,7 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
 #pragma unroll
     for (int i = 0; i < kBlock; ++i)
       if (r.has(i)) {
-        v.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
+        v = r.begins(i) ? State2{b0[i], b1[i]} : State2{fmaf(a0[i], v.v0, b0[i]), fmaf(a1[i], v.v1, b1[i])};
         store2(out + size_t(i) * C, v.v0, v.v1, both, past);
         if (last && r.ends(i)) store2(last + size_t(ws.owner[r.t0 + i]) * C + c, v.v0, v.v1, both);
       }
@@ -686,14 +697,17 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
           if (r.ends(i)) {
             const State2 e = of_sequence(dlast, ws, r, i, C, c, both);
             ends[wave][i][lane] = make_float2(e.v0, e.v1);
-            p = {0.f, e.v0, 0.f, e.v1};
+            p.b0 = e.v0;
+            p.b1 = e.v1;
           }
           p.b0 = gate0(i) * (pd[i].get(0) + p.b0);
           p.b1 = gate1(i) * (pd[i].get(1) + p.b1);
-          p.a0 = join_factor(p.a0, gate0(i));
-          p.a1 = join_factor(p.a1, gate1(i));
+          p.a0 *= gate0(i);
+          p.a1 *= gate1(i);
         }
     }
+    p.a0 = factor(p.a0, r.marks >> 16);
+    p.a1 = factor(p.a1, r.marks >> 16);
   }
   lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
   State2 e = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);

@@ -1,5 +1,5 @@
 """recurrence() and its gradient: the states' gradient in the place of its
-input."""
+input, states that are not finite, gates of zero."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +58,85 @@ def test_gradient_of_the_states_in_place(lengths, C, kind, dtype):
         assert torch.equal(place, want[2]) and torch.equal(dx, want[0]) and torch.equal(dg, want[1]), turn
     if p is not None:
         forms.within(place.cpu(), p.dh0, p.dh0_tol, "dh0")
+
+
+# rows of sequences, and which of them the tests touch: by tiles, whose gates'
+# product falls below the smallest fp32 value over their rows, and row by row
+LONG = [([4000], 0), ([700, 0, 9000, 300], 2), ([2100, 5000], 0), ([100] * 400, 7)]
+
+
+def gates_and(lengths, C, dtype, kind):
+    x, gate, h0, offsets, dh, dlast = forms.inputs(lengths, C, dtype, kind)
+    if kind == "decay":      # none that remembers nothing
+        gate = torch.where(gate == 0, torch.full_like(gate, 0.4), gate)
+    return x, gate, h0, offsets, dh, dlast
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lengths,at", LONG)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")], ids=["nan", "inf", "-inf"])
+def test_a_state_that_is_not_finite_stays_so_to_its_sequences_end(value, lengths, at, kind, dtype):
+    """h = a h + b with a > 0 and b finite: an infinity stays that infinity, NaN
+    NaN, and nothing else changes; the gradient the same in the other order."""
+    C = 70
+    say(f"[case] {value} in {len(lengths)} sequences {kind} {dtype}")
+    x, gate, h0, offsets, dh, dlast = gates_and(lengths, C, dtype, kind)
+    if kind == "decay":
+        gate = gate.abs()
+    begin = sum(lengths[:at])
+    end, S, T = begin + lengths[at], len(lengths), x.shape[0]
+    clean_last, clean_states = torch.empty_like(h0), forms.kept(T, C)
+    clean = recurrence(x, gate, kind, offsets=offsets, h0=h0, last=clean_last, states=clean_states)
+    grads = recurrence_backward(dh, x, gate, clean_states, kind, offsets=offsets, h0=h0, dlast=dlast)
+    same = (lambda t: t.isnan()) if value != value else (lambda t: t == value)  # noqa: E731
+    for row in (begin, begin + 20):
+        bad, bad0 = x.clone(), h0.clone()
+        bad[row, 3] = value
+        bad0[at, 5] = value
+        last, states = torch.empty_like(h0), forms.kept(T, C)
+        h = recurrence(bad, gate, kind, offsets=offsets, h0=bad0, last=last, states=states)
+        hit, ends = torch.zeros_like(h, dtype=torch.bool), torch.zeros_like(last, dtype=torch.bool)
+        hit[row:end, 3], hit[begin:end, 5], ends[at, 3], ends[at, 5] = True, True, True, True
+        assert same(h[hit]).all() and same(last[ends]).all()
+        assert torch.equal(h[~hit], clean[~hit]) and torch.equal(last[~ends], clean_last[~ends])
+        # the states kept are those of h: the gradient of the gate reads them
+        dgate = recurrence_backward(dh, bad, gate, states, kind, offsets=offsets, h0=bad0, dlast=dlast)[1]
+        if kind == "sigmoid":
+            touched = torch.zeros_like(hit)
+            touched[row:end, 3], touched[begin:end, 5] = True, True
+            assert not dgate[touched].isfinite().any() and torch.equal(dgate[~touched], grads[1][~touched])
+        else:
+            assert not dgate[3].isfinite() and not dgate[5].isfinite() and dgate[6:].isfinite().all()
+    for row in (end - 1, end - 21):
+        bad, bad_last = dh.clone(), dlast.clone()
+        bad[row, 3] = value
+        bad_last[at, 5] = value
+        dx, dgate, dh0 = recurrence_backward(bad, x, gate, clean_states, kind, offsets=offsets, h0=h0, dlast=bad_last)
+        hit, ends = torch.zeros_like(dx, dtype=torch.bool), torch.zeros_like(dh0, dtype=torch.bool)
+        hit[begin:row + 1, 3], hit[begin:end, 5], ends[at, 3], ends[at, 5] = True, True, True, True
+        assert same(dx[hit]).all() and same(dh0[ends]).all()
+        assert torch.equal(dx[~hit], grads[0][~hit]) and torch.equal(dh0[~ends], grads[2][~ends])
+        if kind == "sigmoid":
+            assert not dgate[hit].isfinite().any() and torch.equal(dgate[~hit], grads[1][~hit])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_gate_of_zero_forgets_a_finite_state(kind):
+    """Rows whose gate is 0 in the middle of tiles, and at their ends, whatever
+    finite state came before; rows behind them are those of a sequence that
+    begins there."""
+    T, C = 3000, 130
+    x, gate, _, _, _, _ = forms.inputs([T], C, torch.float32, kind)
+    if kind == "decay":
+        gate = torch.zeros_like(gate)
+        assert torch.equal(recurrence(x, gate, kind, h0=torch.full((1, C), 1e30, device=DEV)), x)
+        return
+    cuts = [0, 5, 128, 1023, 1024, 2048, 2999]
+    for c in cuts:
+        gate[c] = float("-inf")
+    first = torch.full((1, C), 1e30, device=DEV)
+    h = recurrence(x, gate, h0=first)
+    for a, b in zip(cuts, cuts[1:] + [T]):
+        p = forms.Plain([b - a], x[a:b], gate[a:b], kind, None)
+        forms.within(h[a:b].cpu(), p.h, p.h_tol, f"rows from {a}")
