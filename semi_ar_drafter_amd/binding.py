@@ -632,8 +632,15 @@ def _optional(t, name, dtype, shape, device):
 
 def _no_graph(name, *tensors):
     """The operators record nothing for autograd: a tensor whose gradient it
-    would be asked for is refused rather than cut off silently."""
-    if _torch().is_grad_enabled():
+    would be asked for, or that carries a forward-mode tangent (without a
+    gradient mode to turn off), is refused rather than cut off silently."""
+    torch = _torch()
+    forward = torch.autograd.forward_ad
+    if forward._current_level >= 0:      # some dual level is open: unpack_dual() costs a microsecond a tensor
+        for t in tensors:
+            if t is not None and forward.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{name}() carries no tangents for forward-mode autograd: call it on detached tensors")
+    if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise RuntimeError(f"{name}() records no graph for autograd: call it under torch.no_grad() (or on "
@@ -713,7 +720,8 @@ def linear(x, w, bias=None, act: str = "none", residual=None, pre=None, out=None
     function) or "silu".  `pre`, a float32 [M, N] tensor, receives
     x @ w.T + bias for linear_backward.  `out` takes y; it may be `residual`.
     Nothing is recorded for autograd: inputs that require a gradient are
-    refused while torch's gradient mode is on."""
+    refused while torch's gradient mode is on, and inputs with a forward-mode
+    tangent always."""
     torch = _torch()
     lib = load()
     dt = _storage(x, "x")
