@@ -66,21 +66,28 @@ __device__ __forceinline__ void store2(T* p, float a, float b, bool both, bool p
 }
 
 // a = 1 / (1 + exp(-g)) and 1 - a = exp(-g) a, each to its own relative accuracy:
-// nothing cancels for gates near 1.  exp(-g) is held below 2^120, so that the
-// product with a = 2^-120 stays 1; minimum() passes NaN on.  For bf16 logits by
-// the hardware's base-2 exponential and reciprocal (one unit in the last place
-// each: a is off by 2^-23, which a state multiplies by the rows that it lives).
+// nothing cancels for gates near 1.  From g = -87 on, where a falls below 2^-125,
+// it is 0 and 1 - a is 1; minimum() passes NaN on.  For bf16 logits the
+// exponential is the hardware's of base 2, with log2(e) = HI + the rest: g HI is
+// exact, as HI has 16 bits, and the rest enters as exp(-g REST) to first order
+// (off by 2^-23 at |g| = 87); the reciprocal is the hardware's, off by one unit in
+// the last place.  (Without that product and the 0 for far logits 65536 rows of
+// 2560 in training take 709 us instead of 725, and 1 - a is off by |g| 2^-24.)
 template <typename T>
 __device__ __forceinline__ void gate_of(float g, float* a, float* rest) {
+  const float m = __builtin_elementwise_minimum(-g, 87.f);
+  float e, r;
   if constexpr (sizeof(T) == 4) {
-    const float e = expf(__builtin_elementwise_minimum(-g, 83.f));
-    *a = 1.f / (1.f + e);
-    *rest = e * *a;
+    e = expf(m);
+    r = 1.f / (1.f + e);
   } else {
-    const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(g * -1.44269504088896341f, 120.f));
-    *a = __builtin_amdgcn_rcpf(1.f + e);
-    *rest = e * *a;
+    constexpr float HI = 1.44268798828125f, REST = 4.888495152e-06f;   // REST = 1 - HI ln 2
+    e = __builtin_amdgcn_exp2f(m * HI);
+    e = fmaf(e, __builtin_elementwise_maximum(m, -200.f) * REST, e);   // (not 0 times infinity)
+    r = __builtin_amdgcn_rcpf(1.f + e);
   }
+  *a = m >= 87.f ? 0.f : r;
+  *rest = e * r;
 }
 
 // First and last row (exclusive) of sequence s.

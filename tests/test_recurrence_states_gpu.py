@@ -140,3 +140,37 @@ def test_a_gate_of_zero_forgets_a_finite_state(kind):
     for a, b in zip(cuts, cuts[1:] + [T]):
         p = forms.Plain([b - a], x[a:b], gate[a:b], kind, None)
         forms.within(h[a:b].cpu(), p.h, p.h_tol, f"rows from {a}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_gates_keep_their_relative_accuracy(dtype):
+    """a and 1 - a of a logit, each by itself: a state of 2^60 and no input
+    leaves a 2^60, an input of 1 and no state 1 - a.  At worst one is off by 2 u
+    for the exponential, 3 for its correction, 1 for the sum, 2 for the reciprocal
+    and 1 for the product: 12 u are enough."""
+    from layers import U32
+    g = torch.arange(-86.0, 86.25, 0.25).to(dtype).unique()
+    S = len(g)
+    gate = g.view(S, 1).to(DEV).contiguous()
+    want = torch.sigmoid(g.double())
+    rest = torch.sigmoid(-g.double())
+    for rows in (1, 700):                       # one wave's sequences; tiles
+        x = torch.zeros((rows, S), device=DEV, dtype=dtype)
+        h0, last = torch.full((1, S), 2.0 ** 60, device=DEV), torch.empty((1, S), device=DEV)
+        logits = gate.view(1, S).expand(rows, S).contiguous()
+        if rows > 1:                            # all but one row keep the state
+            logits[1:] = float("inf")
+        recurrence(x, logits, sequences=1, h0=h0, last=last)
+        forms.within(last[0].cpu() * 2.0 ** -60, want, 12 * U32 * want, "a")
+        x[0] = 1
+        recurrence(x, logits, sequences=1, last=last)
+        forms.within(last[0].cpu(), rest, 12 * U32 * rest, "1 - a")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_a_logit_of_minus_infinity_is_a_gate_of_zero(dtype):
+    x = torch.zeros((40, 2), device=DEV, dtype=dtype)
+    gate = torch.zeros_like(x)
+    gate[0], gate[20] = float("-inf"), torch.finfo(dtype).min
+    h0, last = torch.full((1, 2), 1e30, device=DEV), torch.empty((1, 2), device=DEV)
+    assert not recurrence(x, gate, h0=h0, last=last).any() and not last.any()
