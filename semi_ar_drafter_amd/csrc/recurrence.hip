@@ -771,8 +771,12 @@ constexpr int kWaves = 8, kWavesBackward = 4;
 // one another (bf16, 256 channels: 1 sequence of 32 rows 20 against 26, of 64 38
 // and 26; 16 of 64 39 and 33, of 512 278 and 71; 128 of 64 41 and 75, of 512 293
 // and 398; with 2560 channels 16 of 512 296 and 106, 128 of 64 72 and 116).  Of
-// sequences that differ the longest is taken to be three times the mean.
-bool tiled(int T, int S, bool packed) { return 250l * (packed ? 3 : 1) * T >= S * (10000l + 3l * T); }
+// sequences that differ the longest is taken to be three times the mean, or all
+// rows of one or two (one of 20 rows 17 us against 25, of 32 22 and 25, of 48 25
+// by tiles).  The host does not see the lengths: where one of hundreds of
+// sequences has nearly all rows, it is gone through row by row all the same (511
+// of 3 rows and one of 64000, 2560 channels: 38 ms, with 12 sequences 0.68).
+bool tiled(int T, int S, bool packed) { return 250l * (packed ? S < 3 ? S : 3 : 1) * T >= S * (10000l + 3l * T); }
 
 // Whether the tiles' outputs go by the caches: with long rows, whose tiles are
 // bound by memory (in training, us with and without: 65536 x 2560 bf16 706
