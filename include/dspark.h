@@ -783,7 +783,10 @@ size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
  *                 Rows from offsets[S] on are left as they were.  NULL: T / S
  *                 rows each (S divides T).  Offsets outside [0, T] are cut to it.
  *   x         [T][C]
- *   gate      [T][C] in the storage type (SIGMOID), or fp32 [C] (DECAY)
+ *   gate      [T][C] in the storage type (SIGMOID), or fp32 [C] (DECAY), of any
+ *                 sign, magnitude up to 1.09: with more the product over 1024 rows,
+ *                 which long sequences are joined by, overflows, and a state that
+ *                 step by step would be finite may be infinite or NaN.
  *   h0   fp32 [S][C] or NULL (zeros)
  *   h         [T][C] out
  *   last fp32 [S][C] out, or NULL: the state after each sequence's last row

@@ -1033,9 +1033,9 @@ def recurrence(x, gate, kind: str = "sigmoid", offsets=None, sequences=None, h0=
     h [T, C].
 
     kind "sigmoid": a = sigmoid(gate), b = (1 - a) * x, with gate [T, C] of x's
-    type; kind "decay": a = gate, a float32 [C], b = x (the RNN head's state,
-    without rounding it at every step).  x [T, C] is float32 or bfloat16; the
-    state is carried in float32.
+    type; kind "decay": a = gate, a float32 [C] of magnitudes up to 1.09, b = x
+    (the RNN head's state, without rounding it at every step).  x [T, C] is
+    float32 or bfloat16; the state is carried in float32.
 
     Sequences: `offsets`, int32 [S + 1], of packed ones (rows behind the last
     are left as they were in `out`), or `sequences` of equal length (by default

@@ -174,3 +174,42 @@ def test_a_logit_of_minus_infinity_is_a_gate_of_zero(dtype):
     gate[0], gate[20] = float("-inf"), torch.finfo(dtype).min
     h0, last = torch.full((1, 2), 1e30, device=DEV), torch.empty((1, 2), device=DEV)
     assert not recurrence(x, gate, h0=h0, last=last).any() and not last.any()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("lengths", [[1500], [700, 0, 1400], [3, 40, 17] * 20])
+def test_decays_above_one(lengths, dtype):
+    """States that grow, up to 1.05^1500 = 6e31, with factors of both signs."""
+    C = 130
+    say(f"[case] growing states {lengths[:3]} {dtype}")
+    x, gate, h0, offsets, dh, dlast = forms.inputs(lengths, C, dtype, "decay")
+    gate = torch.linspace(0.99, 1.05, C, device=DEV)
+    gate[::3] *= -1
+    gate[7] = 1.0
+    T, S = x.shape[0], len(lengths)
+    states, last = forms.kept(T, C), torch.empty_like(h0)
+    p = forms.Plain(lengths, x, gate, "decay", h0, dh, dlast)
+    h = recurrence(x, gate, "decay", offsets=offsets, h0=h0, states=states, last=last)
+    forms.within(h.cpu(), p.h, p.h_tol, "h")
+    forms.within(last.cpu(), p.last, p.last_tol, "last")
+    dx, dg, d0 = recurrence_backward(dh, x, gate, states, "decay", offsets=offsets, h0=h0, dlast=dlast)
+    forms.within(dx.cpu(), p.dx, p.dx_tol, "dx")
+    forms.within(d0.cpu(), p.dh0, p.dh0_tol, "dh0")
+    small = gate.abs().cpu() < 1.02      # the other gradients' products of states leave fp32
+    forms.within(dg.cpu()[small], p.dgate[small], p.dgate_tol[small], "dgate")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_a_largest_decay_over_many_tiles(dtype):
+    """1.09 from a state of 0: zeros stay zeros whatever the product of the gates
+    has become, and a state that begins late is what it is step by step."""
+    T, C = 4000, 6
+    x = torch.zeros((T, C), device=DEV, dtype=dtype)
+    x[3300:, 1] = 1.0
+    x[3990:, 2] = 1e-30
+    gate = torch.full((C,), 1.09, device=DEV)
+    h = recurrence(x, gate, "decay")
+    assert not h[:, [0, 3, 4, 5]].any() and not h[:3300, 1].any() and not h[:3990, 2].any()
+    for c, n in ((1, 700), (2, 10)):
+        p = forms.Plain([n], x[-n:, c:c + 1], gate[:1], "decay", None)
+        forms.within(h[-n:, c:c + 1].cpu(), p.h, p.h_tol, f"channel {c}")
