@@ -48,7 +48,11 @@ template <> struct Pair<float> {
   }
   __device__ __forceinline__ float get(int i) const { return __uint_as_float(raw[i]); }
 };
-// past: by the caches, which need not keep it.
+// past: by the caches, which need not keep it: so tiles write h and the gradients
+// (forward, and in training with what reads them next, us with and without, bf16: 65536 x
+// 2560 283 against 298 and 1110 against 1143, 16384 x 512 42 and 43, 145 and 144,
+// 1024 x 1024 14.3 and 14.4, 42 and 42; fp32: 65536 x 1600 273 and 292, 1244 and
+// 1297, 1024 x 1024 16.5 and 17.3, 48 and 52).
 template <typename T>
 __device__ __forceinline__ void store2(T* p, float a, float b, bool both, bool past = false) {
   if (both && past) {
@@ -522,7 +526,7 @@ __device__ __forceinline__ State2 of_sequence(const float* v, const TileSpace& w
 template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles, int C, const T* __restrict__ x,
                                                       const void* __restrict__ gate, const float* h0, T* __restrict__ h,
-                                                      float* last, float* __restrict__ states, bool past) {
+                                                      float* last, float* __restrict__ states) {
   __shared__ TileLds<W> lds;
   int k, c0;
   take_tile(ws, C, &k, &c0);
@@ -606,14 +610,14 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
     for (int i = 0; i < kBlock; ++i) {
       v.v0 = fmaf(a0[i], v.v0, b0[i]);
       v.v1 = fmaf(a1[i], v.v1, b1[i]);
-      store2(out + size_t(i) * C, v.v0, v.v1, both, past);
+      store2(out + size_t(i) * C, v.v0, v.v1, both, true);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kBlock; ++i)
       if (r.has(i)) {
         v = r.begins(i) ? State2{b0[i], b1[i]} : State2{fmaf(a0[i], v.v0, b0[i]), fmaf(a1[i], v.v1, b1[i])};
-        store2(out + size_t(i) * C, v.v0, v.v1, both, past);
+        store2(out + size_t(i) * C, v.v0, v.v1, both, true);
         if (last && r.ends(i)) store2(last + size_t(ws.owner[r.t0 + i]) * C + c, v.v0, v.v1, both);
       }
   }
@@ -629,7 +633,7 @@ template <typename T, bool SIGMOID, int W>
 __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
     TileSpace ws, int tiles, int C, const T* __restrict__ dh, const T* __restrict__ x, const void* __restrict__ gate,
     const float* __restrict__ h0, const float* dlast, const float* __restrict__ states, T* __restrict__ dx,
-    T* __restrict__ dg, float* dh0, float* __restrict__ part, bool past) {
+    T* __restrict__ dg, float* dh0, float* __restrict__ part) {
   __shared__ TileLds<W> lds;
   __shared__ float2 ends[W][kBlock][64];   // dlast where a sequence ends
   int k, c0;
@@ -725,10 +729,10 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
       const size_t at = size_t(r.t0 + i) * C + c;
       if (SIGMOID) {
         const float u0 = d0 * r0[i], u1 = d1 * r1[i];
-        if (dx) store2(dx + at, u0, u1, both, past);
-        if (dg) store2(dg + at, u0 * w0[i], u1 * w1[i], both, past);
+        if (dx) store2(dx + at, u0, u1, both, true);
+        if (dg) store2(dg + at, u0 * w0[i], u1 * w1[i], both, true);
       } else {
-        if (dx) store2(dx + at, d0, d1, both, past);
+        if (dx) store2(dx + at, d0, d1, both, true);
         sum0 = fmaf(d0, w0[i], sum0);
         sum1 = fmaf(d1, w1[i], sum1);
       }
@@ -777,13 +781,6 @@ constexpr int kWaves = 8, kWavesBackward = 4;
 // sequences has nearly all rows, it is gone through row by row all the same (511
 // of 3 rows and one of 64000, 2560 channels: 38 ms, with 12 sequences 0.68).
 bool tiled(int T, int S, bool packed) { return 250l * (packed ? S < 3 ? S : 3 : 1) * T >= S * (10000l + 3l * T); }
-
-// Whether the tiles' outputs go by the caches: with long rows, whose tiles are
-// bound by memory (in training, us with and without: 65536 x 2560 bf16 706
-// against 837, 16384 x 2560 178 and 221, 8192 x 1001 fp32 90 and 135); with
-// short ones a tile waits for the one before, and for its stores (16384 x 1024
-// bf16 122 against 108, x 512 120 against 97).
-bool past_caches(int C, size_t elem) { return C * elem >= 4000; }
 
 // Offsets of TileSpace's parts, and of dgate's shares behind them.
 struct TileLayout {
@@ -842,7 +839,7 @@ hipError_t forward_t(const RecurrenceArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((tile_kernel<T, SIGMOID, kWaves>), dim3(unsigned(l.tiles) * ((a.C + 127) / 128)),
                        dim3(64 * kWaves), 0, stream, ws, l.tiles, a.C, static_cast<const T*>(a.x), a.gate, a.h0,
-                       static_cast<T*>(a.h), a.last, a.states, past_caches(a.C, sizeof(T)));
+                       static_cast<T*>(a.h), a.last, a.states);
     return hipGetLastError();
   }
   const dim3 grid((a.C + 127) / 128, groups(a.S, false));
@@ -870,8 +867,7 @@ hipError_t backward_t(const RecurrenceArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((tile_backward_kernel<T, SIGMOID, kWavesBackward>),
                        dim3(unsigned(l.tiles) * ((a.C + 127) / 128)), dim3(64 * kWavesBackward), 0, stream, ws, l.tiles,
                        a.C, static_cast<const T*>(a.dh), static_cast<const T*>(a.x), a.gate, a.h0, a.dlast,
-                       a.states_in, static_cast<T*>(a.dx), SIGMOID ? static_cast<T*>(a.dgate) : nullptr, a.dh0, part,
-                       past_caches(a.C, sizeof(T)));
+                       a.states_in, static_cast<T*>(a.dx), SIGMOID ? static_cast<T*>(a.dgate) : nullptr, a.dh0, part);
     e = hipGetLastError();
   } else if (a.S > 0) {
     hipLaunchKernelGGL((rows_backward_kernel<T, SIGMOID>), dim3((a.C + 127) / 128, g), dim3(256), 0, stream,
