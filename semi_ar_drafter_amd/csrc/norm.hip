@@ -436,9 +436,12 @@ hipError_t norm_t(const NormArgs& a, hipStream_t stream) {
 }
 
 // Whether dw and db are made beside dx in one launch, from the inputs again,
-// instead of from shares in a second one (forward and backward, us, bf16: 128 x
-// 2560 9.2 against 13.3, 512 x 2560 13.9 against 18.2, 512 x 1001 16.4 against
-// 16.8, 1024 x 1001 27 against 23).
+// instead of from shares in a second one (forward and backward, us, bf16: 64 x
+// 64 6.7 against 9.0, 128 x 2560 7.8 and 13.1, 512 x 1001 12.8 and 14.9, 512 x
+// 5120 18.6 and 24.2, 512 x 32768 181 and 190, 1024 x 256 14.9 and 14.0, 1024 x
+// 32768 390 and 374; fp32: 512 x 1001 10.4 and 14.2, 512 x 5120 20.9 and 23.5, 1024
+// x 2560 28.1 and 23.7; only fp32 rows of 16384 channels and more lose at 512, 74
+// and 70).
 bool beside(int M) { return M <= 512; }
 
 template <typename T, bool CENTER>
