@@ -13,8 +13,9 @@
 // by block of 16 rows, from the fp32 states that the forward pass kept.
 //
 // Bound by memory, and with long sequences by the words that tiles pass on:
-// 65536 rows of 2560 take 257 us forward for 1.0 GB, 436 backward for 1.7 GB (212
-// and 358 without the words); a step of 256 sequences 3.9 us.
+// 65536 rows of 2560 take 275 us forward for 1.0 GB, 441 backward for 1.7 GB, in
+// training 724 together with their setup (the same loads and stores without the
+// words: 212 and 358, with cheaper gates); a step of 256 sequences 3.9 us.
 #include "launch.h"
 #include "projection.h"
 
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(256) void gate_join_kernel(int C, int units, const 
 // makes its (A, B), LDS joins the waves', and the tile's pair is published.
 // Every kSub-th tile publishes the pair of the last kSub, and every kGroup-th
 // the state behind it; a tile folds, in order, the last such state, the pairs
-// of kSub tiles since then and the single ones since then: 14 words at most,
+// of kSub tiles since then and the single ones since then: 15 words at most,
 // and the tiles wait for one another in a row once in kGroup only.  The order
 // of all sums is fixed: results do not depend on which tile comes first.
 //
@@ -293,13 +294,12 @@ constexpr int kSpin = 1 << 22;   // polls of a few hundred nanoseconds; a state 
 constexpr uint64_t kEmpty = ~uint64_t(0);
 constexpr int kLine = 32;   // 32-bit words
 
+constexpr float kBegins = __builtin_nanf("");   // A where a sequence begins
 __device__ __forceinline__ float join(float a, float b, float before) {
   return a != a || before == 0.f ? b : fmaf(a, before, b);
 }
-// A of rows with the product a of gates; begun: one of them begins a sequence.
-__device__ __forceinline__ float factor(float a, bool begun = false) {
-  return begun ? __uint_as_float(0x7FC00000u) : a == 0.f ? copysignf(__uint_as_float(1u), a) : a;
-}
+// A of rows with the product a of gates and marks.
+__device__ __forceinline__ float factor(float a) { return a == 0.f ? copysignf(__uint_as_float(1u), a) : a; }
 
 // A published pair in one 64-bit word, written and read whole: no order between
 // memory accesses is needed.  All ones mean that it is not there yet.
@@ -541,7 +541,8 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
     decay0 = static_cast<const float*>(gate)[c];
     decay1 = both ? static_cast<const float*>(gate)[c + 1] : 0.f;
   }
-  // a row: state -> a state + b; the first of a sequence: b, from its h0
+  // a row: state -> a state + b; one that is not there changes nothing, and the
+  // first of a sequence (a marked, b from its h0) forgets what was before
   float a0[kBlock], a1[kBlock], b0[kBlock], b1[kBlock];
   Pair2 p;
   if (live) {
@@ -580,25 +581,23 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
       for (int i = 0; i < kBlock; ++i)
         if (r.has(i)) load(i);
 #pragma unroll
-      for (int i = 0; i < kBlock; ++i)
+      for (int i = 0; i < kBlock; ++i) {
+        a0[i] = a1[i] = 1.f;
+        b0[i] = b1[i] = 0.f;
         if (r.has(i)) {
           make(i);
           if (r.begins(i)) {
             const State2 v = of_sequence(h0, ws, r, i, C, c, both);
             b0[i] = fmaf(a0[i], v.v0, b0[i]);
             b1[i] = fmaf(a1[i], v.v1, b1[i]);
-            p.b0 = b0[i];
-            p.b1 = b1[i];
-          } else {
-            p.b0 = fmaf(a0[i], p.b0, b0[i]);
-            p.b1 = fmaf(a1[i], p.b1, b1[i]);
+            a0[i] = a1[i] = kBegins;
           }
-          p.a0 *= a0[i];
-          p.a1 *= a1[i];
         }
+        p.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
+      }
     }
-    p.a0 = factor(p.a0, r.marks & 0xFFFFu);
-    p.a1 = factor(p.a1, r.marks & 0xFFFFu);
+    p.a0 = factor(p.a0);
+    p.a1 = factor(p.a1);
   }
   lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
   State2 v = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);
@@ -616,7 +615,7 @@ __global__ __launch_bounds__(64 * W, 4) void tile_kernel(TileSpace ws, int tiles
 #pragma unroll
     for (int i = 0; i < kBlock; ++i)
       if (r.has(i)) {
-        v = r.begins(i) ? State2{b0[i], b1[i]} : State2{fmaf(a0[i], v.v0, b0[i]), fmaf(a1[i], v.v1, b1[i])};
+        v.behind(make_float4(a0[i], b0[i], a1[i], b1[i]));
         store2(out + size_t(i) * C, v.v0, v.v1, both, true);
         if (last && r.ends(i)) store2(last + size_t(ws.owner[r.t0 + i]) * C + c, v.v0, v.v1, both);
       }
@@ -708,6 +707,7 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
           if (r.ends(i)) {
             const State2 e = of_sequence(dlast, ws, r, i, C, c, both);
             ends[wave][i][lane] = make_float2(e.v0, e.v1);
+            p.a0 = p.a1 = kBegins;
             p.b0 = e.v0;
             p.b1 = e.v1;
           }
@@ -717,8 +717,8 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
           p.a1 *= gate1(i);
         }
     }
-    p.a0 = factor(p.a0, r.marks >> 16);
-    p.a1 = factor(p.a1, r.marks >> 16);
+    p.a0 = factor(p.a0);
+    p.a1 = factor(p.a1);
   }
   lds.pairs[wave][lane] = make_float4(p.a0, p.b0, p.a1, p.b1);
   State2 e = state_before<W>(lds, ws, k, tiles, C, c, live, both, wave, lane);
@@ -766,7 +766,7 @@ __global__ __launch_bounds__(64 * W) void tile_backward_kernel(
 }
 
 // Waves of a tile: eight, or (backwards, where a wave holds three rows' worth
-// of registers) four, so that two workgroups share a compute unit.
+// of registers) four, so that two workgroups share a compute unit, of bf16 three.
 constexpr int kWaves = 8, kWavesBackward = 4;
 
 // Whether the rows are split into tiles.  In training, us: a wave takes 4 + 0.5
