@@ -705,8 +705,9 @@ size_t dspark_hidden_draft_workspace_bytes(int B, int gamma, int V, int r, int d
  * dspark_norm — normalisation of rows, with the residual stream's sum in the
  * same pass: what stands before each projection of a backbone's layer.
  *
- * Defined by: [P-blog] §4 parallel stage (the backbone whose hidden states
- * the heads read); the formula, for every row:
+ * Defined by: the formula below, the usual one of backbones; [P-blog] §4 names
+ * the backbone, whose hidden states the heads read, and gives none.  For every
+ * row:
  *   s    = x + residual                     (rounded to the storage type; s = x without one)
  *   mu   = mean_c s          (LAYER; RMS: 0)
  *   rstd = 1 / sqrt(mean_c (s - mu)^2 + eps)
@@ -765,9 +766,10 @@ size_t dspark_norm_backward_workspace_bytes(int M, int C, dspark_dtype dtype);
  * RNN head's state over whole sequences (DECAY), and the recurrent layer of a
  * backbone (SIGMOID); with sequences of one row it is the step of a decoder.
  *
- * Defined by: [P-blog] §4 (RNN head: its state carries information from every
- * earlier position; dspark_rnn_draft's reading is a per-channel decayed
- * state); the formula, for the rows t of every sequence in order:
+ * Defined by: the formulas below.  DECAY is the reading that dspark_rnn_draft
+ * has of [P-blog] §4 (RNN head: its state carries information from every earlier
+ * position); SIGMOID, the usual gated form for recurrent layers, stands in no
+ * page.  For the rows t of every sequence in order:
  *   SIGMOID  a_t = 1 / (1 + exp(-gate[t])),  b_t = (1 - a_t) x[t]
  *   DECAY    a_t = gate (per channel),       b_t = x[t]
  *   h[t] = a_t h[t-1] + b_t        (the sequence's h0, or 0, before its first row)
@@ -847,8 +849,8 @@ size_t dspark_recurrence_backward_workspace_bytes(int T, int S, int C, dspark_dt
  * dspark_gated_linear — the gated feed-forward projection of a backbone's
  * layer: both products, the activation and their product in one kernel.
  *
- * Defined by: [P-blog] §4 parallel stage (the backbone whose hidden states the
- * heads read); the formula:
+ * Defined by: the formula below, the usual one of backbones; [P-blog] §4 names
+ * the backbone, whose hidden states the heads read, and gives none:
  *   zg = x wg^T + bg,  zu = x wu^T + bu     (fp32 accumulate)
  *   y  = act(zg) zu                         (fp32, rounded once to the storage type)
  *

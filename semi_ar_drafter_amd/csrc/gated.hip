@@ -11,14 +11,18 @@
 //   dx         C(a = input, b = row) = sum_n wg[n][a] dzg[b][n] + wu[n][a] dzu[b][n]:
 //              one contraction of two parts
 //   dwg, dwu   C(a = input, b = column of dz) = sum_m x[m][a] dz[m][b]: one product
-// dz is rounded to the storage type, which the products take (see linear.hip);
-// the pre-activations that the gradient reads are fp32: rounded to bf16 they
-// would add half a bf16 step of zu to every dzg.
+// dz is rounded to the storage type, which the products take (see linear.hip):
+// bf16 gradients are off by 2.35e-3 of their norm, where their own rounding alone
+// is 1.66e-3; keeping the rounded-off part as a second operand would double both
+// products (1.4 ms more of 2.3 at 4096 x 10240 x 5120).  The pre-activations that
+// the gradient reads are fp32: rounded to bf16 they would add half a bf16 step of
+// zu to every dzg.
 //
 // Bound by reading the weights with few rows (16384 x 4096, one row: 45.8 us, 5.9
-// TB/s), by the main loop of the matrix unit's tiles with many (2048 rows: 431 us,
-// 1.28 PFLOP/s; 4096 x 10240 x 5120 in training: 719 us forward with its 420 MB of
-// pre-activations and outputs, gradients 694 and 802 us, dz 107).
+// TB/s), by the main loop of the matrix unit's tiles with many (2048 rows: 428 to
+// 476 us from card to card, 1.15 to 1.28 PFLOP/s; 4096 x 10240 x 5120 in training
+// 2.29 to 2.33 ms, under the profiler: 709 us forward with its 420 MB of
+// pre-activations and outputs, gradients 683 and 760 us, dz 112).
 #include "launch.h"
 #include "product.h"
 
@@ -129,18 +133,6 @@ __global__ __launch_bounds__(256) void join_gated_kernel(int M, int splits, cons
   epi.finish(g, u, b, a, epi.na - a);
 }
 
-// A few rows (M <= 16): both weights are read once, straight into the matrix
-// instruction's operand registers; each of eight waves takes a share of the
-// contraction, and LDS joins them (16384 x 4096, one row: 46.5 us, 5.8 TB/s, with
-// four waves 57).  16 features per workgroup.  Any K: rows need element alignment
-// only, and what is left of the contraction is masked.
-//
-// A load takes 128 bytes of each of 8 features, whole lines (with 64 bytes of
-// 16 features, as the instruction's operand wants them, 10240 x 5120 takes 55 us
-// for one row instead of 43): its operand rows l < 8 hold feature l and the
-// first 32 of 64 of the contraction, l >= 8 feature l - 8 and the other 32.  Two
-// instructions multiply it by both halves of x; of each result the half that
-// belongs together is used.
 // 16 bytes of a row.  ODD: rows of an odd number of values, of which every
 // second begins between two words: loads that do so take twice as long, so the
 // words are loaded and shifted (one row, 4480 x 3999: 47 us before, 34 so).  A value behind the
@@ -163,6 +155,18 @@ __device__ __forceinline__ u32x4_t load_row(const bf16_t* p) {
   return v;
 }
 
+// A few rows (M <= 16): both weights are read once, straight into the matrix
+// instruction's operand registers; each of eight waves takes a share of the
+// contraction, and LDS joins them (16384 x 4096, one row: 45.8 us, 5.9 TB/s, with
+// four waves 57).  16 features per workgroup.  Any K: rows need element alignment
+// only, and what is left of the contraction is masked.
+//
+// A load takes 128 bytes of each of 8 features, whole lines (with 64 bytes of
+// 16 features, as the instruction's operand wants them, 10240 x 5120 takes 55 us
+// for one row instead of 43): its operand rows l < 8 hold feature l and the
+// first 32 of 64 of the contraction, l >= 8 feature l - 8 and the other 32.  Two
+// instructions multiply it by both halves of x; of each result the half that
+// belongs together is used.
 template <bool ODD>
 __global__ __launch_bounds__(512) void few_rows_gated_kernel(int M, int N, int K, const bf16_t* __restrict__ x,
                                                             const bf16_t* __restrict__ wg,
@@ -414,7 +418,7 @@ GatedEpi<T> gated_epi(const GatedArgs& a) {
 
 // Where the rows are few enough for few_rows_gated_kernel (weights from memory,
 // us, against the tiles: one row of 8192 x 2560 17.3 and 20.3, of 16384 x 4096
-// 46.5 and 60.7; sixteen 20.6 and 21.7, 50.9 and 60.3), whose rows of x come in
+// 45.8 and 60.7; sixteen 20.6 and 21.7, 50.9 and 60.3), whose rows of x come in
 // 64-byte pieces: a long contraction of more than four is the tiles' (10240 x
 // 5120, four rows 43.9 and 42.5, sixteen 50.8 and 44.2), unless they had to copy
 // unaligned weights first.

@@ -6,9 +6,10 @@
 //   ds = rstd (q - mean q - n mean(q n)) + dsum           (rms: without mean q)
 //   dw = sum over rows of dy n,  db = sum over rows of dy
 //
-// Bound by memory (16384 x 5120 with a residual: 142 us forward for 671 MB, 4.7
-// TB/s, and 150 backward; one row: 3.8 us, latency).  A row is read once and kept in registers as it is stored,
-// 16 bytes a lane and load; its mean and the sum of squares around it are made
+// Bound by memory (16384 x 5120 with a residual, in training: 271 us for 1.34 GB
+// and 21 MB of shares, 5.0 TB/s; under the profiler 140 forward, 160 and 7
+// backward; one row: 3.6 us, latency).  A row is read once and kept in registers
+// as it is stored, 16 bytes a lane and load; its mean and the sum of squares around it are made
 // wave by wave and joined in LDS (n_a, m_a, M_a with n_b, m_b, M_b: the squares
 // around the joint mean are M_a + M_b + (m_a - m_b)^2 n_a n_b / (n_a + n_b)),
 // so that no precision is lost to a mean that is large against the spread.

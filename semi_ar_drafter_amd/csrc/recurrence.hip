@@ -13,8 +13,8 @@
 // by block of 16 rows, from the fp32 states that the forward pass kept.
 //
 // Bound by memory, and with long sequences by the words that tiles pass on:
-// 65536 rows of 2560 take 275 us forward for 1.0 GB, 441 backward for 1.7 GB, in
-// training 724 together with their setup (the same loads and stores without the
+// 65536 rows of 2560 take 268 us forward for 1.0 GB, 438 backward for 1.7 GB, in
+// training 717 together with their setup (the same loads and stores without the
 // words: 212 and 358, with cheaper gates); a step of 256 sequences 3.9 us.
 #include "launch.h"
 #include "projection.h"
